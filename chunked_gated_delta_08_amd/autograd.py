@@ -1,4 +1,6 @@
-"""torch.autograd wrapper around the library's chunked forward and backward.
+"""torch.autograd wrappers around the library's chunked forward and backward, and
+around the operators that stand beside it in a layer (gated RMSNorm, residual add
+with RMSNorm, gated linear recurrence).
 
 FlashQLA backward explainer §一: the chunked gated delta rule is exposed to
 training code as one autograd function; its forward saves the gate as the
@@ -45,3 +47,80 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, cu_
     Differentiable in q, k, v, g, beta and initial_state.  cu_seqlens: int32 CUDA
     tensor [N+1] (varlen; then the batch is 1) or None.  The final state is fp32."""
     return ChunkGatedDeltaRule.apply(q, k, v, g, beta, initial_state, scale, cu_seqlens, B, BT, seg_chunks)
+
+
+class GatedRMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, z, w, eps, act):
+        x, w = x.contiguous(), w.contiguous()
+        z = None if z is None else z.contiguous()
+        ctx.save_for_backward(x, z, w)
+        ctx.cfg = (eps, act)
+        return binding.gated_norm_fwd(x, z, w, eps=eps, act=act)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, z, w = ctx.saved_tensors
+        r = binding.gated_norm_bwd(x, z, w, dy.contiguous(), eps=ctx.cfg[0], act=ctx.cfg[1])
+        return r["dx"], r["dz"], r["dw"], None, None
+
+
+def gated_rms_norm(x, z, weight, eps=1e-5, act="silu"):
+    """RMSNorm of x [..., D] times weight [D] (fp32) times the gate act(z); z None: no gate.
+
+    Differentiable in x, z and weight.  act is "silu" or "sigmoid"."""
+    return GatedRMSNorm.apply(x, z, weight, eps, act)
+
+
+class AddRMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, res, w, scale, eps):
+        x, res, w = x.contiguous(), res.contiguous(), w.contiguous()
+        scale = None if scale is None else scale.contiguous()
+        out = binding.add_norm_fwd(x, res, w, scale=scale, eps=eps)
+        ctx.save_for_backward(None if scale is None else x, out["res"], w, scale)
+        ctx.eps = eps
+        return out["y"], out["res"]
+
+    @staticmethod
+    def backward(ctx, dy, dres):
+        x, res, w, scale = ctx.saved_tensors
+        r = binding.add_norm_bwd(dy.contiguous(), dres.contiguous(), res, w, x=x, scale=scale, eps=ctx.eps)
+        return r["dx"], r["dres"], r["dw"], r["dscale"], None
+
+
+def add_rms_norm(x, res, weight, scale=None, eps=1e-5):
+    """y, res' = the residual stream res' = res + scale x and y = RMSNorm(res') weight.
+
+    Differentiable in x, res, weight and scale ([D] fp32, None: 1).  res is in x's
+    type or fp32; the gradients are taken at the stored res'."""
+    return AddRMSNorm.apply(x, res, weight, scale, eps)
+
+
+class GatedLinearRecurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, h0, cu_seqlens, cu_seqlens_host, B):
+        x, g = x.contiguous(), g.contiguous()
+        h0 = None if h0 is None else h0.contiguous()
+        out = binding.glr_fwd(x, g, h0=h0, cu_seqlens=cu_seqlens, cu_seqlens_host=cu_seqlens_host, B=B,
+                              want_states=True)
+        ctx.save_for_backward(x, g, h0, out["states"], cu_seqlens, cu_seqlens_host)
+        ctx.B = B
+        return out["h"], out["ht"]
+
+    @staticmethod
+    def backward(ctx, dh, dht):
+        x, g, h0, states, cu_seqlens, cu_seqlens_host = ctx.saved_tensors
+        r = binding.glr_bwd(x, g, dh.contiguous(), states, dht=dht.contiguous(), h0=h0, cu_seqlens=cu_seqlens,
+                            cu_seqlens_host=cu_seqlens_host, B=ctx.B,
+                            want_dh0=h0 is not None and ctx.needs_input_grad[2])
+        return r["dx"], r["dg"], r["dh0"], None, None, None
+
+
+def gated_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, cu_seqlens_host=None, B=1):
+    """h, final_state of h_t = exp(g_t) h_{t-1} + x_t over x [B*T, D], the log-gate g [B*T, D] fp32.
+
+    Differentiable in x, g and initial_state ([N, D] fp32).  cu_seqlens as for
+    chunk_gated_delta_rule; cu_seqlens_host, its CPU copy, avoids a copy in each pass.
+    The final state is fp32."""
+    return GatedLinearRecurrence.apply(x, g, initial_state, cu_seqlens, cu_seqlens_host, B)

@@ -487,3 +487,387 @@ def bigdn_bwd(qkv, beta, decay, qw, kw, cos, sin, dout, F, S, k_scale=1.0, norm_
     else:
         _check(lib.bigdn_bwd_events(*args, events))
     return out
+
+
+# --------------------------------------------------------------------------
+# Layer operators (include/gdn_layer.h): gated RMSNorm, residual add with
+# RMSNorm, gated linear recurrence, single-token steps.  Every tensor of a call
+# is on one device, which need not be the current one; `stream` (default: that
+# device's current stream) belongs to it.  Preallocated outputs are checked like
+# inputs; which of them may be an input's own buffer is said in the header.
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+                ("res_dtype", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+class GlrProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("N", ctypes.c_int),
+                ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p), ("dtype", ctypes.c_int)]
+
+
+GLR_TILE = 16
+ACTS = {"silu": 0, "sigmoid": 1}
+EXPORTED_LAYER = ["norm_workspace_size", "gated_norm_fwd", "gated_norm_bwd", "add_norm_fwd", "add_norm_bwd",
+                  "glr_num_states", "glr_workspace_size", "glr_fwd", "glr_bwd", "glr_step", "gdr_step"]
+_i, _i64, _f = ctypes.c_int, ctypes.c_int64, ctypes.c_float
+_np, _gp = ctypes.POINTER(NormProblem), ctypes.POINTER(GlrProblem)
+lib.norm_workspace_size.restype = _sz
+lib.norm_workspace_size.argtypes = [_np]
+lib.gated_norm_fwd.argtypes = [_np] + [_vp] * 5
+lib.gated_norm_bwd.argtypes = [_np] + [_vp] * 8 + [_sz, _vp]
+lib.add_norm_fwd.argtypes = [_np] + [_vp] * 7
+lib.add_norm_bwd.argtypes = [_np] + [_vp] * 11 + [_sz, _vp]
+lib.glr_num_states.restype = _i64
+lib.glr_num_states.argtypes = [_gp]
+lib.glr_workspace_size.restype = _sz
+lib.glr_workspace_size.argtypes = [_gp]
+lib.glr_fwd.argtypes = [_gp] + [_vp] * 7 + [_sz, _vp]
+lib.glr_bwd.argtypes = [_gp] + [_vp] * 10 + [_sz, _vp]
+lib.glr_step.argtypes = [_i, _i, _i64, _i] + [_vp] * 6
+lib.gdr_step.argtypes = [_i] * 5 + [_i64, _f, _i] + [_vp] * 9
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
+
+
+def _launch(dev, stream, temps, call):
+    """call(stream handle) with `dev` current.  `temps`: tensors allocated for this
+    call on the current stream; the allocator is told when another one uses them."""
+    current = torch.cuda.current_stream(dev)
+    if stream is None:
+        stream = current
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    elif stream != current:
+        for t in temps:
+            if t is not None:
+                t.record_stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        _check(call(stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(stream.cuda_stream))
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def check_gated_norm_args(x, z, w, dy=None, act="silu", need_dy=False, cuda=True):
+    """x, z (None: no gate), dy [..., D] of one dtype; w [D] fp32."""
+    _need(x, "x", cuda=cuda)
+    if x.dtype not in _DT:
+        raise TypeError(f"x has dtype {x.dtype}; expected one of {_FLOATS}")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    if act not in ACTS:
+        raise ValueError(f"act is {act!r}; expected one of {sorted(ACTS)}")
+    _need(z, "z", x.dtype, x.shape, cuda=cuda, optional=True)
+    _need(w, "w", torch.float32, x.shape[-1:], cuda=cuda)
+    if need_dy:
+        _need(dy, "dy", x.dtype, x.shape, cuda=cuda)
+    _same_device(x, z, w, dy)
+
+
+def _norm_problem(x, eps, res_dtype=None, act="silu"):
+    D = x.shape[-1]
+    return NormProblem(x.numel() // D if D else 0, D, eps, _DT[x.dtype], _DT[res_dtype or x.dtype], ACTS[act])
+
+
+def norm_workspace_size(rows, D, dtype):
+    """Bytes of workspace gated_norm_bwd and add_norm_bwd need."""
+    return int(lib.norm_workspace_size(ctypes.byref(NormProblem(rows, D, 0.0, _DT[dtype], _DT[dtype], 0))))
+
+
+def _norm_workspace(p, workspace, dev):
+    if workspace is None:
+        return torch.empty(int(lib.norm_workspace_size(ctypes.byref(p))), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8)
+    return workspace
+
+
+def gated_norm_fwd(x, z, w, eps=1e-5, act="silu", out=None, stream=None):
+    """y = x rsqrt(mean(x^2) + eps) w act(z) over the last axis; z None: no gate."""
+    check_gated_norm_args(x, z, w, act=act)
+    y = torch.empty_like(x) if out is None else out
+    _need(y, "out", x.dtype, x.shape)
+    _same_device(x, y)
+    p = _norm_problem(x, eps, act=act)
+    _launch(x.device, stream, (y,) if out is None else (),
+            lambda s: lib.gated_norm_fwd(ctypes.byref(p), _p(x), _p(z), _p(w), _p(y), s))
+    return y
+
+
+def gated_norm_bwd(x, z, w, dy, eps=1e-5, act="silu", out=None, workspace=None, stream=None):
+    """Gradients of gated_norm_fwd.  Returns dict dx, dz (None without z), dw (fp32)."""
+    check_gated_norm_args(x, z, w, dy, act=act, need_dy=True)
+    own = []
+    if out is None:
+        out = {"dx": torch.empty_like(x), "dz": None if z is None else torch.empty_like(z), "dw": torch.empty_like(w)}
+        own += list(out.values())
+    _need(out["dx"], "dx", x.dtype, x.shape)
+    _need(out["dw"], "dw", torch.float32, w.shape)
+    if z is not None:
+        _need(out["dz"], "dz", x.dtype, x.shape)
+    dz = None if z is None else out["dz"]
+    p = _norm_problem(x, eps, act=act)
+    ws = _norm_workspace(p, workspace, x.device)
+    own += [ws] if workspace is None else []
+    _same_device(x, out["dx"], dz, out["dw"], ws)
+    _launch(x.device, stream, own,
+            lambda s: lib.gated_norm_bwd(ctypes.byref(p), _p(x), _p(z), _p(w), _p(dy), _p(out["dx"]), _p(dz),
+                                         _p(out["dw"]), _p(ws), ws.numel(), s))
+    return out
+
+
+def check_add_norm_args(x, res, w, scale=None, cuda=True):
+    """x [..., D]; res of x's shape, in x's dtype or fp32; w, scale (None: 1) [D] fp32."""
+    _need(x, "x", cuda=cuda)
+    if x.dtype not in _DT:
+        raise TypeError(f"x has dtype {x.dtype}; expected one of {_FLOATS}")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    _need(res, "res", shape=x.shape, cuda=cuda)
+    if res.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"res has dtype {res.dtype}, expected {x.dtype} or torch.float32")
+    _need(w, "w", torch.float32, x.shape[-1:], cuda=cuda)
+    _need(scale, "scale", torch.float32, x.shape[-1:], cuda=cuda, optional=True)
+    _same_device(x, res, w, scale)
+
+
+def add_norm_fwd(x, res, w, scale=None, eps=1e-5, out=None, stream=None):
+    """res' = res + scale x and y = RMSNorm(res') w.  Returns dict y (x's dtype), res
+    (res's dtype).  out={"y": ..., "res": res} updates the residual stream in place."""
+    check_add_norm_args(x, res, w, scale)
+    own = out is None
+    if own:
+        out = {"y": torch.empty_like(x), "res": torch.empty_like(res)}
+    _need(out["y"], "y", x.dtype, x.shape)
+    _need(out["res"], "res", res.dtype, x.shape)
+    _same_device(x, out["y"], out["res"])
+    p = _norm_problem(x, eps, res.dtype)
+    _launch(x.device, stream, out.values() if own else (),
+            lambda s: lib.add_norm_fwd(ctypes.byref(p), _p(x), _p(res), _p(w), _p(scale), _p(out["y"]),
+                                       _p(out["res"]), s))
+    return out
+
+
+def check_add_norm_bwd_args(dy, dres, res, w, x=None, scale=None, cuda=True):
+    """As check_add_norm_args, dy in x's place; dres (None: zero) like res; x and scale both or neither."""
+    check_add_norm_args(dy, res, w, scale, cuda=cuda)
+    _need(dres, "dres", res.dtype, res.shape, cuda=cuda, optional=True)
+    if (x is None) != (scale is None):
+        raise ValueError("x and scale come together: the scale's gradient reads x")
+    _need(x, "x", dy.dtype, dy.shape, cuda=cuda, optional=True)
+    _same_device(dy, dres, x)
+
+
+def add_norm_bwd(dy, dres, res, w, x=None, scale=None, eps=1e-5, out=None, workspace=None, stream=None):
+    """Gradients of add_norm_fwd: dy of y, dres (None: zero) of res', at res = the
+    forward's res'.  Returns dict dx (dy's dtype), dres, dw, dscale (None without
+    scale).  Without scale and in one dtype, dx is dres, the same tensor."""
+    check_add_norm_bwd_args(dy, dres, res, w, x, scale)
+    own = []
+    one = scale is None and dy.dtype == res.dtype
+    if out is None:
+        d = torch.empty_like(res)
+        out = {"dx": d if one else torch.empty_like(dy), "dres": d, "dw": torch.empty_like(w),
+               "dscale": None if scale is None else torch.empty_like(scale)}
+        own += list(out.values())
+    _need(out["dres"], "dres", res.dtype, res.shape)
+    _need(out["dx"], "dx", dy.dtype, dy.shape)
+    _need(out["dw"], "dw", torch.float32, w.shape)
+    if scale is not None:
+        _need(out["dscale"], "dscale", torch.float32, w.shape)
+    dx = None if out["dx"] is out["dres"] else out["dx"]
+    ds = None if scale is None else out["dscale"]
+    p = _norm_problem(dy, eps, res.dtype)
+    ws = _norm_workspace(p, workspace, dy.device)
+    own += [ws] if workspace is None else []
+    _same_device(dy, out["dres"], out["dx"], out["dw"], ds, ws)
+    _launch(dy.device, stream, own,
+            lambda s: lib.add_norm_bwd(ctypes.byref(p), _p(dy), _p(dres), _p(res), _p(w), _p(x), _p(scale), _p(dx),
+                                       _p(out["dres"]), _p(out["dw"]), _p(ds), _p(ws), ws.numel(), s))
+    return out
+
+
+def check_glr_args(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, dh=None, dht=None, states=None,
+                   bwd=False, cuda=True):
+    """x, dh [B*T, D] of one dtype; g [B*T, D] fp32; h0, dht [N, D] fp32; states
+    [ceil(B*T / GLR_TILE), D] fp32; cu_seqlens int32 [N+1], cu_seqlens_host the same on the CPU.  Returns N."""
+    _need(x, "x", cuda=cuda)
+    if x.dtype not in _DT:
+        raise TypeError(f"x has dtype {x.dtype}; expected one of {_FLOATS}")
+    if x.dim() != 2:
+        raise ValueError("x must be [B*T, D]")
+    ntok, D = x.shape
+    _need(g, "g", torch.float32, x.shape, cuda=cuda)
+    if B < 1 or (cu_seqlens is None and ntok % B != 0):
+        raise ValueError(f"the token count {ntok} is not a multiple of B = {B}")
+    if cu_seqlens is not None and B != 1:
+        raise ValueError("B must be 1 with cu_seqlens")
+    N = _nseq(cu_seqlens, B, cuda)
+    if cu_seqlens_host is not None:
+        if cu_seqlens is None:
+            raise ValueError("cu_seqlens_host without cu_seqlens")
+        _need(cu_seqlens_host, "cu_seqlens_host", torch.int32, cu_seqlens.shape, cuda=False)
+        if cu_seqlens_host.is_cuda:
+            raise ValueError("cu_seqlens_host must be a CPU tensor")
+    _need(h0, "h0", torch.float32, (N, D), cuda=cuda, optional=True)
+    if bwd:
+        _need(dh, "dh", x.dtype, x.shape, cuda=cuda)
+        _need(dht, "dht", torch.float32, (N, D), cuda=cuda, optional=True)
+        _need(states, "states", torch.float32, (-(-ntok // GLR_TILE), D), cuda=cuda)
+    _same_device(x, g, h0, cu_seqlens, dh, dht, states)
+    return N
+
+
+def _glr_problem(x, cu_seqlens, cu_seqlens_host, B):
+    """The problem struct and what has to outlive its use.  Without a host mirror
+    cu_seqlens is copied to the host, which waits for the current stream."""
+    ntok, D = x.shape
+    if cu_seqlens is None:
+        return GlrProblem(B, ntok // B, D, 0, None, None, _DT[x.dtype]), None
+    host = cu_seqlens.detach().cpu() if cu_seqlens_host is None else cu_seqlens_host
+    return GlrProblem(1, ntok, D, host.numel() - 1, cu_seqlens.data_ptr(), host.data_ptr(), _DT[x.dtype]), host
+
+
+def glr_num_states(ntok):
+    """Rows of glr_fwd's `states` for ntok = B*T tokens."""
+    return -(-ntok // GLR_TILE)
+
+
+def _glr_workspace(p, workspace, dev):
+    if workspace is None:
+        n = int(lib.glr_workspace_size(ctypes.byref(p)))
+        return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _need(workspace, "workspace", torch.uint8)
+    return workspace
+
+
+def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=True, want_states=False, out=None,
+            workspace=None, stream=None):
+    """Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t over [B*T, D].  Returns dict
+    h (x's dtype), ht [N, D] fp32, states (for glr_bwd, when wanted).  Give
+    cu_seqlens_host (the CPU copy of cu_seqlens) to avoid a copy and its wait."""
+    N = check_glr_args(x, g, h0, cu_seqlens, cu_seqlens_host, B)
+    ntok, D = x.shape
+    dev = x.device
+    own = []
+    if out is None:
+        out = {"h": torch.empty_like(x),
+               "ht": torch.empty((N, D), dtype=torch.float32, device=dev) if want_ht else None,
+               "states": torch.empty((glr_num_states(ntok), D), dtype=torch.float32, device=dev) if want_states
+               else None}
+        own += list(out.values())
+    _need(out["h"], "h", x.dtype, x.shape)
+    _need(out["ht"], "ht", torch.float32, (N, D), optional=True)
+    _need(out["states"], "states", torch.float32, (glr_num_states(ntok), D), optional=True)
+    p, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B)
+    ws = _glr_workspace(p, workspace, dev)
+    own += [ws] if workspace is None else []
+    _same_device(x, *out.values(), ws)
+    _launch(dev, stream, own,
+            lambda s: lib.glr_fwd(ctypes.byref(p), _p(x), _p(g), _p(h0), _p(out["h"]), _p(out["ht"]),
+                                  _p(out["states"]), _p(ws), 0 if ws is None else ws.numel(), s))
+    del keep
+    return out
+
+
+def glr_bwd(x, g, dh, states, dht=None, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_dh0=True, out=None,
+            workspace=None, stream=None):
+    """Gradients of glr_fwd for dh of h and dht of ht; states from glr_fwd(want_states=True).
+    Returns dict dx (x's dtype), dg fp32, dh0 [N, D] fp32."""
+    N = check_glr_args(x, g, h0, cu_seqlens, cu_seqlens_host, B, dh, dht, states, bwd=True)
+    D, dev = x.shape[1], x.device
+    own = []
+    if out is None:
+        out = {"dx": torch.empty_like(x), "dg": torch.empty_like(g),
+               "dh0": torch.empty((N, D), dtype=torch.float32, device=dev) if want_dh0 else None}
+        own += list(out.values())
+    _need(out["dx"], "dx", x.dtype, x.shape)
+    _need(out["dg"], "dg", torch.float32, x.shape)
+    _need(out["dh0"], "dh0", torch.float32, (N, D), optional=True)
+    p, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B)
+    ws = _glr_workspace(p, workspace, dev)
+    own += [ws] if workspace is None else []
+    _same_device(x, *out.values(), ws)
+    _launch(dev, stream, own,
+            lambda s: lib.glr_bwd(ctypes.byref(p), _p(x), _p(g), _p(h0), _p(states), _p(dh), _p(dht), _p(out["dx"]),
+                                  _p(out["dg"]), _p(out["dh0"]), _p(ws), 0 if ws is None else ws.numel(), s))
+    del keep
+    return out
+
+
+def _check_pool(state, slots, n, shape, cuda):
+    _need(state, "state", torch.float32, cuda=cuda)
+    if state.dim() != 1 + len(shape) or tuple(state.shape[1:]) != tuple(shape):
+        raise ValueError(f"state has shape {tuple(state.shape)}, expected [slots, {', '.join(map(str, shape))}]")
+    _need(slots, "slots", torch.int32, (n,), cuda=cuda, optional=True)
+    if slots is None and n > state.shape[0]:
+        raise ValueError(f"{n} rows and {state.shape[0]} states: give slots, or a state for each row")
+
+
+def check_glr_step_args(x, g, state, slots=None, cuda=True):
+    """x [N, D]; g [N, D] fp32; state [slots, D] fp32; slots [N] int32 or None."""
+    _need(x, "x", cuda=cuda)
+    if x.dtype not in _DT:
+        raise TypeError(f"x has dtype {x.dtype}; expected one of {_FLOATS}")
+    if x.dim() != 2:
+        raise ValueError("x must be [N, D]")
+    _need(g, "g", torch.float32, x.shape, cuda=cuda)
+    _check_pool(state, slots, x.shape[0], x.shape[1:], cuda)
+    _same_device(x, g, state, slots)
+
+
+def glr_step(x, g, state, slots=None, out=None, stream=None):
+    """One token of glr_fwd's recurrence per row, on the states state[slots[n]], updated
+    in place.  A row whose slot is outside the pool is padding (its h is zero); rows of
+    one slot are successive tokens.  Returns h [N, D] (x's dtype)."""
+    check_glr_step_args(x, g, state, slots)
+    h = torch.empty_like(x) if out is None else out
+    _need(h, "out", x.dtype, x.shape)
+    _same_device(x, h)
+    _launch(x.device, stream, (h,) if out is None else (),
+            lambda s: lib.glr_step(x.shape[0], x.shape[1], state.shape[0], _DT[x.dtype], _p(x), _p(g), _p(slots),
+                                   _p(state), _p(h), s))
+    return h
+
+
+def check_gdr_step_args(q, k, v, g, beta, state, slots=None, cuda=True):
+    """q, k [N, HK, K]; v [N, HV, V]; beta [N, HV] (one dtype); g [N, HV] fp32; state
+    [slots, HV, K, V] fp32; slots [N] int32 or None."""
+    _need(v, "v", cuda=cuda)
+    _need(k, "k", v.dtype, cuda=cuda)
+    if v.dtype not in _DT:
+        raise TypeError(f"v has dtype {v.dtype}; expected one of {_FLOATS}")
+    if k.dim() != 3 or v.dim() != 3 or k.shape[0] != v.shape[0]:
+        raise ValueError("k must be [N, HK, K] and v [N, HV, V]")
+    N, HV, V = v.shape
+    HK, K = k.shape[1:]
+    if HK < 1 or HV < 1 or HV % HK != 0:
+        raise ValueError(f"HV ({HV}) must be a multiple of HK ({HK})")
+    _need(q, "q", v.dtype, k.shape, cuda=cuda)
+    _need(beta, "beta", v.dtype, (N, HV), cuda=cuda)
+    _need(g, "g", torch.float32, (N, HV), cuda=cuda)
+    _check_pool(state, slots, N, (HV, K, V), cuda)
+    _same_device(v, q, k, g, beta, state, slots)
+
+
+def gdr_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, stream=None):
+    """One token of the gated delta rule per row, on the states state[slots[n]] (fp32
+    [slots, HV, K, V], as gdr_chunk_fwd's ht), updated in place; g is the token's raw
+    log-gate.  Slots as for glr_step.  Returns o [N, HV, V] (v's dtype)."""
+    check_gdr_step_args(q, k, v, g, beta, state, slots)
+    o = torch.empty_like(v) if out is None else out
+    _need(o, "out", v.dtype, v.shape)
+    _same_device(v, o)
+    (N, HK, K), (_, HV, V) = k.shape, v.shape
+    _launch(v.device, stream, (o,) if out is None else (),
+            lambda s: lib.gdr_step(N, HK, HV, K, V, state.shape[0], scale or 0.0, _DT[v.dtype], _p(q), _p(k), _p(v),
+                                   _p(g), _p(beta), _p(slots), _p(state), _p(o), s))
+    return o

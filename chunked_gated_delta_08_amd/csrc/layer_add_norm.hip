@@ -1,0 +1,223 @@
+// layer_add_norm.hip -- the residual add with RMSNorm, forward and backward
+// (include/gdn_layer.h), and the join of both norms' weight gradients.
+//
+// Per row of D elements:
+//   h = res + s x,  r = (sum h^2 / D + eps)^(-1/2),  n = h r,  y = n w,  res' = h
+//   dn = dy w,  dh = dres + r (dn - n mean(dn n)),
+//   dx = s dh,  ds = sum_rows dh x,  dw = sum_rows dy n
+// y is formed from the unrounded h; the backward takes the stored res' for h.
+// Bound by HBM, built like the gated norm (layer_gated_norm.hip).
+#include "layer_rows.hpp"
+
+namespace layer {
+namespace {
+
+template <class E, class R, int VEC, int TPR, int NV>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void add_norm_fwd_kernel(NormArgs a) {
+    constexpr int NT = TPR > 256 ? TPR : 256, GR = NT / TPR;
+    __shared__ float lds[TPR > 64 ? 2 * NT / 64 : 1];
+    const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, D = a.D;
+    const float inv = 1.f / (float)D;
+    int phase = 0;
+    for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
+        const bool live = r0 + grp < a.rows;
+        const long off = (live ? r0 + grp : a.rows - 1) * D;
+        const E* x = (const E*)a.x + off;
+        const R* res = (const R*)a.res + off;
+        Raw<E, VEC> xr[NV];
+        Raw<R, VEC> rr[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++) load_raw<E, VEC>(xr[i], x, (i * TPR + lane) * VEC, D);
+#pragma unroll
+        for (int i = 0; i < NV; i++) load_raw<R, VEC>(rr[i], res, (i * TPR + lane) * VEC, D);
+        float h[NV][VEC], s[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            Raw<float, VEC> sc;
+            if (a.scale) load_raw<float, VEC>(sc, a.scale, (i * TPR + lane) * VEC, D);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                const float v = (float)xr[i].v[e];
+                h[i][e] = (float)rr[i].v[e] + (a.scale ? sc.v[e] * v : v);
+                s[0] += h[i][e] * h[i][e];
+            }
+        }
+        row_sum<TPR, 1, NT>(s, lds, phase);
+        const float r = rsqrtf(s[0] * inv + a.eps);
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * VEC;
+            Raw<float, VEC> w;
+            load_raw<float, VEC>(w, a.w, c, D);
+            store_vec<R, VEC>((R*)a.res_out + off, c, D, h[i]);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) h[i][e] *= r * w.v[e];
+            store_vec<E, VEC>((E*)a.y + off, c, D, h[i]);
+        }
+    }
+}
+
+template <class E, class R, int VEC, int TPR, int NV, bool SCALE>
+__global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
+    constexpr int GR = BT / TPR;
+    __shared__ float lds[BT * VEC];
+    __shared__ float red[TPR > 64 ? 2 * 2 * (BT / 64) : 1];
+    const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, D = a.D;
+    const float inv = 1.f / (float)D;
+    float dw[NV][VEC], ds[SCALE ? NV : 1][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            dw[i][e] = 0.f;
+            if (SCALE) ds[i][e] = 0.f;
+        }
+    int phase = 0;
+    for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
+        const bool live = r0 + grp < a.rows;
+        const long off = (live ? r0 + grp : a.rows - 1) * D;
+        Raw<E, VEC> gr[NV], xr[SCALE ? NV : 1];
+        Raw<R, VEC> hr[NV], rr[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * VEC;
+            load_raw<E, VEC>(gr[i], (const E*)a.dy + off, c, D);
+            load_raw<R, VEC>(hr[i], (const R*)a.res + off, c, D);
+            if (a.dres) load_raw<R, VEC>(rr[i], (const R*)a.dres + off, c, D);
+            if constexpr (SCALE) load_raw<E, VEC>(xr[i], (const E*)a.x + off, c, D);
+        }
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            Raw<float, VEC> w;
+            load_raw<float, VEC>(w, a.w, (i * TPR + lane) * VEC, D);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                const float h = (float)hr[i].v[e];
+                s[0] += h * h;
+                s[1] += (float)gr[i].v[e] * w.v[e] * h;
+            }
+        }
+        row_sum<TPR, 2, BT>(s, red, phase);
+        const float r = rsqrtf(s[0] * inv + a.eps), m = r * s[1] * inv;
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * VEC;
+            Raw<float, VEC> w, sc;
+            load_raw<float, VEC>(w, a.w, c, D);
+            if constexpr (SCALE) load_raw<float, VEC>(sc, a.scale, c, D);
+            float dh[VEC], dx[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                const float n = (float)hr[i].v[e] * r, g = (float)gr[i].v[e];
+                dh[e] = r * (g * w.v[e] - n * m) + (a.dres ? (float)rr[i].v[e] : 0.f);
+                dw[i][e] += g * n;
+                if constexpr (SCALE) {
+                    ds[i][e] += dh[e] * (float)xr[i].v[e];
+                    dx[e] = dh[e] * sc.v[e];
+                } else {
+                    dx[e] = dh[e];
+                }
+            }
+            store_vec<R, VEC>((R*)a.dres_out + off, c, D, dh);
+            if (a.dx) store_vec<E, VEC>((E*)a.dx + off, c, D, dx);
+        }
+    }
+    float* part = a.part + (long)blockIdx.x * D * (SCALE ? 2 : 1);
+    write_part<VEC, TPR, NV>(dw, part, D, lds);
+    if constexpr (SCALE) write_part<VEC, TPR, NV>(ds, part + D, D, lds);
+}
+
+// out[c] = sum over the partial rows in a fixed order: 16 columns per
+// workgroup, 64 row slices, joined pairwise.  Column c < D goes to dw, the
+// others to dscale.
+__global__ __launch_bounds__(1024) void norm_wsum_kernel(const float* part, int blocks, int n, int D, float* dw,
+                                                         float* dscale) {
+    __shared__ float lds[64][17];
+    const int c = blockIdx.x * 16 + (threadIdx.x & 15), sl = threadIdx.x >> 4;
+    float t = 0.f;
+    if (c < n)
+        for (int b = sl; b < blocks; b += 64) t += part[(long)b * n + c];
+    lds[sl][threadIdx.x & 15] = t;
+    __syncthreads();
+    for (int m = 32; m >= 1; m /= 2) {
+        if (sl < m) lds[sl][threadIdx.x & 15] += lds[sl + m][threadIdx.x & 15];
+        __syncthreads();
+    }
+    if (sl == 0 && c < n) {
+        if (c < D) dw[c] = lds[0][threadIdx.x & 15];
+        else dscale[c - D] = lds[0][threadIdx.x & 15];
+    }
+}
+
+
+__global__ void zero_kernel(float* a, float* b, int n) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    a[i] = 0.f;
+    if (b) b[i] = 0.f;
+}
+
+template <class E, class R> hipError_t add_fwd(const NormArgs& a, hipStream_t s) {
+    constexpr int VEC = sizeof(R) == 4 ? 4 : 8;
+    return split_rows<64, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+        constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, NT = TPR > 256 ? TPR : 256;
+        hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV>), dim3(grid_rows(a.rows, NT / TPR, 1 << 20)),
+                           dim3(NT), 0, s, a);
+        return hipGetLastError();
+    });
+}
+
+template <class E, class R> hipError_t add_bwd(const NormArgs& a0, hipStream_t s) {
+    constexpr int VEC = sizeof(R) == 4 ? 4 : 8;
+    NormArgs a = a0;
+    int blocks = 1;
+    const hipError_t e = split_rows<64, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+        constexpr int TPR = decltype(T)::value, NV = decltype(N)::value;
+        blocks = grid_rows(a.rows, BT / TPR, MAX_BWD_BLOCKS);
+        if (blocks == 1 && !a.scale) a.part = a.dw;
+        if (a.scale)
+            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, true>), dim3(blocks), dim3(BT), 0, s, a);
+        else
+            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, false>), dim3(blocks), dim3(BT), 0, s, a);
+        return hipGetLastError();
+    });
+    return e != hipSuccess ? e : norm_wsum(a, blocks, a.D * (a.scale ? 2 : 1), s);
+}
+
+}  // namespace
+
+size_t norm_part_floats(long rows, int D) {   // at least one row of partial sums per workgroup of BT / 512 rows or more
+    return (size_t)grid_rows(rows > 0 ? rows : 1, 1, MAX_BWD_BLOCKS) * D * 2;
+}
+
+hipError_t norm_wsum(const NormArgs& a, int blocks, int n, hipStream_t s) {
+    if (blocks == 1 && n == a.D) return hipSuccess;   // the only workgroup wrote dw itself
+    hipLaunchKernelGGL(norm_wsum_kernel, dim3((n + 15) / 16), dim3(1024), 0, s, a.part, blocks, n, a.D, a.dw,
+                       a.dscale);
+    return hipGetLastError();
+}
+hipError_t norm_zero_grads(const NormArgs& a, hipStream_t s) {   // no rows: the column sums are zero
+    hipLaunchKernelGGL(zero_kernel, dim3((a.D + 255) / 256), dim3(256), 0, s, a.dw, a.dscale, a.D);
+    return hipGetLastError();
+}
+
+#define BY_TYPES(F, a, s)                                                                      \
+    switch (a.dtype) {                                                                         \
+        case GDR_F32: return F<float, float>(a, s);                                            \
+        case GDR_F16: return a.res_dtype == GDR_F32 ? F<f16, float>(a, s) : F<f16, f16>(a, s); \
+        default: return a.res_dtype == GDR_F32 ? F<bf16, float>(a, s) : F<bf16, bf16>(a, s);   \
+    }
+
+hipError_t launch_add_norm_fwd(const NormArgs& a, hipStream_t s) {
+    if (a.rows == 0) return hipSuccess;
+    BY_TYPES(add_fwd, a, s)
+}
+hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t s) {
+    if (a.rows == 0) return norm_zero_grads(a, s);
+    BY_TYPES(add_bwd, a, s)
+}
+
+}  // namespace layer

@@ -1,0 +1,140 @@
+// layer_rows.hpp -- device and host pieces shared by the two norms
+// (layer_gated_norm.hip, layer_add_norm.hip).
+//
+// A row of D elements is held by TPR lanes (a part of a wave, a wave, or
+// several waves of one workgroup), NV vectors of VEC elements each: 16 bytes of
+// the widest type per load.  All arithmetic is fp32; outputs are rounded once.
+#pragma once
+#include <type_traits>
+
+#include "../../include/gdn_layer.h"
+#include "gdr_device.hpp"
+#include "layer_launch.hpp"
+
+namespace layer {
+using gdr::bf16;
+using gdr::f16;
+
+// N elements at any element-aligned address: the vector type's alignment is the
+// element's, so rows of odd length keep wide loads (unaligned global accesses
+// are native on gfx950).
+template <class E, int N> struct VecU { typedef E t __attribute__((ext_vector_type(N), aligned(sizeof(E)))); };
+
+template <class E, int VEC> struct Raw {
+    typename VecU<E, VEC>::t v;   // as loaded; widened to fp32 where it is used
+};
+
+// VEC elements of a row from column c; columns past D read as zero.
+template <class E, int VEC>
+__device__ __forceinline__ void load_raw(Raw<E, VEC>& r, const E* row, int c, int D) {
+    if (c + VEC <= D) {
+        r.v = *(const typename VecU<E, VEC>::t*)(row + c);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e++) r.v[e] = c + e < D ? row[c + e] : (E)0.f;
+    }
+}
+template <class E, int VEC>
+__device__ __forceinline__ void store_vec(E* row, int c, int D, const float (&x)[VEC]) {
+    if (c + VEC <= D) {
+        typename VecU<E, VEC>::t t;
+#pragma unroll
+        for (int e = 0; e < VEC; e++) t[e] = (E)x[e];
+        *(typename VecU<E, VEC>::t*)(row + c) = t;
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e++)
+            if (c + e < D) row[c + e] = (E)x[e];
+    }
+}
+
+// sigmoid in fp32: relative error below (|z| + 4) 2^-24 (the exponent's argument
+// is rounded once, exp2 and rcp are within one unit in the last place).
+__device__ __forceinline__ float sigmoid_f(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896f * z));
+}
+
+// Sum over the TPR lanes of a row; for TPR = 256 over the four waves of the
+// group through `lds` (one float per wave of the workgroup and value, used
+// alternately by `phase` so that one barrier per row is enough).
+template <int TPR, int NVAL, int THREADS>
+__device__ __forceinline__ void row_sum(float (&s)[NVAL], float* lds, int phase) {
+    constexpr int W = TPR < 64 ? TPR : 64;
+#pragma unroll
+    for (int m = 1; m < W; m *= 2)
+#pragma unroll
+        for (int j = 0; j < NVAL; j++) s[j] += __shfl_xor(s[j], m, 64);
+    if constexpr (TPR > 64) {
+        constexpr int NW = THREADS / 64;
+        float* buf = lds + phase * NW * NVAL;
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int j = 0; j < NVAL; j++) buf[w * NVAL + j] = s[j];
+        gdr::lds_barrier();
+        const int w0 = w & ~(TPR / 64 - 1);
+#pragma unroll
+        for (int j = 0; j < NVAL; j++) {
+            s[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < TPR / 64; i++) s[j] += buf[(w0 + i) * NVAL + j];
+        }
+    }
+}
+
+constexpr int BT = 512;   // threads of a backward workgroup
+
+// Adds the groups' column sums in group order and writes them to part[which].
+template <int VEC, int TPR, int NV>
+__device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* out, int D, float* lds) {
+    constexpr int GR = BT / TPR;
+    const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < VEC; e++) lds[(grp * TPR + lane) * VEC + e] = acc[i][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < TPR * VEC; c += BT) {
+            float t = 0.f;
+            for (int k = 0; k < GR; k++) t += lds[k * TPR * VEC + c];
+            if (i * TPR * VEC + c < D) out[i * TPR * VEC + c] = t;
+        }
+    }
+}
+
+
+// Calls f(TPR, NV) for a row of nvt vectors: the smallest power of two of lanes
+// up to a wave with one vector each, then two vectors each, then 256 lanes
+// with one or two, 512 with two or (4-element vectors only) four.
+// MIN_TPR: rows as narrow as a part of a wave are not split further than this.
+template <int MIN_TPR, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
+#define LAYER_CASE(T, N) return f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
+    if constexpr (MIN_TPR < 64) {
+        if (nvt <= 8) LAYER_CASE(8, 1);
+        if (nvt <= 16) LAYER_CASE(16, 1);
+        if (nvt <= 32) LAYER_CASE(32, 1);
+    }
+    if (nvt <= 64) LAYER_CASE(64, 1);
+    if (nvt <= 128) LAYER_CASE(64, 2);
+    if (nvt <= 256) LAYER_CASE(256, 1);
+    if (nvt <= 512) LAYER_CASE(256, 2);
+    if constexpr (VEC == 4) {
+        if (nvt > 1024) LAYER_CASE(512, 4);
+    }
+    LAYER_CASE(512, 2);
+#undef LAYER_CASE
+}
+
+constexpr int MAX_BWD_BLOCKS = 512;   // two workgroups of eight waves per CU
+
+inline int grid_rows(long rows, int per, long most) {
+    const long n = (rows + per - 1) / per;
+    return (int)(n < most ? n : most);
+}
+
+// Joins the backward's partial column sums (layer_add_norm.hip).
+hipError_t norm_wsum(const NormArgs& a, int blocks, int n, hipStream_t s);
+hipError_t norm_zero_grads(const NormArgs& a, hipStream_t s);
+
+}  // namespace layer

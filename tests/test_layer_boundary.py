@@ -1,0 +1,295 @@
+"""CPU tests of the layer operators' boundary (include/gdn_layer.h): exported
+symbols, host-side refusals with their status codes before anything is launched,
+and the binding's argument checks."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def B():
+    from chunked_gated_delta_08_amd import binding
+    return binding
+
+
+def test_header_symbols_exported(B):
+    hdr = open(os.path.join(ROOT, "include", "gdn_layer.h")).read()
+    declared = set(re.findall(r"^(?:int64_t |size_t |int )(\w+)\(", hdr, flags=re.M))
+    assert declared == set(B.EXPORTED_LAYER)
+    for name in declared:
+        assert hasattr(B.lib, name), name
+    assert int(re.search(r"#define GLR_TILE (\d+)", hdr)[1]) == B.GLR_TILE
+
+
+# Addresses that are never read: every call below is refused on the host.  Each
+# buffer of a call has 2^40 bytes of its own.
+def at(i, off=0):
+    return ctypes.c_void_p((i + 1) * (1 << 40) + off)
+
+
+BIG = 1 << 39
+
+
+def norm(B, rows=4, D=8, eps=1e-5, dtype=2, res=2, act=0):
+    return B.NormProblem(rows, D, eps, dtype, res, act)
+
+
+def gated_fwd(B, p, **kw):
+    a = dict(x=at(0), z=at(1), w=at(2), y=at(3), **{})
+    a.update(kw)
+    return B.lib.gated_norm_fwd(ctypes.byref(p), a["x"], a["z"], a["w"], a["y"], None)
+
+
+def gated_bwd(B, p, ws_bytes=BIG, **kw):
+    a = dict(x=at(0), z=at(1), w=at(2), dy=at(3), dx=at(4), dz=at(5), dw=at(6), ws=at(7))
+    a.update(kw)
+    return B.lib.gated_norm_bwd(ctypes.byref(p), a["x"], a["z"], a["w"], a["dy"], a["dx"], a["dz"], a["dw"], a["ws"],
+                                ws_bytes, None)
+
+
+def add_fwd(B, p, **kw):
+    a = dict(x=at(0), res=at(1), w=at(2), scale=at(3), y=at(4), out=at(5))
+    a.update(kw)
+    return B.lib.add_norm_fwd(ctypes.byref(p), a["x"], a["res"], a["w"], a["scale"], a["y"], a["out"], None)
+
+
+def add_bwd(B, p, ws_bytes=BIG, **kw):
+    a = dict(dy=at(0), dres=at(1), res=at(2), w=at(3), x=at(4), scale=at(5), dx=at(6), out=at(7), dw=at(8), ds=at(9),
+             ws=at(10))
+    a.update(kw)
+    return B.lib.add_norm_bwd(ctypes.byref(p), a["dy"], a["dres"], a["res"], a["w"], a["x"], a["scale"], a["dx"],
+                              a["out"], a["dw"], a["ds"], a["ws"], ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), -1), (dict(D=0), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1),
+    (dict(eps=float("inf")), -1), (dict(dtype=3), -1), (dict(D=8193), -2), (dict(rows=1 << 60), -2)])
+def test_norm_problem_refused(B, kw, code):
+    p = norm(B, **kw)
+    assert gated_fwd(B, p) == code and gated_bwd(B, p) == code
+    assert add_fwd(B, p) == code and add_bwd(B, p) == code
+    assert B.lib.norm_workspace_size(ctypes.byref(p)) == 0
+
+
+def test_norm_types_refused(B):
+    assert gated_fwd(B, norm(B, act=2)) == -1 and gated_bwd(B, norm(B, act=2)) == -1
+    for dtype, res in ((2, 1), (1, 2), (0, 2)):
+        assert add_fwd(B, norm(B, dtype=dtype, res=res)) == -1 and add_bwd(B, norm(B, dtype=dtype, res=res)) == -1
+
+
+def test_norm_null_refused(B):
+    p = norm(B)
+    for n in ("x", "w", "y"):
+        assert gated_fwd(B, p, **{n: None}) == -1
+    for n in ("x", "w", "dy", "dx", "dw", "z", "dz"):   # dz exactly where z is
+        assert gated_bwd(B, p, **{n: None}) == -1
+    for n in ("x", "res", "w", "y", "out"):
+        assert add_fwd(B, p, **{n: None}) == -1
+    for n in ("dy", "res", "w", "x", "scale", "dx", "out", "dw", "ds"):
+        assert add_bwd(B, p, **{n: None}) == -1
+
+
+def test_norm_overlap_and_alignment_refused(B):
+    p = norm(B)   # a row-block of 64 bytes
+    assert gated_fwd(B, p, y=at(0, 16)) == -1            # y starts inside x
+    assert gated_fwd(B, p, y=at(2)) == -1                # y on w
+    assert gated_fwd(B, p, x=at(0, 1)) == -1             # not on an element
+    assert gated_fwd(B, p, w=at(2, 2)) == -1
+    assert gated_bwd(B, p, dx=at(1)) == -1               # dx may replace x or dy, not z
+    assert gated_bwd(B, p, dz=at(4)) == -1               # two outputs on one buffer
+    assert gated_bwd(B, p, dw=at(3)) == -1
+    assert add_fwd(B, p, out=at(0)) == -1                # res_out may replace res only
+    assert add_fwd(B, p, out=at(1, 2)) == -1
+    assert add_bwd(B, p, out=at(0)) == -1 and add_bwd(B, p, dx=at(7)) == -1 and add_bwd(B, p, ds=at(8)) == -1
+
+
+def test_norm_workspace(B):
+    p = norm(B, rows=1000, D=128)
+    need = B.lib.norm_workspace_size(ctypes.byref(p))
+    assert need > 0
+    for f in (gated_bwd, add_bwd):
+        assert f(B, p, ws_bytes=need - 1) == -3 and f(B, p, ws=None) == -3
+    assert gated_bwd(B, p, ws=at(7, 8)) == -3 and add_bwd(B, p, ws=at(10, 8)) == -3
+
+
+def test_norm_no_rows_needs_no_launch(B):
+    assert gated_fwd(B, norm(B, rows=0), x=None, z=None, w=None, y=None) == 0
+    assert add_fwd(B, norm(B, rows=0), x=None, res=None, y=None, out=None) == 0
+
+
+def glr(B, Bb=1, T=100, D=8, dtype=2, cu=None, N=None, host=True):
+    p = B.GlrProblem(Bb, T, D, 0, None, None, dtype)
+    keep = None
+    if cu is not None:
+        keep = (ctypes.c_int32 * len(cu))(*cu)
+        p.N = len(cu) - 1 if N is None else N
+        p.cu_seqlens = 512            # a device address the host never reads
+        p.cu_seqlens_host = ctypes.addressof(keep) if host else None
+    return p, keep
+
+
+def glr_fwd(B, p, ws_bytes=BIG, **kw):
+    a = dict(x=at(0), g=at(1), h0=at(2), h=at(3), ht=at(4), states=at(5), ws=at(6))
+    a.update(kw)
+    return B.lib.glr_fwd(ctypes.byref(p), a["x"], a["g"], a["h0"], a["h"], a["ht"], a["states"], a["ws"], ws_bytes,
+                         None)
+
+
+def glr_bwd(B, p, ws_bytes=BIG, **kw):
+    a = dict(x=at(0), g=at(1), h0=at(2), states=at(3), dh=at(4), dht=at(5), dx=at(6), dg=at(7), dh0=at(8), ws=at(9))
+    a.update(kw)
+    return B.lib.glr_bwd(ctypes.byref(p), a["x"], a["g"], a["h0"], a["states"], a["dh"], a["dht"], a["dx"], a["dg"],
+                         a["dh0"], a["ws"], ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(Bb=0), -1), (dict(T=-1), -1), (dict(D=0), -1), (dict(dtype=5), -1),
+    (dict(cu=[0, 50, 100], host=False), -1), (dict(cu=[1, 50, 100]), -1), (dict(cu=[0, 60, 50, 100]), -1),
+    (dict(cu=[0, 50, 99]), -1), (dict(cu=[0, 50, 100], Bb=2), -1), (dict(cu=[0, 100], N=0), -1),
+    (dict(D=(1 << 20) + 1), -2), (dict(Bb=1 << 12, T=1 << 20), -2), (dict(Bb=1 << 20, T=1, D=1 << 20), -2)])
+def test_glr_problem_refused(B, kw, code):
+    p, keep = glr(B, **kw)
+    assert glr_fwd(B, p) == code and glr_bwd(B, p) == code
+    assert B.lib.glr_num_states(ctypes.byref(p)) == -1 and B.lib.glr_workspace_size(ctypes.byref(p)) == 0
+
+
+def test_glr_buffers_refused(B):
+    p, _ = glr(B)
+    for n in ("x", "g", "h"):
+        assert glr_fwd(B, p, **{n: None}) == -1
+    for n in ("x", "g", "states", "dh", "dx", "dg"):
+        assert glr_bwd(B, p, **{n: None}) == -1
+    assert glr_fwd(B, p, h=at(0)) == -1 and glr_fwd(B, p, ht=at(2)) == -1 and glr_fwd(B, p, g=at(1, 2)) == -1
+    assert glr_bwd(B, p, dg=at(1)) == -1 and glr_bwd(B, p, dx=at(4)) == -1 and glr_bwd(B, p, dh0=at(5, 4)) == -1
+
+
+def test_glr_states_and_empty(B):
+    for T, n in ((0, 0), (1, 1), (16, 1), (17, 2)):
+        p, _ = glr(B, T=T)
+        assert B.lib.glr_num_states(ctypes.byref(p)) == n == B.glr_num_states(T)
+    p, _ = glr(B, T=0)
+    assert glr_fwd(B, p, ht=None) == 0 and glr_bwd(B, p, dh0=None) == 0   # nothing to write
+
+
+def test_glr_workspace(B):
+    p, _ = glr(B, T=100000, D=300)
+    need = B.lib.glr_workspace_size(ctypes.byref(p))
+    if need:
+        for f, ws in ((glr_fwd, 6), (glr_bwd, 9)):
+            assert f(B, p, ws_bytes=need - 1) == -3 and f(B, p, ws=None) == -3 and f(B, p, ws=at(ws, 8)) == -3
+
+
+def step(B, N=4, D=8, slots=4, dtype=2, **kw):
+    a = dict(x=at(0), g=at(1), slots=at(2), state=at(3), h=at(4))
+    a.update(kw)
+    return B.lib.glr_step(N, D, slots, dtype, a["x"], a["g"], a["slots"], a["state"], a["h"], None)
+
+
+def rule(B, N=4, HK=1, HV=2, K=64, V=64, slots=4, scale=0.0, dtype=2, **kw):
+    a = dict(q=at(0), k=at(1), v=at(2), g=at(3), beta=at(4), slots=at(5), state=at(6), o=at(7))
+    a.update(kw)
+    return B.lib.gdr_step(N, HK, HV, K, V, slots, scale, dtype, a["q"], a["k"], a["v"], a["g"], a["beta"], a["slots"],
+                          a["state"], a["o"], None)
+
+
+def test_steps_refused(B):
+    assert step(B, N=-1) == -1 and step(B, D=0) == -1 and step(B, dtype=9) == -1 and step(B, slots=-1) == -1
+    assert B.lib.glr_step(5, 8, 4, 2, at(0), at(1), None, at(3), at(4), None) == -1   # no slots, too few states
+    assert step(B, N=65537) == -2 and step(B, D=(1 << 20) + 1) == -2 and step(B, N=65536, D=1 << 20) == -2
+    for n in ("x", "g", "state", "h"):
+        assert step(B, **{n: None}) == -1
+    assert step(B, h=at(3)) == -1 and step(B, h=at(0, 2)) == -1 and step(B, state=at(1)) == -1
+    assert step(B, N=0, x=None, g=None, h=None, state=None) == 0
+
+    for kw in (dict(N=-1), dict(HK=0), dict(HK=2, HV=3), dict(K=0), dict(dtype=-1), dict(scale=float("nan")),
+               dict(scale=float("inf"))):
+        assert rule(B, **kw) == -1, kw
+    for kw in (dict(K=96, V=96), dict(K=64, V=128), dict(HV=1025, HK=1), dict(N=65537), dict(N=65536, HV=1024)):
+        assert rule(B, **kw) == -2, kw
+    for n in ("q", "k", "v", "g", "beta", "state", "o"):
+        assert rule(B, **{n: None}) == -1
+    assert rule(B, o=at(0)) == -1 and rule(B, state=at(2)) == -1 and rule(B, g=at(3, 1)) == -1
+    assert rule(B, N=0, q=None, k=None, v=None, g=None, beta=None, o=None, state=None) == 0
+
+
+# ------------------------------------------------------------ binding checks
+bf, f16, f32 = torch.bfloat16, torch.float16, torch.float32
+Z = torch.zeros
+
+
+@pytest.mark.parametrize("a,exc", [
+    (dict(z=Z(4, 8)), TypeError), (dict(z=Z(4, 7, dtype=bf)), ValueError), (dict(w=Z(8, dtype=bf)), TypeError),
+    (dict(w=Z(7)), ValueError), (dict(x=Z(8, 4, dtype=bf).T), ValueError), (dict(act="relu"), ValueError),
+    (dict(dy=None), ValueError), (dict(dy=Z(4, 8)), TypeError), (dict(x=Z(4, 8, dtype=torch.float64)), TypeError),
+    (dict(x=3), TypeError)])
+def test_gated_norm_args(B, a, exc):
+    d = dict(x=Z(4, 8, dtype=bf), z=Z(4, 8, dtype=bf), w=Z(8), dy=Z(4, 8, dtype=bf), act="silu")
+    B.check_gated_norm_args(need_dy=True, cuda=False, **d)
+    B.check_gated_norm_args(need_dy=True, cuda=False, **{**d, "z": None})
+    with pytest.raises(exc):
+        B.check_gated_norm_args(need_dy=True, cuda=False, **{**d, **a})
+
+
+@pytest.mark.parametrize("a,exc", [
+    (dict(res=Z(4, 8, dtype=f16)), TypeError), (dict(res=Z(3, 8)), ValueError), (dict(w=Z(8, dtype=bf)), TypeError),
+    (dict(scale=Z(4)), ValueError), (dict(x=None), ValueError), (dict(scale=None), ValueError),
+    (dict(dres=Z(4, 8, dtype=bf)), TypeError), (dict(x=Z(4, 8)), TypeError)])
+def test_add_norm_args(B, a, exc):
+    d = dict(dy=Z(4, 8, dtype=bf), dres=Z(4, 8), res=Z(4, 8), w=Z(8), x=Z(4, 8, dtype=bf), scale=Z(8))
+    B.check_add_norm_bwd_args(cuda=False, **d)
+    B.check_add_norm_bwd_args(cuda=False, **{**d, "x": None, "scale": None, "dres": None})
+    with pytest.raises(exc):
+        B.check_add_norm_bwd_args(cuda=False, **{**d, **a})
+
+
+@pytest.mark.parametrize("a,exc", [
+    (dict(g=Z(6, 5, dtype=bf)), TypeError), (dict(g=Z(5, 5)), ValueError), (dict(h0=Z(1, 5)), ValueError),
+    (dict(B=4), ValueError), (dict(B=0), ValueError), (dict(dh=Z(6, 5)), TypeError), (dict(dht=Z(2, 4)), ValueError),
+    (dict(states=Z(2, 5)), ValueError), (dict(B=1, cu_seqlens=torch.tensor([0, 2, 6])), TypeError),
+    (dict(cu_seqlens=torch.tensor([0, 2, 6], dtype=torch.int32)), ValueError),   # B = 2 beside it
+    (dict(cu_seqlens_host=torch.tensor([0, 2, 6], dtype=torch.int32)), ValueError),
+    (dict(x=Z(6, 5, 1, dtype=bf)), ValueError)])
+def test_glr_args(B, a, exc):
+    d = dict(x=Z(6, 5, dtype=bf), g=Z(6, 5), h0=Z(2, 5), B=2, dh=Z(6, 5, dtype=bf), dht=Z(2, 5), states=Z(1, 5))
+    assert B.check_glr_args(bwd=True, cuda=False, **d) == 2
+    cu = torch.tensor([0, 2, 6], dtype=torch.int32)
+    assert B.check_glr_args(bwd=True, cuda=False, **{**d, "B": 1, "cu_seqlens": cu, "cu_seqlens_host": cu}) == 2
+    with pytest.raises(exc):
+        B.check_glr_args(bwd=True, cuda=False, **{**d, **a})
+
+
+@pytest.mark.parametrize("a,exc", [
+    (dict(state=Z(3, 2, 8, 8)), ValueError), (dict(state=Z(4, 2, 8, 8, dtype=bf)), TypeError),
+    (dict(state=Z(4, 2, 8, 4)), ValueError), (dict(slots=Z(4, dtype=torch.int64)), TypeError),
+    (dict(slots=Z(3, dtype=torch.int32)), ValueError), (dict(q=Z(4, 2, 8, dtype=bf)), ValueError),
+    (dict(k=Z(4, 1, 8)), TypeError), (dict(beta=Z(4, 2)), TypeError), (dict(g=Z(4, 1)), ValueError),
+    (dict(state=Z(4, 2, 8, 8).transpose(2, 3)), ValueError)])
+def test_gdr_step_args(B, a, exc):
+    d = dict(q=Z(4, 1, 8, dtype=bf), k=Z(4, 1, 8, dtype=bf), v=Z(4, 2, 8, dtype=bf), g=Z(4, 2), beta=Z(4, 2, dtype=bf),
+             state=Z(4, 2, 8, 8))
+    B.check_gdr_step_args(cuda=False, **d)
+    B.check_gdr_step_args(cuda=False, **{**d, "state": Z(1, 2, 8, 8), "slots": Z(4, dtype=torch.int32)})
+    with pytest.raises(exc):
+        B.check_gdr_step_args(cuda=False, **{**d, **a})
+
+
+@pytest.mark.parametrize("a,exc", [
+    (dict(state=Z(3, 8)), ValueError), (dict(state=Z(4, 7)), ValueError), (dict(g=Z(4, 8, dtype=bf)), TypeError),
+    (dict(slots=Z(4)), TypeError), (dict(x=Z(4, 2, 4, dtype=bf)), ValueError)])
+def test_glr_step_args(B, a, exc):
+    d = dict(x=Z(4, 8, dtype=bf), g=Z(4, 8), state=Z(4, 8))
+    B.check_glr_step_args(cuda=False, **d)
+    with pytest.raises(exc):
+        B.check_glr_step_args(cuda=False, **{**d, **a})
+
+
+def test_gpu_tensors_are_needed(B):
+    with pytest.raises(ValueError):
+        B.gated_norm_fwd(Z(4, 8), None, Z(8))
+    with pytest.raises(ValueError):
+        B.glr_fwd(Z(4, 8), Z(4, 8))
