@@ -41,6 +41,7 @@ struct GlrArgs {
     void* ws;
 };
 size_t glr_ws_bytes(const GlrArgs& a);
+long glr_workgroups(const GlrArgs& a);
 hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t s);
 
