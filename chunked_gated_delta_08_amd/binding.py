@@ -503,7 +503,8 @@ class NormProblem(ctypes.Structure):
 
 class GlrProblem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("N", ctypes.c_int),
-                ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p), ("dtype", ctypes.c_int)]
+                ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("polls", ctypes.c_int)]
 
 
 GLR_TILE = 16
@@ -726,14 +727,15 @@ def check_glr_args(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, dh
     return N
 
 
-def _glr_problem(x, cu_seqlens, cu_seqlens_host, B):
+def _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls=0):
     """The problem struct and what has to outlive its use.  Without a host mirror
     cu_seqlens is copied to the host, which waits for the current stream."""
     ntok, D = x.shape
     if cu_seqlens is None:
-        return GlrProblem(B, ntok // B, D, 0, None, None, _DT[x.dtype]), None
+        return GlrProblem(B, ntok // B, D, 0, None, None, _DT[x.dtype], polls), None
     host = cu_seqlens.detach().cpu() if cu_seqlens_host is None else cu_seqlens_host
-    return GlrProblem(1, ntok, D, host.numel() - 1, cu_seqlens.data_ptr(), host.data_ptr(), _DT[x.dtype]), host
+    return GlrProblem(1, ntok, D, host.numel() - 1, cu_seqlens.data_ptr(), host.data_ptr(), _DT[x.dtype],
+                      polls), host
 
 
 def glr_num_states(ntok):
@@ -750,7 +752,7 @@ def _glr_workspace(p, workspace, dev):
 
 
 def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=True, want_states=False, out=None,
-            workspace=None, stream=None):
+            workspace=None, stream=None, polls=0):
     """Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t over [B*T, D].  Returns dict
     h (x's dtype), ht [N, D] fp32, states (for glr_bwd, when wanted).  Give
     cu_seqlens_host (the CPU copy of cu_seqlens) to avoid a copy and its wait."""
@@ -767,7 +769,7 @@ def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=T
     _need(out["h"], "h", x.dtype, x.shape)
     _need(out["ht"], "ht", torch.float32, (N, D), optional=True)
     _need(out["states"], "states", torch.float32, (glr_num_states(ntok), D), optional=True)
-    p, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B)
+    p, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
     ws = _glr_workspace(p, workspace, dev)
     own += [ws] if workspace is None else []
     _same_device(x, *out.values(), ws)
@@ -779,7 +781,7 @@ def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=T
 
 
 def glr_bwd(x, g, dh, states, dht=None, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_dh0=True, out=None,
-            workspace=None, stream=None):
+            workspace=None, stream=None, polls=0):
     """Gradients of glr_fwd for dh of h and dht of ht; states from glr_fwd(want_states=True).
     Returns dict dx (x's dtype), dg fp32, dh0 [N, D] fp32."""
     N = check_glr_args(x, g, h0, cu_seqlens, cu_seqlens_host, B, dh, dht, states, bwd=True)
@@ -792,7 +794,7 @@ def glr_bwd(x, g, dh, states, dht=None, h0=None, cu_seqlens=None, cu_seqlens_hos
     _need(out["dx"], "dx", x.dtype, x.shape)
     _need(out["dg"], "dg", torch.float32, x.shape)
     _need(out["dh0"], "dh0", torch.float32, (N, D), optional=True)
-    p, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B)
+    p, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
     ws = _glr_workspace(p, workspace, dev)
     own += [ws] if workspace is None else []
     _same_device(x, *out.values(), ws)

@@ -10,20 +10,22 @@
 // element in bf16 against a few operations), so each reads its tensors once:
 //   - The token axis of the whole batch is cut into tiles of L tokens, one wave
 //     each, C channels a lane, the tile held in registers; W tiles make a
-//     segment, one workgroup.  A tile's map is composed in registers, the tiles
-//     of a segment through LDS.
-//   - Across segments each workgroup publishes its map (P, H) before it waits for
-//     anything, then composes the maps of the segments before it.  Segments are
-//     grouped by G; the last one of a group publishes the state that leaves it,
-//     so a segment reads at most G - 1 maps and one state.  The order of every
-//     composition is fixed by the sizes alone: equal inputs give equal bits.
+//     segment, one pass of a workgroup.  A tile's map is composed in registers,
+//     the tiles of a segment through LDS.
+//   - Across segments: a workgroup publishes its segment's map (P, H) before it
+//     waits for anything.  G segments make a group, whose last one publishes the
+//     group's map; G groups make a block, whose last one publishes the state that
+//     leaves it.  What enters a segment is one state, at most G - 1 group maps and
+//     at most G - 1 maps, one read by each wave, composed in an order fixed by
+//     the sizes alone: equal inputs give equal bits.
 //   - A sequence that begins inside takes its state from h0 and nothing from
 //     before, by a branch that is uniform over the wave (a product with zero
 //     would let another sequence's infinity or NaN through).
-// Waiting ends: a workgroup takes its segment from a counter, so the segments
-// that it waits for belong to workgroups that already run, and those publish
-// their maps without waiting; a group's state waits for the previous group's
-// only.  (A poll also gives up after POLLS tries and yields NaN.)
+// Waiting ends, whatever the order in which workgroups start: after `polls` tries
+// a workgroup takes up the first earlier segment whose map is not there, as if it
+// were its own (both give the same bits), and then begins its own again.  The
+// first segment that is not finished waits for nothing, so it is finished by
+// whoever has it, or by one that waits for it.
 // The state is carried in fp32 throughout; h and dx are rounded once.  The
 // backward recomputes h_{t-1} from the states that the forward saved at every
 // tile, not from the rounded h: dg is an fp32 output.
@@ -37,11 +39,8 @@ namespace {
 using gdr::bf16;
 using gdr::f16;
 constexpr int L = GLR_TILE;
-constexpr int W = 8;            // waves (tiles) of a segment
-constexpr int SEG = W * L;      // tokens of a segment
-constexpr int G = 16;           // segments of a group
-constexpr int PPW = (G - 2) / W + 1;   // maps a wave composes
-constexpr int POLLS = 1 << 22;
+constexpr int G = 8;            // segments of a group, groups of a block
+constexpr int SLEEP = 8;        // 64 clocks each between two looks
 
 template <class E, int N> struct VecU { typedef E t __attribute__((ext_vector_type(N), aligned(sizeof(E)))); };
 
@@ -54,39 +53,8 @@ __device__ __forceinline__ unsigned bits_of(float x) { return x != x ? 0x7fc0000
 __device__ __forceinline__ void publish(u64* p, float P, float H) {
     __hip_atomic_store(p, (u64)bits_of(P) << 32 | bits_of(H), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void publish(unsigned* p, float h) {
-    __hip_atomic_store(p, bits_of(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// Waits until C consecutive values are there.
-template <int C> __device__ __forceinline__ void await(const u64* p, float (&P)[C], float (&H)[C]) {
-    u64 v[C];
-    for (int n = 0; n < POLLS; n++) {
-        bool all = true;
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-            v[c] = __hip_atomic_load(p + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            all = all && v[c] != NOT_YET;
-        }
-        if (all) break;
-        __builtin_amdgcn_s_sleep(1);
-    }
-#pragma unroll
-    for (int c = 0; c < C; c++) P[c] = __uint_as_float(v[c] >> 32), H[c] = __uint_as_float((unsigned)v[c]);
-}
-template <int C> __device__ __forceinline__ void await(const unsigned* p, float (&h)[C]) {
-    unsigned v[C];
-    for (int n = 0; n < POLLS; n++) {
-        bool all = true;
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-            v[c] = __hip_atomic_load(p + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            all = all && v[c] != ~0u;
-        }
-        if (all) break;
-        __builtin_amdgcn_s_sleep(1);
-    }
-#pragma unroll
-    for (int c = 0; c < C; c++) h[c] = __uint_as_float(v[c]);
+__device__ __forceinline__ u64 peek(const u64* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // ------------------------------------------------------------- sequences
@@ -94,14 +62,16 @@ template <int C> __device__ __forceinline__ void await(const unsigned* p, float 
 struct Seqs {
     const int32_t* cu;
     int T, nseq;
-    __device__ __forceinline__ int first(int n) const { return cu ? cu[n] : n * T; }
+    __device__ __forceinline__ int first(int n) const {
+        return cu ? __builtin_amdgcn_readfirstlane(cu[n]) : n * T;
+    }
     // the (non-empty) sequence of token t
     __device__ __forceinline__ int of(int t) const {
         if (!cu) return t / T;
         int lo = 0, hi = nseq;   // first(lo) <= t < first(hi)
         while (hi - lo > 1) {
             const int m = (lo + hi) >> 1;
-            if (cu[m] <= t) lo = m;
+            if (first(m) <= t) lo = m;
             else hi = m;
         }
         return lo;
@@ -154,354 +124,515 @@ template <int C> __device__ __forceinline__ void store_row(float* p, const float
     *(typename VecU<float, C>::t*)p = t;
 }
 // The row of sequence n of a [nseq, D] tensor, zero where it is absent.
-template <int C> __device__ __forceinline__ void seq_row(const float* s, int n, int D, int ch, float (&v)[C]) {
+template <int C> __device__ __forceinline__ void seq_row(const float* s, int n, int D, unsigned ch, float (&v)[C]) {
 #pragma unroll
     for (int c = 0; c < C; c++) v[c] = 0.f;
-    if (s) load_row<C>(s + (long)n * D + ch, v);
+    if (s) load_row<C>(gdr::at32(s + (long)n * D, ch), v);
 }
 // Sequences without tokens before token t, at which one begins (or the end of
 // all): their output row is their input row.
 template <int C>
-__device__ __forceinline__ void pass_empty(const Seqs& q, int n, int t, const float* in, float* out, int D, int ch) {
+__device__ __forceinline__ void pass_empty(const Seqs& q, int n, int t, const float* in, float* out, int D, unsigned ch) {
     for (int m = n - 1; m >= 0 && q.first(m) == t; m--) {
         float v[C];
         seq_row<C>(in, m, D, ch, v);
-        store_row<C>(out + (long)m * D + ch, v);
+        store_row<C>(gdr::at32(out + (long)m * D, ch), v);
     }
 }
 
-// The workspace: a counter, the segments' maps and the groups' states, all set
-// to ones before (NOT_YET; the counter then gives 0 after one increment).
+// The workspace: the maps of segments and groups and the states that leave blocks
+// (as maps with P = 0), all set to NOT_YET before.
 struct Ws {
-    unsigned* count;
-    u64* map;          // [nseg][D]
-    unsigned* state;   // [groups][D]: what enters group 1, 2, ...
+    u64 *map, *group, *state;   // [segments][D], [groups][D], [blocks][D]
 };
-constexpr size_t WS_HEAD = 256;
-__host__ __device__ __forceinline__ Ws carve(void* ws, int nseg, int D) {
-    char* b = (char*)ws;
-    return Ws{(unsigned*)b, (u64*)(b + WS_HEAD), (unsigned*)(b + WS_HEAD + (size_t)nseg * D * 8)};
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ size_t ws_bytes(int nseg, int D) {
+    return ((size_t)nseg + ceil_div(nseg, G) + ceil_div(nseg, G * G)) * D * 8;
+}
+__device__ __forceinline__ Ws carve(void* ws, int nseg, int D) {
+    u64* group = (u64*)ws + (size_t)nseg * D;
+    return Ws{(u64*)ws, group, group + (size_t)ceil_div(nseg, G) * D};
 }
 
-// What enters segment `idx` (in processing order): the composition of the maps
-// of segments src .. idx - 1, src the one in which the sequence was entered, or
-// the state that entered the group.  Called by all waves; `mp` holds W maps.
-template <int C>
-__device__ __forceinline__ void enter_segment(const Ws& ws, int idx, int src, int D, int ch, float (*mp)[2][64 * C],
-                                              float (&in)[C]) {
-    const int w = threadIdx.x >> 6, l = threadIdx.x & 63, g0 = idx / G * G;
-    const bool whole = src >= g0;                   // the sequence was entered in this group
-    const int j0 = whole ? src : g0, j = j0 + w * PPW;
-    float P[C], H[C];
-#pragma unroll
-    for (int c = 0; c < C; c++) P[c] = 1.f, H[c] = 0.f;
-    if (w == 0 && !whole) await<C>(ws.state + (size_t)(g0 / G - 1) * D + ch, H);
-#pragma unroll
-    for (int i = 0; i < PPW; i++) {
-        if (j + i >= idx) break;
-        float p[C], h[C];
-        await<C>(ws.map + (size_t)(j + i) * D + ch, p, h);
-        if (j + i == src) {   // whatever came before does not reach past it
-#pragma unroll
-            for (int c = 0; c < C; c++) P[c] = 0.f, H[c] = h[c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; c++) P[c] *= p[c], H[c] = p[c] * H[c] + h[c];
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < C; c++) mp[w][0][l * C + c] = P[c], mp[w][1][l * C + c] = H[c];
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; c++) in[c] = mp[0][1][l * C + c];
-#pragma unroll
-    for (int v = 1; v < W; v++)
-        if (j0 + v * PPW < idx)
-#pragma unroll
-            for (int c = 0; c < C; c++) in[c] = mp[v][0][l * C + c] * in[c] + mp[v][1][l * C + c];
-}
-
-// Composes the segment's tiles: `mp` the tiles' maps in processing order, bit v
-// of `cut` set where tile v does not depend on what enters it.
+// Composes onto (P, H) the tiles [v0, v1) of a segment: `mp` their maps in
+// processing order, bit v of `cut` set where tile v does not depend on what enters it.
 template <int C>
 __device__ __forceinline__ void through_tiles(const float (*mp)[2][64 * C], unsigned cut, int v0, int v1,
                                               float (&P)[C], float (&H)[C]) {
-    const int l = threadIdx.x & 63;
+    const int l = gdr::lane_o();
+#pragma unroll 2
     for (int v = v0; v < v1; v++) {
-        if (cut >> v & 1) {
-#pragma unroll
-            for (int c = 0; c < C; c++) P[c] = 0.f, H[c] = mp[v][1][l * C + c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; c++) {
-                const float p = mp[v][0][l * C + c];
-                P[c] *= p;
-                H[c] = p * H[c] + mp[v][1][l * C + c];
-            }
-        }
-    }
-}
-
-// The segment's place among the others: processing index and channel block.
-__device__ __forceinline__ void take(const Ws& ws, bool chain, int nblk, int* tick, int& idx, int& blk) {
-    unsigned k = blockIdx.x;
-    if (chain) {
-        if (threadIdx.x == 0)
-            *tick = (int)(__hip_atomic_fetch_add(ws.count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u);
-        __syncthreads();
-        k = (unsigned)__builtin_amdgcn_readfirstlane(*tick);
-    }
-    idx = (int)(k / (unsigned)nblk);
-    blk = (int)(k % (unsigned)nblk);
-}
-
-// Rows of a tile from token t0c on, C channels of each; rows past the last
-// token read it again (they are not used).
-template <class E, int C>
-__device__ __forceinline__ void load_tile(const E* p, int D, int last, typename VecU<E, C>::t (&v)[L]) {
-#pragma unroll
-    for (int i = 0; i < L; i++) v[i] = *(const typename VecU<E, C>::t*)(p + (unsigned)min(i, last) * (unsigned)D);
-}
-
-template <class E, int C>
-__global__ __launch_bounds__(64 * W) void glr_fwd_kernel(GlrArgs a, int nblk, int nseg, bool chain) {
-    __shared__ float mp[W][2][64 * C], ep[W][2][64 * C];
-    __shared__ unsigned cuts[W];
-    __shared__ int tick;
-    const Ws ws = carve(a.ws, nseg, a.D);
-    int seg, blk;
-    take(ws, chain, nblk, &tick, seg, blk);
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, D = a.D;
-    const int ntok = (int)a.ntok, ch = min((blk * 64 + l) * C, D - C);   // lanes past the end repeat the last channels
-    const Seqs q{a.cu, a.T, a.nseq};
-    const Tile tile(q, seg * SEG + w * L, ntok);
-    const int t0c = min(tile.t0, ntok - 1);
-    const long base = (long)t0c * D + ch;
-    typename VecU<E, C>::t x[L];
-    float al[L][C];
-    {
-        typename VecU<float, C>::t g[L];
-        load_tile<float, C>(a.g + base, D, ntok - 1 - t0c, g);
-        load_tile<E, C>((const E*)a.x + base, D, ntok - 1 - t0c, x);
-#pragma unroll
-        for (int i = 0; i < L; i++)
-#pragma unroll
-            for (int c = 0; c < C; c++) {   // past the end: the identity
-                al[i][c] = i < tile.nt ? expf(g[i][c]) : 1.f;
-                if (i >= tile.nt) x[i][c] = (E)0.f;
-            }
-    }
-    float P[C], H[C];
-#pragma unroll
-    for (int c = 0; c < C; c++) P[c] = 1.f, H[c] = 0.f;
-    {
-        int n = tile.n0;
-#pragma unroll
-        for (int i = 0; i < L; i++) {
-            if (tile.begins >> i & 1) {
-                if (i > 0) n = q.next(n);
-                seq_row<C>(a.h0, n, D, ch, H);
-            }
-#pragma unroll
-            for (int c = 0; c < C; c++) {
-                P[c] *= al[i][c];
-                H[c] = al[i][c] * H[c] + (float)x[i][c];
-            }
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < C; c++) mp[w][0][l * C + c] = P[c], mp[w][1][l * C + c] = H[c];
-    if (l == 0) cuts[w] = tile.begins != 0;
-    __syncthreads();
-    unsigned cut = 0;
-#pragma unroll
-    for (int v = 0; v < W; v++) cut |= cuts[v] << v;
-    cut = __builtin_amdgcn_readfirstlane(cut);
-    float in[C];
-#pragma unroll
-    for (int c = 0; c < C; c++) in[c] = 0.f;
-    const int T0 = seg * SEG;
-    if (chain) {
-        if (w == 0 && seg + 1 < nseg) {
-#pragma unroll
-            for (int c = 0; c < C; c++) P[c] = 1.f, H[c] = 0.f;
-            through_tiles<C>(mp, cut, 0, W, P, H);
-#pragma unroll
-            for (int c = 0; c < C; c++) publish(ws.map + (size_t)seg * D + ch + c, P[c], H[c]);
-            asm volatile("" ::: "memory");   // published before anything is waited for
-        }
-        const int s0 = q.first(q.of(T0));   // where the sequence that enters began
-        if (s0 < T0) enter_segment<C>(ws, seg, s0 / SEG, D, ch, ep, in);
-        if (w == 0 && seg % G == G - 1 && seg + 1 < nseg) {
-            float p1[C], out[C];
-#pragma unroll
-            for (int c = 0; c < C; c++) p1[c] = 1.f, out[c] = in[c];
-            through_tiles<C>(mp, cut, 0, W, p1, out);
-#pragma unroll
-            for (int c = 0; c < C; c++) publish(ws.state + (size_t)(seg / G) * D + ch + c, out[c]);
-        }
-    }
-    if (tile.nt == 0) return;
-#pragma unroll
-    for (int c = 0; c < C; c++) P[c] = 1.f;
-    through_tiles<C>(mp, cut, 0, w, P, in);
-    E* out = (E*)a.h + base;
-    int n = tile.n0;
-#pragma unroll
-    for (int i = 0; i < L; i++) {
-        if (tile.begins >> i & 1) {
-            if (i > 0) {
-                if (a.ht) store_row<C>(a.ht + (long)n * D + ch, in);   // the state that the sequence ends with
-                n = q.next(n);
-            }
-            if (a.ht) pass_empty<C>(q, n, tile.t0 + i, a.h0, a.ht, D, ch);
-            seq_row<C>(a.h0, n, D, ch, in);
-        }
-        if (i == 0 && a.states) store_row<C>(a.states + (long)(tile.t0 / L) * D + ch, in);
-        typename VecU<E, C>::t o;
+        const bool cuts = cut >> v & 1;
 #pragma unroll
         for (int c = 0; c < C; c++) {
-            in[c] = al[i][c] * in[c] + (float)x[i][c];
-            o[c] = (E)in[c];
+            const float p = mp[v][0][l * C + c], h = mp[v][1][l * C + c];
+            P[c] = cuts ? 0.f : P[c] * p;
+            H[c] = cuts ? h : p * H[c] + h;
         }
-        if (i < tile.nt) *(typename VecU<E, C>::t*)(out + (unsigned)i * (unsigned)D) = o;
     }
-    if (a.ht && tile.t0 + tile.nt == q.first(n + 1)) {
-        store_row<C>(a.ht + (long)n * D + ch, in);
-        if (tile.t0 + tile.nt == ntok) pass_empty<C>(q, a.nseq, ntok, a.h0, a.ht, D, ch);
+}
+
+// Bit v: tile v of the segment does not depend on what enters it.
+template <int W> __device__ __forceinline__ unsigned cut_bits(const unsigned* cuts) {
+    unsigned all = 0;
+#pragma unroll
+    for (int v = 0; v < W; v++) all |= cuts[v] << v;
+    return __builtin_amdgcn_readfirstlane(all);
+}
+template <int W, int C> using Maps = float[W][2][64 * C];
+
+// Hands a wave's tile map (P, H) to the others and composes the maps of the tiles
+// before its own (kept in `qi` for enter_tile), and its own onto them into (P, H).
+// `cut`: the tile does not depend on what enters it.  Returns whether (P, H) so
+// composed does not.
+template <int W, int C>
+__device__ __forceinline__ bool tiles_before(Maps<W, C>& mp, Maps<W, C>& qi, unsigned* cuts, int w, bool cut, float (&P)[C],
+                                             float (&H)[C]) {
+    const int l = gdr::lane_o();
+#pragma unroll
+    for (int c = 0; c < C; c++) mp[w][0][l * C + c] = P[c], mp[w][1][l * C + c] = H[c];
+    if (l == 0) cuts[w] = cut;
+    gdr::lds_barrier();
+    const unsigned all = cut_bits<W>(cuts);
+    float Q[C], I[C];
+#pragma unroll
+    for (int c = 0; c < C; c++) Q[c] = 1.f, I[c] = 0.f;
+    through_tiles<C>(mp, all, 0, w, Q, I);
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        qi[w][0][l * C + c] = Q[c], qi[w][1][l * C + c] = I[c];
+        H[c] = cut ? H[c] : P[c] * I[c] + H[c];
+        P[c] = cut ? 0.f : P[c] * Q[c];
+    }
+    return all & ((2u << w) - 1);
+}
+// What enters a tile: the maps of those before it applied to what enters the segment.
+template <int W, int C>
+__device__ __forceinline__ void enter_tile(const Maps<W, C>& qi, unsigned cuts_before, int w, float (&in)[C]) {
+    const int l = gdr::lane_o();
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        const float I = qi[w][1][l * C + c];
+        in[c] = cuts_before ? I : qi[w][0][l * C + c] * in[c] + I;
+    }
+}
+
+
+// Waits until the maps at `a` and `b` (uniform; NULL: none) are there and leaves
+// them in LDS.  Both are read at once, so what is there costs one round trip; what
+// is not is looked for by one element of each (whole rows read by every wave in
+// flight over and over would take a good part of the bandwidth), then read again.
+// False after `polls` tries without success.
+template <int W, int C>
+__device__ __forceinline__ bool await(const u64* a, const u64* b, unsigned ch, int w, int polls, Maps<W, C>& ea,
+                                      Maps<W, C>& eb) {
+    u64 u[C], v[C];
+    bool all = false;
+    const unsigned one = __builtin_amdgcn_readfirstlane(ch) + C - 1;
+    for (int n = 0;;) {
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            if (a) u[c] = peek(gdr::at32(a, ch + c));
+            if (b) v[c] = peek(gdr::at32(b, ch + c));
+        }
+        all = true;
+#pragma unroll
+        for (int c = 0; c < C; c++) all = all && (!a || u[c] != NOT_YET) && (!b || v[c] != NOT_YET);
+        all = __all(all);
+        if (all || ++n >= polls) break;
+        for (; n < polls; n++) {
+            __builtin_amdgcn_s_sleep(SLEEP);
+            const u64 x = a ? peek(a + one) : 0, y = b ? peek(b + one) : 0;
+            if (x != NOT_YET && y != NOT_YET) break;
+        }
+    }
+    const int l = gdr::lane_o();
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        if (a) ea[w][0][l * C + c] = __uint_as_float((unsigned)(u[c] >> 32)), ea[w][1][l * C + c] = __uint_as_float((unsigned)u[c]);
+        if (b) eb[w][0][l * C + c] = __uint_as_float((unsigned)(v[c] >> 32)), eb[w][1][l * C + c] = __uint_as_float((unsigned)v[c]);
+    }
+    return all;
+}
+
+// Whether all waves of the workgroup say yes, after a barrier.
+template <int W> __device__ __forceinline__ bool all_waves(bool yes, unsigned* votes, int w) {
+    if (gdr::lane_o() == 0) votes[w] = yes;
+    gdr::lds_barrier();
+    unsigned all = 1;
+#pragma unroll
+    for (int v = 0; v < W; v++) all &= votes[v];
+    return __builtin_amdgcn_readfirstlane(all);
+}
+
+template <int C>
+__device__ __forceinline__ void publish_row(u64* p, unsigned ch, const float (&P)[C], const float (&H)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; c++) publish(gdr::at32(p, ch + c), P[c], H[c]);
+    asm volatile("" ::: "memory");   // published before anything after it is waited for
+}
+
+// All of a segment's business with the others, by all waves: publishes its map,
+// its group's and its block's state where it is their last, and returns what
+// enters it.  `idx` counts segments in processing order, `src` is the one in which
+// the sequence that enters was itself entered (src = idx: none enters).  (P, H) is
+// the segment's map in wave W - 1 (w: place in processing order), `cut` whether it
+// does not depend on what enters; `tot` keeps it.  False if it did not get all
+// that it waits for.
+template <int W, int C>
+__device__ __forceinline__ bool exchange(const Ws& ws, int idx, int nseg, int src, int D, unsigned ch, int w, int polls,
+                                         bool cut, const float (&P)[C], const float (&H)[C], Maps<W, C>& ea, Maps<W, C>& eb,
+                                         float (*tot)[64 * C], unsigned (*votes)[W], float (&in)[C]) {
+    const int l = gdr::lane_o();
+    const bool entered = src < idx, later = idx + 1 < nseg, tells = w == W - 1 && later;
+    const bool closes = later && idx % G == G - 1;
+    const int g = idx / G, g0 = g * G, first = max(src, g0), na = entered ? idx - first : 0;
+    const bool outside = entered && src < g0, far = outside && src / G < g / G * G;
+    const int gfirst = far ? g / G * G : src / G, nb = outside ? g - gfirst + far : 0;
+    const u64* a = w < na ? ws.map + (size_t)(first + w) * D : nullptr;
+    const u64* b = w >= nb ? nullptr : far && w == 0 ? ws.state + (size_t)(g / G - 1) * D
+                                                     : ws.group + (size_t)(gfirst + w - far) * D;
+    if (tells) {
+        publish_row<C>(ws.map + (size_t)idx * D, ch, P, H);
+        if (closes)
+#pragma unroll
+            for (int c = 0; c < C; c++) tot[0][l * C + c] = P[c], tot[1][l * C + c] = H[c];
+    }
+    if (closes) {   // the group's map needs the maps of the group only
+        float p[C], h[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) p[c] = 1.f, h[c] = 0.f;
+        if (na > 0) {
+            if (!all_waves<W>(await<W, C>(a, nullptr, ch, w, polls, ea, eb), votes[0], w)) return false;
+            through_tiles<C>(ea, outside ? 0u : 1u, 0, na, p, h);
+        }
+        if (tells) {
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                const float P1 = tot[0][l * C + c], H1 = tot[1][l * C + c];
+                p[c] = cut ? 0.f : P1 * p[c];
+                h[c] = cut ? H1 : P1 * h[c] + H1;
+            }
+            publish_row<C>(ws.group + (size_t)g * D, ch, p, h);
+        }
+        a = nullptr;
+    }
+    if (entered) {
+        if (!all_waves<W>(await<W, C>(a, b, ch, w, polls, ea, eb), votes[1], w)) return false;
+        float p[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) p[c] = 1.f, in[c] = 0.f;
+        through_tiles<C>(eb, far ? 0u : 1u, 0, nb, p, in);
+        through_tiles<C>(ea, outside ? 0u : 1u, 0, na, p, in);
+    }
+    if (tells && idx % (G * G) == G * G - 1) {
+        float p[C], h[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            const float P1 = tot[0][l * C + c], H1 = tot[1][l * C + c];
+            p[c] = 0.f;
+            h[c] = cut ? H1 : P1 * in[c] + H1;
+        }
+        publish_row<C>(ws.state + (size_t)(g / G) * D, ch, p, h);
+    }
+    return true;
+}
+
+// The first segment before `idx` whose map is not there (idx: none), found by the
+// first wave for all.
+template <int C>
+__device__ __forceinline__ int first_missing(const Ws& ws, int idx, int D, unsigned ch, int w, int& found) {
+    int j = 0;
+    for (; w == 0 && j < idx; j++) {
+        bool there = true;
+#pragma unroll
+        for (int c = 0; c < C; c++) there = there && peek(gdr::at32(ws.map + (size_t)j * D, ch + c)) != NOT_YET;
+        if (!__all(there)) break;
+    }
+    if (threadIdx.x == 0) found = j;
+    gdr::lds_barrier();
+    return __builtin_amdgcn_readfirstlane(found);
+}
+
+// exp(g), off by at most (|g| + 3) 2^-24 of itself: the exponent's one rounding,
+// log2(e)'s, and two for exp2; zero below 2^-126.  The library's expf is within 2 2^-24, but its
+// range checks hold 64-bit masks for every element of the tile in scalar
+// registers, which then spill.  What the state loses to it is little: a token
+// with a large |g| hardly passes the state on, and over the tokens that do the
+// |g| add up to about one.
+__device__ __forceinline__ float gate(float g) { return __builtin_amdgcn_exp2f(1.44269504f * g); }
+
+// Keeps a value as it was loaded: its widening to fp32 is not carried from one
+// pass over the tile to the next in twice the registers.
+template <class E, int C> __device__ __forceinline__ void as_loaded(typename VecU<E, C>::t (&v)[L]) {
+    if constexpr (C * sizeof(E) >= 4) {
+        constexpr int N = C * sizeof(E) / 4;
+#pragma unroll
+        for (int i = 0; i < L; i++) {
+            unsigned u[N];
+            __builtin_memcpy(u, &v[i], 4 * N);
+#pragma unroll
+            for (int k = 0; k < N; k++) asm volatile("" : "+v"(u[k]));
+            __builtin_memcpy(&v[i], u, 4 * N);
+        }
+    }
+}
+
+// A lane's first channel; lanes past the end repeat the last ones.  (lane_o: what
+// derives from the lane is formed where it is used, not held over the kernel's loop.)
+template <int C> __device__ __forceinline__ unsigned channel(int blk, int D) {
+    return (unsigned)min((blk * 64 + gdr::lane_o()) * C, D - C);
+}
+
+// Tokens past the last one are the identity.
+template <class E, int C>
+__device__ __forceinline__ void past_end(float (&al)[L][C], typename VecU<E, C>::t (&v)[L], int nt) {
+#pragma unroll
+    for (int i = 0; i < L; i++)
+        if (i >= nt)
+#pragma unroll
+            for (int c = 0; c < C; c++) al[i][c] = 1.f, v[i][c] = (E)0.f;
+}
+
+// The same value, tested anew: conditions on it that are uniform are not kept
+// as one 64-bit mask each from one pass over the tile to the next.
+template <class T> __device__ __forceinline__ T anew(T x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
+// Rows of a tile, C channels from `ch` of each; rows past the last token read it
+// again (they are not used).  The row bases are uniform, a lane's channel is a
+// 32-bit offset.  Every element is read and written once: non-temporal.
+template <class E, int C>
+__device__ __forceinline__ void load_tile(const E* p, int D, int last, unsigned ch, typename VecU<E, C>::t (&v)[L]) {
+#pragma unroll
+    for (int i = 0; i < L; i++) {
+        v[i] = __builtin_nontemporal_load((const typename VecU<E, C>::t*)gdr::at32(p, ch));
+        p += i < last ? D : 0;
+    }
+}
+template <class E, int C>
+__device__ __forceinline__ void store_nt(E* row, unsigned ch, typename VecU<E, C>::t v) {
+    __builtin_nontemporal_store(v, (typename VecU<E, C>::t*)gdr::at32(row, ch));
+}
+
+template <class E, int C, int W>
+__global__ __launch_bounds__(64 * W, sizeof(E) == 4 ? 4 : 6) void glr_fwd_kernel(GlrArgs a, int nblk, int nseg, bool chain) {
+    static_assert(G <= W, "one wave reads one map of a row");
+    constexpr int SEG = W * L;   // tokens of a segment
+    __shared__ Maps<W, C> mp, ea, eb, qi;
+    __shared__ float tot[2][64 * C];
+    __shared__ unsigned cuts[W], votes[2][W];
+    __shared__ int missing;
+    const Ws ws = carve(a.ws, nseg, a.D);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.D;
+    const int ntok = (int)a.ntok;
+    const Seqs q{a.cu, a.T, a.nseq};
+    const int own = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+    for (int seg = own;;) {
+        const unsigned ch = channel<C>(blk, D);
+        const Tile tile(q, seg * SEG + w * L, ntok);
+        const int t0c = min(tile.t0, ntok - 1), T0 = seg * SEG;
+        const long base = (long)t0c * D;
+        typename VecU<E, C>::t x[L];
+        float al[L][C];
+        {
+            typename VecU<float, C>::t g[L];
+            load_tile<float, C>(a.g + base, D, ntok - 1 - t0c, ch, g);
+            load_tile<E, C>((const E*)a.x + base, D, ntok - 1 - t0c, ch, x);
+#pragma unroll
+            for (int i = 0; i < L; i++)
+#pragma unroll
+                for (int c = 0; c < C; c++) al[i][c] = gate(g[i][c]);
+            if (tile.nt < L) past_end<E, C>(al, x, tile.nt);
+        }
+        float P[C], H[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) P[c] = 1.f, H[c] = 0.f;
+        {
+            int n = tile.n0;
+#pragma unroll
+            for (int i = 0; i < L; i++) {
+                if (tile.begins >> i & 1) {
+                    if (i > 0) n = q.next(n);
+                    seq_row<C>(a.h0, n, D, ch, H);
+                }
+#pragma unroll
+                for (int c = 0; c < C; c++) {
+                    P[c] *= al[i][c];
+                    H[c] = al[i][c] * H[c] + (float)x[i][c];
+                }
+            }
+        }
+        float in[C];   // what enters the segment
+        const bool cut = tiles_before<W, C>(mp, qi, cuts, w, tile.begins != 0, P, H);
+#pragma unroll
+        for (int c = 0; c < C; c++) in[c] = 0.f;
+        bool got = true;
+        if (chain) {
+            const int s0 = q.first(q.of(T0));   // where the sequence that enters began
+            got = exchange<W, C>(ws, seg, nseg, s0 < T0 ? s0 / SEG : seg, D, ch, w, a.polls, cut, P, H, ea, eb, tot, votes,
+                              in);
+        }
+        if (got && tile.nt > 0) {
+            as_loaded<E, C>(x);
+            const unsigned begins = anew(tile.begins);
+            const int nt = anew(tile.nt);
+            enter_tile<W, C>(qi, cut_bits<W>(cuts) & ((1u << w) - 1), w, in);
+            int n = tile.n0;
+            E* out = (E*)a.h + base;
+#pragma unroll
+            for (int i = 0; i < L; i++, out += D) {
+                if (begins >> i & 1) {
+                    if (i > 0) {
+                        if (a.ht) store_row<C>(gdr::at32(a.ht + (long)n * D, ch), in);   // the state that the sequence ends with
+                        n = q.next(n);
+                    }
+                    if (a.ht) pass_empty<C>(q, n, tile.t0 + i, a.h0, a.ht, D, ch);
+                    seq_row<C>(a.h0, n, D, ch, in);
+                }
+                if (i == 0 && a.states) store_row<C>(gdr::at32(a.states + (long)(tile.t0 / L) * D, ch), in);
+                typename VecU<E, C>::t o;
+#pragma unroll
+                for (int c = 0; c < C; c++) {
+                    in[c] = al[i][c] * in[c] + (float)x[i][c];
+                    o[c] = (E)in[c];
+                }
+                if (i < nt) store_nt<E, C>(out, ch, o);
+            }
+            if (a.ht && tile.t0 + tile.nt == q.first(n + 1)) {
+                store_row<C>(gdr::at32(a.ht + (long)n * D, ch), in);
+                if (tile.t0 + tile.nt == ntok) pass_empty<C>(q, a.nseq, ntok, a.h0, a.ht, D, ch);
+            }
+        }
+        if (got && seg == own) return;
+        gdr::lds_barrier();   // what the next pass writes to LDS has been read
+        seg = got ? own : first_missing<C>(ws, own, D, ch, w, missing);
     }
 }
 
 // The segments in the reverse order of time: processing index idx is segment
 // nseg - 1 - idx, tile W - 1 comes first.
-template <class E, int C>
-__global__ __launch_bounds__(64 * W) void glr_bwd_kernel(GlrArgs a, int nblk, int nseg, bool chain) {
-    __shared__ float mp[W][2][64 * C], ep[W][2][64 * C];
-    __shared__ unsigned cuts[W];
-    __shared__ int tick;
+template <class E, int C, int W>
+__global__ __launch_bounds__(64 * W, 4) void glr_bwd_kernel(GlrArgs a, int nblk, int nseg, bool chain) {
+    static_assert(G <= W, "one wave reads one map of a row");
+    constexpr int SEG = W * L;   // tokens of a segment
+    __shared__ Maps<W, C> mp, ea, eb, qi;
+    __shared__ float tot[2][64 * C];
+    __shared__ unsigned cuts[W], votes[2][W];
+    __shared__ int missing;
     const Ws ws = carve(a.ws, nseg, a.D);
-    int idx, blk;
-    take(ws, chain, nblk, &tick, idx, blk);
-    const int seg = nseg - 1 - idx;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, D = a.D;
-    const int ntok = (int)a.ntok, ch = min((blk * 64 + l) * C, D - C);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.D;
+    const int ntok = (int)a.ntok, pw = W - 1 - w;   // pw: the tile's place in processing order
     const Seqs q{a.cu, a.T, a.nseq};
-    const Tile tile(q, seg * SEG + w * L, ntok);
-    const int t0c = min(tile.t0, ntok - 1);
-    const long base = (long)t0c * D + ch;
-    // tokens that end a sequence
-    unsigned ends = 0;
-    if (tile.nt > 0) {
-        ends = tile.begins >> 1;
-        if (q.first(tile.n1 + 1) == tile.t0 + tile.nt) ends |= 1u << (tile.nt - 1);
-    }
-    typename VecU<E, C>::t dh[L];
-    float al[L][C], hp[L][C];   // a_t and h_{t-1}
-    {
-        typename VecU<E, C>::t x[L];
-        typename VecU<float, C>::t g[L];
-        load_tile<float, C>(a.g + base, D, ntok - 1 - t0c, g);
-        load_tile<E, C>((const E*)a.x + base, D, ntok - 1 - t0c, x);
-        load_tile<E, C>((const E*)a.dh + base, D, ntok - 1 - t0c, dh);
-        float h[C];
-        load_row<C>(a.states + (long)(t0c / L) * D + ch, h);
-        int n = tile.n0;
-#pragma unroll
-        for (int i = 0; i < L; i++) {
-            if (i > 0 && (tile.begins >> i & 1)) {
-                n = q.next(n);
-                seq_row<C>(a.h0, n, D, ch, h);
-            }
-#pragma unroll
-            for (int c = 0; c < C; c++) {
-                al[i][c] = i < tile.nt ? expf(g[i][c]) : 1.f;   // past the end: the identity
-                if (i >= tile.nt) dh[i][c] = (E)0.f;
-                hp[i][c] = h[c];
-                h[c] = al[i][c] * h[c] + (float)x[i][c];
-            }
+    const int own = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+    for (int idx = own;;) {
+        const int seg = nseg - 1 - idx;
+        const unsigned ch = channel<C>(blk, D);
+        const Tile tile(q, seg * SEG + w * L, ntok);
+        const int t0c = min(tile.t0, ntok - 1), T1 = min((seg + 1) * SEG, ntok);
+        const long base = (long)t0c * D;
+        unsigned ends = 0;   // tokens that end a sequence
+        if (tile.nt > 0) {
+            ends = tile.begins >> 1;
+            if (q.first(tile.n1 + 1) == tile.t0 + tile.nt) ends |= 1u << (tile.nt - 1);
         }
-    }
-    float P[C], M[C];
+        typename VecU<E, C>::t dh[L];
+        float al[L][C], hp[L][C];   // a_t and h_{t-1}
+        {
+            typename VecU<E, C>::t x[L];
+            typename VecU<float, C>::t g[L];
+            load_tile<float, C>(a.g + base, D, ntok - 1 - t0c, ch, g);
+            load_tile<E, C>((const E*)a.x + base, D, ntok - 1 - t0c, ch, x);
+            load_tile<E, C>((const E*)a.dh + base, D, ntok - 1 - t0c, ch, dh);
+            float h[C];
+            load_row<C>(gdr::at32(a.states + (long)(t0c / L) * D, ch), h);
 #pragma unroll
-    for (int c = 0; c < C; c++) P[c] = 1.f, M[c] = 0.f;
-    {
-        int n = tile.n1;
+            for (int i = 0; i < L; i++)
 #pragma unroll
-        for (int i = L - 1; i >= 0; i--) {
-            if (ends >> i & 1) {
-                if (i + 1 < tile.nt) n = q.prev(n);
-                seq_row<C>(a.dht, n, D, ch, M);
-            }
+                for (int c = 0; c < C; c++) al[i][c] = gate(g[i][c]);
+            if (tile.nt < L) past_end<E, C>(al, dh, tile.nt);
+            int n = tile.n0;
 #pragma unroll
-            for (int c = 0; c < C; c++) {
-                P[c] *= al[i][c];
-                M[c] = al[i][c] * ((float)dh[i][c] + M[c]);
+            for (int i = 0; i < L; i++) {
+                if (i > 0 && (tile.begins >> i & 1)) {
+                    n = q.next(n);
+                    seq_row<C>(a.h0, n, D, ch, h);
+                }
+#pragma unroll
+                for (int c = 0; c < C; c++) {
+                    hp[i][c] = h[c];
+                    h[c] = al[i][c] * h[c] + (float)x[i][c];
+                }
             }
         }
+        float P[C], M[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) P[c] = 1.f, M[c] = 0.f;
+        {
+            int n = tile.n1;
+#pragma unroll
+            for (int i = L - 1; i >= 0; i--) {
+                if (ends >> i & 1) {
+                    if (i + 1 < tile.nt) n = q.prev(n);
+                    seq_row<C>(a.dht, n, D, ch, M);
+                }
+#pragma unroll
+                for (int c = 0; c < C; c++) {
+                    P[c] *= al[i][c];
+                    M[c] = al[i][c] * ((float)dh[i][c] + M[c]);
+                }
+            }
+        }
+        float in[C];
+        const bool cut = tiles_before<W, C>(mp, qi, cuts, pw, ends != 0, P, M);
+#pragma unroll
+        for (int c = 0; c < C; c++) in[c] = 0.f;
+        bool got = true;
+        if (chain) {
+            const int e0 = q.first(q.of(T1 - 1) + 1);   // where the sequence that enters from the right ends
+            got = exchange<W, C>(ws, idx, nseg, e0 > T1 ? nseg - 1 - (e0 - 1) / SEG : idx, D, ch, pw, a.polls, cut, P, M, ea,
+                              eb, tot, votes, in);
+        }
+        if (got && tile.nt > 0) {
+            as_loaded<E, C>(dh);
+            const unsigned begins = anew(tile.begins), end = anew(ends);
+            const int nt = anew(tile.nt);
+            enter_tile<W, C>(qi, cut_bits<W>(cuts) & ((1u << pw) - 1), pw, in);
+            int n = tile.n1;
+            E* dx = (E*)a.dx + base + (long)(L - 1) * D;
+            float* dgr = a.dg + base + (long)(L - 1) * D;
+#pragma unroll
+            for (int i = L - 1; i >= 0; i--, dx -= D, dgr -= D) {
+                if (end >> i & 1) {
+                    if (i + 1 < nt) n = q.prev(n);
+                    seq_row<C>(a.dht, n, D, ch, in);
+                }
+                typename VecU<E, C>::t o;
+                typename VecU<float, C>::t dg;
+#pragma unroll
+                for (int c = 0; c < C; c++) {
+                    const float lam = (float)dh[i][c] + in[c];
+                    in[c] = al[i][c] * lam;
+                    o[c] = (E)lam;
+                    dg[c] = in[c] * hp[i][c];
+                }
+                if (i < nt) {
+                    store_nt<E, C>(dx, ch, o);
+                    store_nt<float, C>(dgr, ch, dg);
+                }
+                if (a.dh0 && (begins >> i & 1)) {
+                    store_row<C>(gdr::at32(a.dh0 + (long)n * D, ch), in);
+                    pass_empty<C>(q, n, tile.t0 + i, a.dht, a.dh0, D, ch);
+                }
+            }
+            if (a.dh0 && tile.t0 + tile.nt == ntok) pass_empty<C>(q, a.nseq, ntok, a.dht, a.dh0, D, ch);
+        }
+        if (got && idx == own) return;
+        gdr::lds_barrier();   // what the next pass writes to LDS has been read
+        idx = got ? own : first_missing<C>(ws, own, D, ch, w, missing);
     }
-    const int pw = W - 1 - w;   // the tile's place in processing order
-#pragma unroll
-    for (int c = 0; c < C; c++) mp[pw][0][l * C + c] = P[c], mp[pw][1][l * C + c] = M[c];
-    if (l == 0) cuts[pw] = ends != 0;
-    __syncthreads();
-    unsigned cut = 0;
-#pragma unroll
-    for (int v = 0; v < W; v++) cut |= cuts[v] << v;
-    cut = __builtin_amdgcn_readfirstlane(cut);
-    float in[C];
-#pragma unroll
-    for (int c = 0; c < C; c++) in[c] = 0.f;
-    const int T1 = min((seg + 1) * SEG, ntok);
-    if (chain) {
-        if (w == 0 && seg > 0) {
-#pragma unroll
-            for (int c = 0; c < C; c++) P[c] = 1.f, M[c] = 0.f;
-            through_tiles<C>(mp, cut, 0, W, P, M);
-#pragma unroll
-            for (int c = 0; c < C; c++) publish(ws.map + (size_t)idx * D + ch + c, P[c], M[c]);
-            asm volatile("" ::: "memory");   // published before anything is waited for
-        }
-        const int e0 = q.first(q.of(T1 - 1) + 1);   // where the sequence that enters from the right ends
-        if (e0 > T1) enter_segment<C>(ws, idx, nseg - 1 - (e0 - 1) / SEG, D, ch, ep, in);
-        if (w == 0 && idx % G == G - 1 && seg > 0) {
-            float p1[C], out[C];
-#pragma unroll
-            for (int c = 0; c < C; c++) p1[c] = 1.f, out[c] = in[c];
-            through_tiles<C>(mp, cut, 0, W, p1, out);
-#pragma unroll
-            for (int c = 0; c < C; c++) publish(ws.state + (size_t)(idx / G) * D + ch + c, out[c]);
-        }
-    }
-    if (tile.nt == 0) return;
-#pragma unroll
-    for (int c = 0; c < C; c++) P[c] = 1.f;
-    through_tiles<C>(mp, cut, 0, pw, P, in);
-    int n = tile.n1;
-#pragma unroll
-    for (int i = L - 1; i >= 0; i--) {
-        if (ends >> i & 1) {
-            if (i + 1 < tile.nt) n = q.prev(n);
-            seq_row<C>(a.dht, n, D, ch, in);
-        }
-        typename VecU<E, C>::t o;
-        float dg[C];
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-            const float lam = (float)dh[i][c] + in[c];
-            in[c] = al[i][c] * lam;
-            o[c] = (E)lam;
-            dg[c] = in[c] * hp[i][c];
-        }
-        if (i < tile.nt) {
-            *(typename VecU<E, C>::t*)((E*)a.dx + base + (unsigned)i * (unsigned)D) = o;
-            store_row<C>(a.dg + base + (unsigned)i * (unsigned)D, dg);
-        }
-        if (a.dh0 && (tile.begins >> i & 1)) {
-            store_row<C>(a.dh0 + (long)n * D + ch, in);
-            pass_empty<C>(q, n, tile.t0 + i, a.dht, a.dh0, D, ch);
-        }
-    }
-    if (a.dh0 && tile.t0 + tile.nt == ntok) pass_empty<C>(q, a.nseq, ntok, a.dht, a.dh0, D, ch);
 }
 
 __global__ __launch_bounds__(256) void glr_clear_kernel(uint4* p, size_t n) {
@@ -515,35 +646,47 @@ __global__ __launch_bounds__(256) void glr_pass_kernel(const float* in, float* o
     if (i < n) out[i] = in ? in[i] : 0.f;
 }
 
-int segments(const GlrArgs& a) { return (int)((a.ntok + SEG - 1) / SEG); }
-// Whether a segment may begin inside a sequence.
-bool chained(const GlrArgs& a) { return segments(a) > 1 && (a.cu || SEG % a.T != 0); }
+constexpr int CH = 2;   // channels of a lane
+// Tiles of a segment.  More of them make fewer segments wait for one another, but
+// a workgroup needs its waves at once: two workgroups of 12 waves fill what the
+// forward's 80 registers a lane leave (fp32 x takes 16 more: 8 waves), two of 8
+// the backward's 116.
+constexpr int WF = 12, WF32 = 8, WB = 8;
+int tiles_of(const GlrArgs& a, bool bwd) { return bwd ? WB : a.dtype == GDR_F32 ? WF32 : WF; }
+
+int segments(const GlrArgs& a, int w) { return (int)((a.ntok + w * L - 1) / (w * L)); }
+int blocks(const GlrArgs& a) {
+    const int c = 64 * (a.D >= CH ? CH : 1);
+    return (a.D + c - 1) / c;
+}
+// Whether a segment of w tiles may begin inside a sequence.
+bool chained(const GlrArgs& a, int w) { return segments(a, w) > 1 && (a.cu || w * L % a.T != 0); }
+size_t ws_of(const GlrArgs& a, int w) {
+    return chained(a, w) ? (ws_bytes(segments(a, w), a.D) + 15) & ~(size_t)15 : 0;
+}
 
 hipError_t pass(const GlrArgs& a, const float* in, float* out, hipStream_t s) {
     const size_t n = (size_t)a.nseq * a.D;
     hipLaunchKernelGGL(glr_pass_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, in, out, n);
     return hipGetLastError();
 }
-hipError_t clear(const GlrArgs& a, hipStream_t s) {
-    const size_t n = glr_ws_bytes(a) / 16;
-    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (uint4*)a.ws, n);
-    return hipGetLastError();
-}
 
 template <class E, int C> hipError_t run(const GlrArgs& a, bool bwd, hipStream_t s) {
-    const bool chain = chained(a);
+    const int w = tiles_of(a, bwd), nseg = segments(a, w), nblk = blocks(a);
+    const bool chain = chained(a, w);
     if (chain) {
-        const hipError_t e = clear(a, s);
+        const size_t n = ws_of(a, w) / 16;
+        hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (uint4*)a.ws, n);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const int nseg = segments(a), nblk = (a.D + 64 * C - 1) / (64 * C);
-    const dim3 grid((unsigned)nseg * nblk), blk(64 * W);
-    if (bwd) hipLaunchKernelGGL((glr_bwd_kernel<E, C>), grid, blk, 0, s, a, nblk, nseg, chain);
-    else hipLaunchKernelGGL((glr_fwd_kernel<E, C>), grid, blk, 0, s, a, nblk, nseg, chain);
+    const dim3 grid((unsigned)nseg * nblk), blk(64 * w);
+    if (bwd) hipLaunchKernelGGL((glr_bwd_kernel<E, C, WB>), grid, blk, 0, s, a, nblk, nseg, chain);
+    else hipLaunchKernelGGL((glr_fwd_kernel<E, C, sizeof(E) == 4 ? WF32 : WF>), grid, blk, 0, s, a, nblk, nseg, chain);
     return hipGetLastError();
 }
 template <class E> hipError_t by_width(const GlrArgs& a, bool bwd, hipStream_t s) {
-    return a.D >= 4 ? run<E, 4>(a, bwd, s) : run<E, 1>(a, bwd, s);
+    return a.D >= CH ? run<E, CH>(a, bwd, s) : run<E, 1>(a, bwd, s);
 }
 hipError_t by_type(const GlrArgs& a, bool bwd, hipStream_t s) {
     switch (a.dtype) {
@@ -555,16 +698,16 @@ hipError_t by_type(const GlrArgs& a, bool bwd, hipStream_t s) {
 
 }  // namespace
 
-long glr_workgroups(const GlrArgs& a) {
-    const int c = a.D >= 4 ? 4 : 1;
-    return (long)segments(a) * ((a.D + 64 * c - 1) / (64 * c));
+long glr_threads(const GlrArgs& a) {
+    const int wf = tiles_of(a, false), wb = tiles_of(a, true);
+    const long f = (long)segments(a, wf) * wf, b = (long)segments(a, wb) * wb;
+    return 64 * (f > b ? f : b) * blocks(a);
 }
 
 size_t glr_ws_bytes(const GlrArgs& a) {
-    if (a.ntok == 0 || !chained(a)) return 0;
-    const int nseg = segments(a);
-    const size_t b = WS_HEAD + (size_t)nseg * a.D * 8 + (size_t)((nseg + G - 1) / G) * a.D * 4;
-    return (b + 15) & ~(size_t)15;
+    if (a.ntok == 0) return 0;
+    const size_t f = ws_of(a, tiles_of(a, false)), b = ws_of(a, tiles_of(a, true));
+    return f > b ? f : b;
 }
 
 hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s) {

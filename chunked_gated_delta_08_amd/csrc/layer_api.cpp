@@ -83,8 +83,10 @@ int check_glr(const glr_problem* p, layer::GlrArgs* a) {
     if (n > (1 << 30) || p->D > (1 << 20)) return GDR_ERR_UNSUPPORTED;
     *a = layer::GlrArgs{};
     a->ntok = (long)n; a->nseq = (int)nseq; a->T = p->T; a->D = p->D; a->dtype = p->dtype; a->cu = p->cu_seqlens;
-    // a launch has fewer than 2^32 threads: 512 in a workgroup, 256 in those that copy states of empty batches
-    if (layer::glr_workgroups(*a) >= (1 << 23) || (n == 0 && nseq * p->D >= (int64_t)1 << 32)) return GDR_ERR_UNSUPPORTED;
+    a->polls = p->polls > 0 ? p->polls : 4096;
+    // a launch has fewer than 2^32 threads
+    if (layer::glr_threads(*a) >= (int64_t)1 << 32 || (n == 0 && nseq * p->D >= (int64_t)1 << 31))
+        return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
 

@@ -34,6 +34,7 @@ struct GlrArgs {
     long ntok;                 // tokens of the flattened axis
     int nseq, T;               // sequences; dense length
     int D, dtype;
+    int polls;                 // tries before a workgroup takes up what it waits for
     const int32_t* cu;         // device cu_seqlens or NULL
     const void* x; const float* g; const float* h0;
     void* h; float* ht; float* states;            // forward outputs; backward reads states
@@ -41,7 +42,7 @@ struct GlrArgs {
     void* ws;
 };
 size_t glr_ws_bytes(const GlrArgs& a);
-long glr_workgroups(const GlrArgs& a);
+long glr_threads(const GlrArgs& a);   // of the larger launch
 hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t s);
 

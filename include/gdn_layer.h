@@ -104,6 +104,9 @@ typedef struct glr_problem {
     const int32_t *cu_seqlens_host; /* host mirror of cu_seqlens [N+1]; required iff cu_seqlens != NULL.
                                        It must hold the same values; it is read during the call only. */
     gdr_dtype dtype;                /* type of x, h, dh, dx */
+    int polls;                      /* how often a workgroup looks for the results of earlier ones before it
+                                       computes them itself; <= 0 selects the default.  Results are the same
+                                       for every value. */
 } glr_problem;
 
 /* Rows of `states`: one for every GLR_TILE tokens of the flattened axis; -1 if invalid. */

@@ -17,6 +17,7 @@ pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
 NORM_OPS = 64
+GATE0 = 2.0 ** -126
 EPS = 1e-5
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 TINY = {"bf16": 1e-38, "f16": 2.0 ** -25, "f32": 1e-38}   # half the smallest step of the type
@@ -260,11 +261,12 @@ def test_add_norm_many_rows_in_place_no_rows(B):
 def glr_ref(x, g, h0, lens, dh=None, dht=None):
     """The recurrence token by token, next to a bound on each value's error.
 
-    Every token adds at most 8 u of |a| H + |x|, H the recurrence of the magnitudes:
-    2 u for exp, 1 u each for the product and the sum, the rest for the products and
-    sums of the same factors that joining pieces of a sequence takes."""
+    Every token adds at most (8 + |g|) u of |a| H + |x|, H the recurrence of the
+    magnitudes: |g| + 3 for the gate, 1 each for the product and the sum, the rest for the
+    products and sums of the same factors that joining pieces of a sequence takes."""
     x, g, h0, dh, dht = (f64(t) for t in (x, g, h0, dh, dht))
     a = g.exp()
+    gm = torch.where(torch.isfinite(g), g.abs(), 0.0)   # an infinite gate is exactly zero
     n, D = len(lens), x.shape[1]
     out = {k: torch.zeros_like(x) for k in ("h", "hp", "H", "Hp", "E", "Ep", "lam", "La", "Le")}
     ht, hte = torch.zeros(n, D, dtype=torch.float64), torch.zeros(n, D, dtype=torch.float64)
@@ -275,8 +277,9 @@ def glr_ref(x, g, h0, lens, dh=None, dht=None):
         for t in range(t, t + m):
             out["hp"][t], out["Hp"][t], out["Ep"][t] = h, H, E
             h = a[t] * h + x[t]
+            E = a[t] * E + GATE0 * H
             H = a[t] * H + x[t].abs()
-            E = a[t] * E + 8 * U * H
+            E = E + (8 + gm[t]) * U * H
             out["h"][t], out["H"][t], out["E"][t] = h, H, E
         t = sum(lens[:i + 1])
         ht[i], hte[i] = h, E
@@ -292,15 +295,16 @@ def glr_ref(x, g, h0, lens, dh=None, dht=None):
                 lam, LA = dh[t] + mu, dh[t].abs() + M
                 le = E + 8 * U * LA
                 out["lam"][t], out["La"][t], out["Le"][t] = lam, LA, le
-                mu, M, E = a[t] * lam, a[t] * LA, a[t] * le + 4 * U * a[t] * LA
+                mu, M, E = a[t] * lam, a[t] * LA, a[t] * le + ((5 + gm[t]) * U * a[t] + GATE0) * LA
             dh0[i], dh0e[i] = mu, E
         ref.update(dx=out["lam"], dg=out["lam"] * a * out["hp"], dh0=dh0)
         err.update(dx=out["Le"], dh0=dh0e + 1e-38,
-                   dg=a * (out["La"] * out["Ep"] + out["Hp"] * out["Le"] + 8 * U * out["La"] * out["Hp"]) + 1e-38)
+                   dg=a * (out["La"] * out["Ep"] + out["Hp"] * out["Le"] + (8 + gm) * U * out["La"] * out["Hp"]) +
+                   GATE0 * out["La"] * out["Hp"] + 1e-38)
     return ref, err
 
 
-GLR_LENS = [[1], [2], [15], [16], [17], [63, 1], [127], [128], [129], [300], [1025], [5, 0, 1, 16, 33, 0, 200],
+GLR_LENS = [[1], [4500], [33, 2500, 1, 4100], [2], [15], [16], [17], [63, 1], [127], [128], [129], [300], [1025], [5, 0, 1, 16, 33, 0, 200],
             [0, 0, 40, 0], [1] * 37, [64] * 3, [100] * 5, [0], [0, 0]]
 
 
@@ -344,6 +348,24 @@ def test_glr_long(B):
     f2 = B.glr_fwd(x.cuda(), g.cuda(), want_states=True, **kw)
     b2 = B.glr_bwd(x.cuda(), g.cuda(), dh.cuda(), f2["states"], dht=dht.cuda(), **kw)
     assert all(torch.equal(f[k], f2[k]) for k in f) and all(torch.equal(b[k], b2[k]) for k in b)
+
+
+@pytest.mark.parametrize("lens,D", [([3000], 130), ([700, 1, 0, 1500, 40], 64), ([9000], 2)])
+def test_glr_without_patience(B, lens, D):
+    """Workgroups that hardly look for the others' results before they compute them themselves give the same bits."""
+    T, N = sum(lens), len(lens)
+    x, g, dh, h0, dht = (t.cuda() for t in (rnd(1, T, D).bfloat16(), -torch.exp(rnd(2, T, D) - 4), rnd(3, T, D).bfloat16(),
+                                            rnd(4, N, D), rnd(5, N, D)))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+    kw = dict(h0=h0, cu_seqlens=cu.cuda(), cu_seqlens_host=cu)
+
+    def both(polls):
+        f = B.glr_fwd(x, g, want_states=True, polls=polls, **kw)
+        return {**f, **B.glr_bwd(x, g, dh, f["states"], dht=dht, polls=polls, **kw)}
+    want = both(0)
+    for polls in (1, 2, 20):
+        got = both(polls)
+        assert all(torch.equal(got[k], want[k]) for k in want), polls
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])

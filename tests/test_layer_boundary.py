@@ -123,7 +123,7 @@ def test_norm_no_rows_needs_no_launch(B):
 
 
 def glr(B, Bb=1, T=100, D=8, dtype=2, cu=None, N=None, host=True):
-    p = B.GlrProblem(Bb, T, D, 0, None, None, dtype)
+    p = B.GlrProblem(Bb, T, D, 0, None, None, dtype, 0)
     keep = None
     if cu is not None:
         keep = (ctypes.c_int32 * len(cu))(*cu)
