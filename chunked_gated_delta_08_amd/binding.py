@@ -12,6 +12,7 @@ Layouts (token axis flattened over the batch, as in include/gdr.h):
   h0, dht, dh0 [N, HV, K, V] fp32
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -530,28 +531,36 @@ lib.gdr_step.argtypes = [_i] * 5 + [_i64, _f, _i] + [_vp] * 9
 
 
 def _same_device(first, *others):
+    dev = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
 
 
-def _launch(dev, stream, temps, call):
-    """call(stream handle) with `dev` current.  `temps`: tensors allocated for this
+# the current stream's handle, without the Stream object around it where torch offers that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(dev, stream, temps, call, *args):
+    """call(*args, stream handle) with `dev` current.  `temps`: tensors allocated for this
     call on the current stream; the allocator is told when another one uses them."""
-    current = torch.cuda.current_stream(dev)
-    if stream is None:
-        stream = current
-    elif stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    elif stream != current:
-        for t in temps:
-            if t is not None:
-                t.record_stream(stream)
+    handle = _current_stream(dev.index)
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        if stream.cuda_stream != handle:
+            for t in temps:
+                if t is not None:
+                    t.record_stream(stream)
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        _check(call(stream.cuda_stream))
+        code = call(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(call(stream.cuda_stream))
+            code = call(*args, handle)
+    if code != 0:
+        _check(code)
 
 
 def _p(t):
@@ -574,32 +583,45 @@ def check_gated_norm_args(x, z, w, dy=None, act="silu", need_dy=False, cuda=True
     _same_device(x, z, w, dy)
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_sizes(rows, D, eps, dtype, res_dtype, act):
+    """The struct of these sizes (calls only read it) and the workspace it needs."""
+    p = NormProblem(rows, D, eps, _DT[dtype], _DT[res_dtype], ACTS[act])
+    return p, int(lib.norm_workspace_size(ctypes.byref(p)))
+
+
 def _norm_problem(x, eps, res_dtype=None, act="silu"):
     D = x.shape[-1]
-    return NormProblem(x.numel() // D if D else 0, D, eps, _DT[x.dtype], _DT[res_dtype or x.dtype], ACTS[act])
+    return _norm_sizes(x.numel() // D if D else 0, D, eps, x.dtype, res_dtype or x.dtype, act)
 
 
 def norm_workspace_size(rows, D, dtype):
     """Bytes of workspace gated_norm_bwd and add_norm_bwd need."""
-    return int(lib.norm_workspace_size(ctypes.byref(NormProblem(rows, D, 0.0, _DT[dtype], _DT[dtype], 0))))
+    return _norm_sizes(rows, D, 0.0, dtype, dtype, "silu")[1]
 
 
-def _norm_workspace(p, workspace, dev):
+def _workspace(workspace, size, dev):
+    """(the workspace, the tensor allocated for it or None); no workspace for a size of 0."""
     if workspace is None:
-        return torch.empty(int(lib.norm_workspace_size(ctypes.byref(p))), dtype=torch.uint8, device=dev)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        return ws, ws
     _need(workspace, "workspace", torch.uint8)
-    return workspace
+    if workspace.device != dev:
+        raise ValueError(f"workspace on {workspace.device}, the tensors on {dev}")
+    return workspace, None
 
 
 def gated_norm_fwd(x, z, w, eps=1e-5, act="silu", out=None, stream=None):
     """y = x rsqrt(mean(x^2) + eps) w act(z) over the last axis; z None: no gate."""
     check_gated_norm_args(x, z, w, act=act)
-    y = torch.empty_like(x) if out is None else out
-    _need(y, "out", x.dtype, x.shape)
-    _same_device(x, y)
-    p = _norm_problem(x, eps, act=act)
-    _launch(x.device, stream, (y,) if out is None else (),
-            lambda s: lib.gated_norm_fwd(ctypes.byref(p), _p(x), _p(z), _p(w), _p(y), s))
+    if out is None:
+        y = torch.empty_like(x)
+    else:
+        y = out
+        _need(y, "out", x.dtype, x.shape)
+        _same_device(x, y)
+    p, _ = _norm_problem(x, eps, act=act)
+    _launch(x.device, stream, (y,) if out is None else (), lib.gated_norm_fwd, p, _p(x), _p(z), _p(w), _p(y))
     return y
 
 
@@ -609,19 +631,18 @@ def gated_norm_bwd(x, z, w, dy, eps=1e-5, act="silu", out=None, workspace=None, 
     own = []
     if out is None:
         out = {"dx": torch.empty_like(x), "dz": None if z is None else torch.empty_like(z), "dw": torch.empty_like(w)}
-        own += list(out.values())
-    _need(out["dx"], "dx", x.dtype, x.shape)
-    _need(out["dw"], "dw", torch.float32, w.shape)
-    if z is not None:
-        _need(out["dz"], "dz", x.dtype, x.shape)
+        own += out.values()
+    else:
+        _need(out["dx"], "dx", x.dtype, x.shape)
+        _need(out["dw"], "dw", torch.float32, w.shape)
+        _need(out["dz"], "dz", x.dtype, x.shape, optional=z is None)
+        _same_device(x, *out.values())
     dz = None if z is None else out["dz"]
-    p = _norm_problem(x, eps, act=act)
-    ws = _norm_workspace(p, workspace, x.device)
-    own += [ws] if workspace is None else []
-    _same_device(x, out["dx"], dz, out["dw"], ws)
-    _launch(x.device, stream, own,
-            lambda s: lib.gated_norm_bwd(ctypes.byref(p), _p(x), _p(z), _p(w), _p(dy), _p(out["dx"]), _p(dz),
-                                         _p(out["dw"]), _p(ws), ws.numel(), s))
+    p, size = _norm_problem(x, eps, act=act)
+    ws, mine = _workspace(workspace, size, x.device)
+    own.append(mine)
+    _launch(x.device, stream, own, lib.gated_norm_bwd, p, _p(x), _p(z), _p(w), _p(dy), _p(out["dx"]), _p(dz),
+            _p(out["dw"]), _p(ws), ws.numel())
     return out
 
 
@@ -644,16 +665,16 @@ def add_norm_fwd(x, res, w, scale=None, eps=1e-5, out=None, stream=None):
     """res' = res + scale x and y = RMSNorm(res') w.  Returns dict y (x's dtype), res
     (res's dtype).  out={"y": ..., "res": res} updates the residual stream in place."""
     check_add_norm_args(x, res, w, scale)
-    own = out is None
-    if own:
+    own = ()
+    if out is None:
         out = {"y": torch.empty_like(x), "res": torch.empty_like(res)}
-    _need(out["y"], "y", x.dtype, x.shape)
-    _need(out["res"], "res", res.dtype, x.shape)
-    _same_device(x, out["y"], out["res"])
-    p = _norm_problem(x, eps, res.dtype)
-    _launch(x.device, stream, out.values() if own else (),
-            lambda s: lib.add_norm_fwd(ctypes.byref(p), _p(x), _p(res), _p(w), _p(scale), _p(out["y"]),
-                                       _p(out["res"]), s))
+        own = out.values()
+    else:
+        _need(out["y"], "y", x.dtype, x.shape)
+        _need(out["res"], "res", res.dtype, x.shape)
+        _same_device(x, *out.values())
+    p, _ = _norm_problem(x, eps, res.dtype)
+    _launch(x.device, stream, own, lib.add_norm_fwd, p, _p(x), _p(res), _p(w), _p(scale), _p(out["y"]), _p(out["res"]))
     return out
 
 
@@ -673,26 +694,24 @@ def add_norm_bwd(dy, dres, res, w, x=None, scale=None, eps=1e-5, out=None, works
     scale).  Without scale and in one dtype, dx is dres, the same tensor."""
     check_add_norm_bwd_args(dy, dres, res, w, x, scale)
     own = []
-    one = scale is None and dy.dtype == res.dtype
     if out is None:
         d = torch.empty_like(res)
-        out = {"dx": d if one else torch.empty_like(dy), "dres": d, "dw": torch.empty_like(w),
-               "dscale": None if scale is None else torch.empty_like(scale)}
-        own += list(out.values())
-    _need(out["dres"], "dres", res.dtype, res.shape)
-    _need(out["dx"], "dx", dy.dtype, dy.shape)
-    _need(out["dw"], "dw", torch.float32, w.shape)
-    if scale is not None:
-        _need(out["dscale"], "dscale", torch.float32, w.shape)
-    dx = None if out["dx"] is out["dres"] else out["dx"]
+        out = {"dx": d if scale is None and dy.dtype == res.dtype else torch.empty_like(dy), "dres": d,
+               "dw": torch.empty_like(w), "dscale": None if scale is None else torch.empty_like(scale)}
+        own += out.values()
+    else:
+        _need(out["dres"], "dres", res.dtype, res.shape)
+        _need(out["dx"], "dx", dy.dtype, dy.shape)
+        _need(out["dw"], "dw", torch.float32, w.shape)
+        _need(out["dscale"], "dscale", torch.float32, w.shape, optional=scale is None)
+        _same_device(dy, *out.values())
+    dx = None if scale is None and out["dx"] is out["dres"] else out["dx"]
     ds = None if scale is None else out["dscale"]
-    p = _norm_problem(dy, eps, res.dtype)
-    ws = _norm_workspace(p, workspace, dy.device)
-    own += [ws] if workspace is None else []
-    _same_device(dy, out["dres"], out["dx"], out["dw"], ds, ws)
-    _launch(dy.device, stream, own,
-            lambda s: lib.add_norm_bwd(ctypes.byref(p), _p(dy), _p(dres), _p(res), _p(w), _p(x), _p(scale), _p(dx),
-                                       _p(out["dres"]), _p(out["dw"]), _p(ds), _p(ws), ws.numel(), s))
+    p, size = _norm_problem(dy, eps, res.dtype)
+    ws, mine = _workspace(workspace, size, dy.device)
+    own.append(mine)
+    _launch(dy.device, stream, own, lib.add_norm_bwd, p, _p(dy), _p(dres), _p(res), _p(w), _p(x), _p(scale), _p(dx),
+            _p(out["dres"]), _p(out["dw"]), _p(ds), _p(ws), ws.numel())
     return out
 
 
@@ -727,28 +746,37 @@ def check_glr_args(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, dh
     return N
 
 
+@functools.lru_cache(maxsize=1024)
+def _glr_sizes(B, T, D, dtype, polls):
+    """The struct of these dense sizes (calls only read it) and the workspace it needs."""
+    p = GlrProblem(B, T, D, 0, None, None, _DT[dtype], polls)
+    return p, int(lib.glr_workspace_size(ctypes.byref(p)))
+
+
 def _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls=0):
-    """The problem struct and what has to outlive its use.  Without a host mirror
-    cu_seqlens is copied to the host, which waits for the current stream."""
+    """The problem struct, the workspace it needs and what has to outlive its use.
+    Without a host mirror cu_seqlens is copied to the host, which waits for the
+    current stream."""
     ntok, D = x.shape
     if cu_seqlens is None:
-        return GlrProblem(B, ntok // B, D, 0, None, None, _DT[x.dtype], polls), None
+        return (*_glr_sizes(B, ntok // B, D, x.dtype, polls), None)
     host = cu_seqlens.detach().cpu() if cu_seqlens_host is None else cu_seqlens_host
-    return GlrProblem(1, ntok, D, host.numel() - 1, cu_seqlens.data_ptr(), host.data_ptr(), _DT[x.dtype],
-                      polls), host
+    p = GlrProblem(1, ntok, D, host.numel() - 1, cu_seqlens.data_ptr(), host.data_ptr(), _DT[x.dtype], polls)
+    return p, int(lib.glr_workspace_size(ctypes.byref(p))), host
+
+
+def glr_workspace_size(ntok, D, dtype, cu_seqlens_host=None, B=1):
+    """Bytes of workspace glr_fwd and glr_bwd need."""
+    if cu_seqlens_host is None:
+        return _glr_sizes(B, ntok // B, D, dtype, 0)[1]
+    host = cu_seqlens_host
+    p = GlrProblem(1, ntok, D, host.numel() - 1, host.data_ptr(), host.data_ptr(), _DT[dtype], 0)
+    return int(lib.glr_workspace_size(ctypes.byref(p)))
 
 
 def glr_num_states(ntok):
     """Rows of glr_fwd's `states` for ntok = B*T tokens."""
     return -(-ntok // GLR_TILE)
-
-
-def _glr_workspace(p, workspace, dev):
-    if workspace is None:
-        n = int(lib.glr_workspace_size(ctypes.byref(p)))
-        return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    _need(workspace, "workspace", torch.uint8)
-    return workspace
 
 
 def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=True, want_states=False, out=None,
@@ -765,17 +793,17 @@ def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=T
                "ht": torch.empty((N, D), dtype=torch.float32, device=dev) if want_ht else None,
                "states": torch.empty((glr_num_states(ntok), D), dtype=torch.float32, device=dev) if want_states
                else None}
-        own += list(out.values())
-    _need(out["h"], "h", x.dtype, x.shape)
-    _need(out["ht"], "ht", torch.float32, (N, D), optional=True)
-    _need(out["states"], "states", torch.float32, (glr_num_states(ntok), D), optional=True)
-    p, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
-    ws = _glr_workspace(p, workspace, dev)
-    own += [ws] if workspace is None else []
-    _same_device(x, *out.values(), ws)
-    _launch(dev, stream, own,
-            lambda s: lib.glr_fwd(ctypes.byref(p), _p(x), _p(g), _p(h0), _p(out["h"]), _p(out["ht"]),
-                                  _p(out["states"]), _p(ws), 0 if ws is None else ws.numel(), s))
+        own += out.values()
+    else:
+        _need(out["h"], "h", x.dtype, x.shape)
+        _need(out["ht"], "ht", torch.float32, (N, D), optional=True)
+        _need(out["states"], "states", torch.float32, (glr_num_states(ntok), D), optional=True)
+        _same_device(x, *out.values())
+    p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
+    ws, mine = _workspace(workspace, size, dev)
+    own.append(mine)
+    _launch(dev, stream, own, lib.glr_fwd, p, _p(x), _p(g), _p(h0), _p(out["h"]), _p(out["ht"]), _p(out["states"]),
+            _p(ws), 0 if ws is None else ws.numel())
     del keep
     return out
 
@@ -790,17 +818,17 @@ def glr_bwd(x, g, dh, states, dht=None, h0=None, cu_seqlens=None, cu_seqlens_hos
     if out is None:
         out = {"dx": torch.empty_like(x), "dg": torch.empty_like(g),
                "dh0": torch.empty((N, D), dtype=torch.float32, device=dev) if want_dh0 else None}
-        own += list(out.values())
-    _need(out["dx"], "dx", x.dtype, x.shape)
-    _need(out["dg"], "dg", torch.float32, x.shape)
-    _need(out["dh0"], "dh0", torch.float32, (N, D), optional=True)
-    p, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
-    ws = _glr_workspace(p, workspace, dev)
-    own += [ws] if workspace is None else []
-    _same_device(x, *out.values(), ws)
-    _launch(dev, stream, own,
-            lambda s: lib.glr_bwd(ctypes.byref(p), _p(x), _p(g), _p(h0), _p(states), _p(dh), _p(dht), _p(out["dx"]),
-                                  _p(out["dg"]), _p(out["dh0"]), _p(ws), 0 if ws is None else ws.numel(), s))
+        own += out.values()
+    else:
+        _need(out["dx"], "dx", x.dtype, x.shape)
+        _need(out["dg"], "dg", torch.float32, x.shape)
+        _need(out["dh0"], "dh0", torch.float32, (N, D), optional=True)
+        _same_device(x, *out.values())
+    p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
+    ws, mine = _workspace(workspace, size, dev)
+    own.append(mine)
+    _launch(dev, stream, own, lib.glr_bwd, p, _p(x), _p(g), _p(h0), _p(states), _p(dh), _p(dht), _p(out["dx"]),
+            _p(out["dg"]), _p(out["dh0"]), _p(ws), 0 if ws is None else ws.numel())
     del keep
     return out
 
@@ -831,12 +859,14 @@ def glr_step(x, g, state, slots=None, out=None, stream=None):
     in place.  A row whose slot is outside the pool is padding (its h is zero); rows of
     one slot are successive tokens.  Returns h [N, D] (x's dtype)."""
     check_glr_step_args(x, g, state, slots)
-    h = torch.empty_like(x) if out is None else out
-    _need(h, "out", x.dtype, x.shape)
-    _same_device(x, h)
-    _launch(x.device, stream, (h,) if out is None else (),
-            lambda s: lib.glr_step(x.shape[0], x.shape[1], state.shape[0], _DT[x.dtype], _p(x), _p(g), _p(slots),
-                                   _p(state), _p(h), s))
+    if out is None:
+        h = torch.empty_like(x)
+    else:
+        h = out
+        _need(h, "out", x.dtype, x.shape)
+        _same_device(x, h)
+    _launch(x.device, stream, (h,) if out is None else (), lib.glr_step, x.shape[0], x.shape[1], state.shape[0],
+            _DT[x.dtype], _p(x), _p(g), _p(slots), _p(state), _p(h))
     return h
 
 
@@ -865,11 +895,13 @@ def gdr_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, stream=N
     [slots, HV, K, V], as gdr_chunk_fwd's ht), updated in place; g is the token's raw
     log-gate.  Slots as for glr_step.  Returns o [N, HV, V] (v's dtype)."""
     check_gdr_step_args(q, k, v, g, beta, state, slots)
-    o = torch.empty_like(v) if out is None else out
-    _need(o, "out", v.dtype, v.shape)
-    _same_device(v, o)
+    if out is None:
+        o = torch.empty_like(v)
+    else:
+        o = out
+        _need(o, "out", v.dtype, v.shape)
+        _same_device(v, o)
     (N, HK, K), (_, HV, V) = k.shape, v.shape
-    _launch(v.device, stream, (o,) if out is None else (),
-            lambda s: lib.gdr_step(N, HK, HV, K, V, state.shape[0], scale or 0.0, _DT[v.dtype], _p(q), _p(k), _p(v),
-                                   _p(g), _p(beta), _p(slots), _p(state), _p(o), s))
+    _launch(v.device, stream, (o,) if out is None else (), lib.gdr_step, N, HK, HV, K, V, state.shape[0], scale or 0.0,
+            _DT[v.dtype], _p(q), _p(k), _p(v), _p(g), _p(beta), _p(slots), _p(state), _p(o))
     return o

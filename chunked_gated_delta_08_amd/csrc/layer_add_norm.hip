@@ -12,60 +12,84 @@
 namespace layer {
 namespace {
 
-template <class E, class R, int VEC, int TPR, int NV>
+template <class E, class R, int VEC, int NV> struct Rows {   // a row as loaded: x (or dy), res, dres and x
+    Raw<E, VEC> e[NV], x[NV];
+    Raw<R, VEC> res[NV], dres[NV];
+};
+template <class T, int VEC, int TPR, int NV>
+__device__ __forceinline__ void load_row(Raw<T, VEC> (&r)[NV], const void* p, long off, int lane, int D) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) load_raw<true>(r[i], (const T*)p + off, (i * TPR + lane) * VEC, D);
+}
+template <int VEC, int TPR, int NV>
+__device__ __forceinline__ void load_weights(float (&w)[NV][VEC], const float* p, int lane, int D) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        Raw<float, VEC> t;
+        load_raw<false>(t, p, (i * TPR + lane) * VEC, D);
+#pragma unroll
+        for (int e = 0; e < VEC; e++) w[i][e] = t.v[e];
+    }
+}
+
+template <class E, class R, int VEC, int TPR, int NV, bool SCALE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void add_norm_fwd_kernel(NormArgs a) {
     constexpr int NT = TPR > 256 ? TPR : 256, GR = NT / TPR;
     __shared__ float lds[TPR > 64 ? 2 * NT / 64 : 1];
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, D = a.D;
     const float inv = 1.f / (float)D;
+    float w[NV][VEC], sc[SCALE ? NV : 1][VEC];
+    load_weights<VEC, TPR, NV>(w, a.w, lane, D);
+    if constexpr (SCALE) load_weights<VEC, TPR, NV>(sc, a.scale, lane, D);
     int phase = 0;
     for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
         const bool live = r0 + grp < a.rows;
         const long off = (live ? r0 + grp : a.rows - 1) * D;
-        const E* x = (const E*)a.x + off;
-        const R* res = (const R*)a.res + off;
-        Raw<E, VEC> xr[NV];
-        Raw<R, VEC> rr[NV];
-#pragma unroll
-        for (int i = 0; i < NV; i++) load_raw<E, VEC>(xr[i], x, (i * TPR + lane) * VEC, D);
-#pragma unroll
-        for (int i = 0; i < NV; i++) load_raw<R, VEC>(rr[i], res, (i * TPR + lane) * VEC, D);
+        Rows<E, R, VEC, NV> in;
+        load_row<E, VEC, TPR, NV>(in.e, a.x, off, lane, D);
+        load_row<R, VEC, TPR, NV>(in.res, a.res, off, lane, D);
         float h[NV][VEC], s[1] = {0.f};
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            Raw<float, VEC> sc;
-            if (a.scale) load_raw<float, VEC>(sc, a.scale, (i * TPR + lane) * VEC, D);
+        for (int i = 0; i < NV; i++)
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                const float v = (float)xr[i].v[e];
-                h[i][e] = (float)rr[i].v[e] + (a.scale ? sc.v[e] * v : v);
+                const float v = (float)in.e[i].v[e];
+                h[i][e] = (float)in.res[i].v[e] + (SCALE ? sc[i][e] * v : v);
                 s[0] += h[i][e] * h[i][e];
             }
-        }
         row_sum<TPR, 1, NT>(s, lds, phase);
         const float r = rsqrtf(s[0] * inv + a.eps);
         if (!live) continue;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int c = (i * TPR + lane) * VEC;
-            Raw<float, VEC> w;
-            load_raw<float, VEC>(w, a.w, c, D);
             store_vec<R, VEC>((R*)a.res_out + off, c, D, h[i]);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) h[i][e] *= r * w.v[e];
+            for (int e = 0; e < VEC; e++) h[i][e] *= r * w[i][e];
             store_vec<E, VEC>((E*)a.y + off, c, D, h[i]);
         }
     }
 }
 
 template <class E, class R, int VEC, int TPR, int NV, bool SCALE>
+__device__ __forceinline__ void load_rows(Rows<E, R, VEC, NV>& r, const NormArgs& a, long row, int lane) {
+    const long off = (row < a.rows ? row : a.rows - 1) * a.D;
+    load_row<E, VEC, TPR, NV>(r.e, a.dy, off, lane, a.D);
+    load_row<R, VEC, TPR, NV>(r.res, a.res, off, lane, a.D);
+    if (a.dres) load_row<R, VEC, TPR, NV>(r.dres, a.dres, off, lane, a.D);
+    if constexpr (SCALE) load_row<E, VEC, TPR, NV>(r.x, a.x, off, lane, a.D);
+}
+
+template <class E, class R, int VEC, int TPR, int NV, bool SCALE, int BT>
 __global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
     constexpr int GR = BT / TPR;
     __shared__ float lds[BT * VEC];
     __shared__ float red[TPR > 64 ? 2 * 2 * (BT / 64) : 1];
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, D = a.D;
     const float inv = 1.f / (float)D;
-    float dw[NV][VEC], ds[SCALE ? NV : 1][VEC];
+    float w[NV][VEC], dw[NV][VEC], sc[SCALE ? NV : 1][VEC], ds[SCALE ? NV : 1][VEC];
+    load_weights<VEC, TPR, NV>(w, a.w, lane, D);
+    if constexpr (SCALE) load_weights<VEC, TPR, NV>(sc, a.scale, lane, D);
 #pragma unroll
     for (int i = 0; i < NV; i++)
 #pragma unroll
@@ -74,60 +98,48 @@ __global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
             if (SCALE) ds[i][e] = 0.f;
         }
     int phase = 0;
+    Rows<E, R, VEC, NV> in, next;
+    load_rows<E, R, VEC, TPR, NV, SCALE>(in, a, (long)blockIdx.x * GR + grp, lane);
     for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
-        const bool live = r0 + grp < a.rows;
-        const long off = (live ? r0 + grp : a.rows - 1) * D;
-        Raw<E, VEC> gr[NV], xr[SCALE ? NV : 1];
-        Raw<R, VEC> hr[NV], rr[NV];
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int c = (i * TPR + lane) * VEC;
-            load_raw<E, VEC>(gr[i], (const E*)a.dy + off, c, D);
-            load_raw<R, VEC>(hr[i], (const R*)a.res + off, c, D);
-            if (a.dres) load_raw<R, VEC>(rr[i], (const R*)a.dres + off, c, D);
-            if constexpr (SCALE) load_raw<E, VEC>(xr[i], (const E*)a.x + off, c, D);
-        }
+        load_rows<E, R, VEC, TPR, NV, SCALE>(next, a, r0 + (long)gridDim.x * GR + grp, lane);
         float s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            Raw<float, VEC> w;
-            load_raw<float, VEC>(w, a.w, (i * TPR + lane) * VEC, D);
+        for (int i = 0; i < NV; i++)
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                const float h = (float)hr[i].v[e];
+                const float h = (float)in.res[i].v[e];
                 s[0] += h * h;
-                s[1] += (float)gr[i].v[e] * w.v[e] * h;
+                s[1] += (float)in.e[i].v[e] * w[i][e] * h;
             }
-        }
         row_sum<TPR, 2, BT>(s, red, phase);
         const float r = rsqrtf(s[0] * inv + a.eps), m = r * s[1] * inv;
-        if (!live) continue;
+        if (r0 + grp < a.rows) {
+            const long off = (r0 + grp) * D;
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int c = (i * TPR + lane) * VEC;
-            Raw<float, VEC> w, sc;
-            load_raw<float, VEC>(w, a.w, c, D);
-            if constexpr (SCALE) load_raw<float, VEC>(sc, a.scale, c, D);
-            float dh[VEC], dx[VEC];
+            for (int i = 0; i < NV; i++) {
+                const int c = (i * TPR + lane) * VEC;
+                float dh[VEC], dx[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const float n = (float)hr[i].v[e] * r, g = (float)gr[i].v[e];
-                dh[e] = r * (g * w.v[e] - n * m) + (a.dres ? (float)rr[i].v[e] : 0.f);
-                dw[i][e] += g * n;
-                if constexpr (SCALE) {
-                    ds[i][e] += dh[e] * (float)xr[i].v[e];
-                    dx[e] = dh[e] * sc.v[e];
-                } else {
-                    dx[e] = dh[e];
+                for (int e = 0; e < VEC; e++) {
+                    const float n = (float)in.res[i].v[e] * r, g = (float)in.e[i].v[e];
+                    dh[e] = r * (g * w[i][e] - n * m) + (a.dres ? (float)in.dres[i].v[e] : 0.f);
+                    dw[i][e] += g * n;
+                    if constexpr (SCALE) {
+                        ds[i][e] += dh[e] * (float)in.x[i].v[e];
+                        dx[e] = dh[e] * sc[i][e];
+                    } else {
+                        dx[e] = dh[e];
+                    }
                 }
+                store_vec<R, VEC>((R*)a.dres_out + off, c, D, dh);
+                if (a.dx) store_vec<E, VEC>((E*)a.dx + off, c, D, dx);
             }
-            store_vec<R, VEC>((R*)a.dres_out + off, c, D, dh);
-            if (a.dx) store_vec<E, VEC>((E*)a.dx + off, c, D, dx);
         }
+        in = next;
     }
     float* part = a.part + (long)blockIdx.x * D * (SCALE ? 2 : 1);
-    write_part<VEC, TPR, NV>(dw, part, D, lds);
-    if constexpr (SCALE) write_part<VEC, TPR, NV>(ds, part + D, D, lds);
+    write_part<VEC, TPR, NV, BT>(dw, part, D, lds);
+    if constexpr (SCALE) write_part<VEC, TPR, NV, BT>(ds, part + D, D, lds);
 }
 
 // out[c] = sum over the partial rows in a fixed order: 16 columns per
@@ -164,8 +176,9 @@ template <class E, class R> hipError_t add_fwd(const NormArgs& a, hipStream_t s)
     constexpr int VEC = sizeof(R) == 4 ? 4 : 8;
     return split_rows<64, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, NT = TPR > 256 ? TPR : 256;
-        hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV>), dim3(grid_rows(a.rows, NT / TPR, 1 << 20)),
-                           dim3(NT), 0, s, a);
+        const dim3 grid(grid_rows(a.rows, NT / TPR, MAX_FWD_BLOCKS));
+        if (a.scale) hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV, true>), grid, dim3(NT), 0, s, a);
+        else hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV, false>), grid, dim3(NT), 0, s, a);
         return hipGetLastError();
     });
 }
@@ -175,13 +188,13 @@ template <class E, class R> hipError_t add_bwd(const NormArgs& a0, hipStream_t s
     NormArgs a = a0;
     int blocks = 1;
     const hipError_t e = split_rows<64, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
-        constexpr int TPR = decltype(T)::value, NV = decltype(N)::value;
+        constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
         blocks = grid_rows(a.rows, BT / TPR, MAX_BWD_BLOCKS);
         if (blocks == 1 && !a.scale) a.part = a.dw;
         if (a.scale)
-            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, true>), dim3(blocks), dim3(BT), 0, s, a);
+            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
         else
-            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, false>), dim3(blocks), dim3(BT), 0, s, a);
+            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);
         return hipGetLastError();
     });
     return e != hipSuccess ? e : norm_wsum(a, blocks, a.D * (a.scale ? 2 : 1), s);

@@ -13,65 +13,72 @@
 namespace layer {
 namespace {
 
-__device__ __forceinline__ void gate(float z, int act, float& f, float& df) {
-    const float s = sigmoid_f(z);
-    if (act == GDN_ACT_SILU) {
-        f = z * s;
-        df = s * (1.f + z * (1.f - s));
-    } else {
-        f = s;
-        df = s * (1.f - s);
+// act(z) and its derivative, from s = sigmoid(z).
+__device__ __forceinline__ float act_of(float z, float s, bool silu) { return silu ? z * s : s; }
+__device__ __forceinline__ float act_slope(float z, float s, bool silu) {
+    return silu ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
+}
+
+template <class E, int VEC, int NV> struct Rows {   // a row of x, z and dy as loaded
+    Raw<E, VEC> x[NV], z[NV], g[NV];
+};
+template <class E, int VEC, int TPR, int NV, bool GATE, bool BWD>
+__device__ __forceinline__ void load_rows(Rows<E, VEC, NV>& r, const NormArgs& a, long row, int lane) {
+    const long off = (row < a.rows ? row : a.rows - 1) * a.D;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int c = (i * TPR + lane) * VEC;
+        load_raw<true>(r.x[i], (const E*)a.x + off, c, a.D);
+        if constexpr (GATE) load_raw<true>(r.z[i], (const E*)a.z + off, c, a.D);
+        if constexpr (BWD) load_raw<true>(r.g[i], (const E*)a.dy + off, c, a.D);
+    }
+}
+template <int VEC, int TPR, int NV>
+__device__ __forceinline__ void load_weights(float (&w)[NV][VEC], const float* p, int lane, int D) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        Raw<float, VEC> t;
+        load_raw<false>(t, p, (i * TPR + lane) * VEC, D);
+#pragma unroll
+        for (int e = 0; e < VEC; e++) w[i][e] = t.v[e];
     }
 }
 
-// ---------------------------------------------------------------- forward
+// One pass: many short-lived workgroups, whose next rows' loads overlap by themselves.
 template <class E, int VEC, int TPR, int NV, bool GATE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void gated_norm_fwd_kernel(NormArgs a) {
     constexpr int NT = TPR > 256 ? TPR : 256, GR = NT / TPR;   // rows a workgroup takes at a time
     __shared__ float lds[TPR > 64 ? 2 * NT / 64 : 1];
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, D = a.D;
     const float inv = 1.f / (float)D;
+    const bool silu = a.act == GDN_ACT_SILU;
     float w[NV][VEC];
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        Raw<float, VEC> t;
-        load_raw<float, VEC>(t, a.w, (i * TPR + lane) * VEC, D);
-#pragma unroll
-        for (int e = 0; e < VEC; e++) w[i][e] = t.v[e];
-    }
+    load_weights<VEC, TPR, NV>(w, a.w, lane, D);
     int phase = 0;
     for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
-        const bool live = r0 + grp < a.rows;
-        const long off = (live ? r0 + grp : a.rows - 1) * D;
-        const E* x = (const E*)a.x + off;
-        const E* z = (const E*)a.z + off;
-        E* y = (E*)a.y + off;
-        Raw<E, VEC> xr[NV], zr[GATE ? NV : 1];
-#pragma unroll
-        for (int i = 0; i < NV; i++) load_raw<E, VEC>(xr[i], x, (i * TPR + lane) * VEC, D);
-        if constexpr (GATE)
-#pragma unroll
-            for (int i = 0; i < NV; i++) load_raw<E, VEC>(zr[i], z, (i * TPR + lane) * VEC, D);
+        Rows<E, VEC, NV> in;
+        load_rows<E, VEC, TPR, NV, GATE, false>(in, a, r0 + grp, lane);
         float s[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < NV; i++)
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                const float v = (float)xr[i].v[e];
+                const float v = (float)in.x[i].v[e];
                 s[0] += v * v;
             }
         row_sum<TPR, 1, NT>(s, lds, phase);
         const float r = rsqrtf(s[0] * inv + a.eps);
-        if (!live) continue;
+        if (r0 + grp >= a.rows) continue;
+        E* y = (E*)a.y + (r0 + grp) * D;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             float o[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                o[e] = (float)xr[i].v[e] * r * w[i][e];
+                o[e] = (float)in.x[i].v[e] * r * w[i][e];
                 if constexpr (GATE) {
-                    const float zz = (float)zr[i].v[e], sg = sigmoid_f(zz);
-                    o[e] *= a.act == GDN_ACT_SILU ? zz * sg : sg;
+                    const float z = (float)in.z[i].v[e];
+                    o[e] *= act_of(z, sigmoid_f(z), silu);
                 }
             }
             store_vec<E, VEC>(y, (i * TPR + lane) * VEC, D, o);
@@ -79,82 +86,76 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void gated_norm_fwd_kernel(N
     }
 }
 
-template <class E, int VEC, int TPR, int NV, bool GATE>
+// A workgroup takes rows in turn, the next one's on their way meanwhile.
+template <class E, int VEC, int TPR, int NV, bool GATE, int BT>
 __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
     constexpr int GR = BT / TPR;
     __shared__ float lds[BT * VEC];
     __shared__ float red[TPR > 64 ? 2 * 2 * (BT / 64) : 1];
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, D = a.D;
     const float inv = 1.f / (float)D;
+    const bool silu = a.act == GDN_ACT_SILU;
     float w[NV][VEC], dw[NV][VEC];
+    load_weights<VEC, TPR, NV>(w, a.w, lane, D);
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        Raw<float, VEC> t;
-        load_raw<float, VEC>(t, a.w, (i * TPR + lane) * VEC, D);
+    for (int i = 0; i < NV; i++)
 #pragma unroll
-        for (int e = 0; e < VEC; e++) w[i][e] = t.v[e], dw[i][e] = 0.f;
-    }
+        for (int e = 0; e < VEC; e++) dw[i][e] = 0.f;
     int phase = 0;
+    Rows<E, VEC, NV> in, next;
+    load_rows<E, VEC, TPR, NV, GATE, true>(in, a, (long)blockIdx.x * GR + grp, lane);
     for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
-        const bool live = r0 + grp < a.rows;
-        const long off = (live ? r0 + grp : a.rows - 1) * D;
-        Raw<E, VEC> xr[NV], gr[NV], zr[GATE ? NV : 1];
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int c = (i * TPR + lane) * VEC;
-            load_raw<E, VEC>(xr[i], (const E*)a.x + off, c, D);
-            load_raw<E, VEC>(gr[i], (const E*)a.dy + off, c, D);
-            if constexpr (GATE) load_raw<E, VEC>(zr[i], (const E*)a.z + off, c, D);
-        }
-        float s[2] = {0.f, 0.f};
+        load_rows<E, VEC, TPR, NV, GATE, true>(next, a, r0 + (long)gridDim.x * GR + grp, lane);
+        float s[2] = {0.f, 0.f}, sg[GATE ? NV : 1][VEC];   // sg: the gate's sigmoid, formed once
 #pragma unroll
         for (int i = 0; i < NV; i++)
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                const float x = (float)xr[i].v[e];
-                float dn = (float)gr[i].v[e] * w[i][e];
+                const float x = (float)in.x[i].v[e];
+                float dn = (float)in.g[i].v[e] * w[i][e];
                 if constexpr (GATE) {
-                    float f, df;
-                    gate((float)zr[i].v[e], a.act, f, df);
-                    dn *= f;
+                    const float z = (float)in.z[i].v[e];
+                    sg[i][e] = sigmoid_f(z);
+                    dn *= act_of(z, sg[i][e], silu);
                 }
                 s[0] += x * x;
                 s[1] += dn * x;
             }
         row_sum<TPR, 2, BT>(s, red, phase);
         const float r = rsqrtf(s[0] * inv + a.eps), m = r * s[1] * inv;   // m = mean(dn n)
-        if (!live) continue;
+        if (r0 + grp < a.rows) {
+            const long off = (r0 + grp) * D;
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int c = (i * TPR + lane) * VEC;
-            float dx[VEC], dz[VEC];
+            for (int i = 0; i < NV; i++) {
+                const int c = (i * TPR + lane) * VEC;
+                float dx[VEC], dz[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const float n = (float)xr[i].v[e] * r, g = (float)gr[i].v[e];
-                float dn = g * w[i][e], t = g * n;   // t = dy n
-                if constexpr (GATE) {
-                    float f, df;
-                    gate((float)zr[i].v[e], a.act, f, df);
-                    dn *= f;
-                    dz[e] = t * w[i][e] * df;
-                    t *= f;
+                for (int e = 0; e < VEC; e++) {
+                    const float n = (float)in.x[i].v[e] * r, g = (float)in.g[i].v[e];
+                    float dn = g * w[i][e], t = g * n;   // t = dy n
+                    if constexpr (GATE) {
+                        const float z = (float)in.z[i].v[e], f = act_of(z, sg[i][e], silu);
+                        dn *= f;
+                        dz[e] = t * w[i][e] * act_slope(z, sg[i][e], silu);
+                        t *= f;
+                    }
+                    dw[i][e] += t;
+                    dx[e] = r * (dn - n * m);
                 }
-                dw[i][e] += t;
-                dx[e] = r * (dn - n * m);
+                store_vec<E, VEC>((E*)a.dx + off, c, D, dx);
+                if constexpr (GATE) store_vec<E, VEC>((E*)a.dz + off, c, D, dz);
             }
-            store_vec<E, VEC>((E*)a.dx + off, c, D, dx);
-            if constexpr (GATE) store_vec<E, VEC>((E*)a.dz + off, c, D, dz);
         }
+        in = next;
     }
-    write_part<VEC, TPR, NV>(dw, a.part + (long)blockIdx.x * D, D, lds);
+    write_part<VEC, TPR, NV, BT>(dw, a.part + (long)blockIdx.x * D, D, lds);
 }
-
 
 template <class E> hipError_t gated_fwd(const NormArgs& a, hipStream_t s) {
     constexpr int VEC = sizeof(E) == 4 ? 4 : 8;
     return split_rows<8, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, NT = TPR > 256 ? TPR : 256;
-        const dim3 grid(grid_rows(a.rows, NT / TPR, 1 << 20));
+        const dim3 grid(grid_rows(a.rows, NT / TPR, MAX_FWD_BLOCKS));
         if (a.z) hipLaunchKernelGGL((gated_norm_fwd_kernel<E, VEC, TPR, NV, true>), grid, dim3(NT), 0, s, a);
         else hipLaunchKernelGGL((gated_norm_fwd_kernel<E, VEC, TPR, NV, false>), grid, dim3(NT), 0, s, a);
         return hipGetLastError();
@@ -166,11 +167,11 @@ template <class E> hipError_t gated_bwd(const NormArgs& a0, hipStream_t s) {
     NormArgs a = a0;
     int blocks = 1;
     const hipError_t e = split_rows<8, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
-        constexpr int TPR = decltype(T)::value, NV = decltype(N)::value;
+        constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
         blocks = grid_rows(a.rows, BT / TPR, MAX_BWD_BLOCKS);
         if (blocks == 1) a.part = a.dw;
-        if (a.z) hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, true>), dim3(blocks), dim3(BT), 0, s, a);
-        else hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, false>), dim3(blocks), dim3(BT), 0, s, a);
+        if (a.z) hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
+        else hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);
         return hipGetLastError();
     });
     return e != hipSuccess ? e : norm_wsum(a, blocks, a.D, s);

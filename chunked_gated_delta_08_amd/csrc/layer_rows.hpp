@@ -25,10 +25,13 @@ template <class E, int VEC> struct Raw {
 };
 
 // VEC elements of a row from column c; columns past D read as zero.
-template <class E, int VEC>
+// NT: read once in the launch, not kept in the caches (what every row reads, the
+// weights, is: non-temporal reads of those doubled the add norm's backward).
+template <bool NT, class E, int VEC>
 __device__ __forceinline__ void load_raw(Raw<E, VEC>& r, const E* row, int c, int D) {
     if (c + VEC <= D) {
-        r.v = *(const typename VecU<E, VEC>::t*)(row + c);
+        auto p = (const typename VecU<E, VEC>::t*)(row + c);
+        r.v = NT ? __builtin_nontemporal_load(p) : *p;
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; e++) r.v[e] = c + e < D ? row[c + e] : (E)0.f;
@@ -40,7 +43,7 @@ __device__ __forceinline__ void store_vec(E* row, int c, int D, const float (&x)
         typename VecU<E, VEC>::t t;
 #pragma unroll
         for (int e = 0; e < VEC; e++) t[e] = (E)x[e];
-        *(typename VecU<E, VEC>::t*)(row + c) = t;
+        __builtin_nontemporal_store(t, (typename VecU<E, VEC>::t*)(row + c));
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; e++)
@@ -82,10 +85,10 @@ __device__ __forceinline__ void row_sum(float (&s)[NVAL], float* lds, int phase)
     }
 }
 
-constexpr int BT = 512;   // threads of a backward workgroup
+
 
 // Adds the groups' column sums in group order and writes them to part[which].
-template <int VEC, int TPR, int NV>
+template <int VEC, int TPR, int NV, int BT>
 __device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* out, int D, float* lds) {
     constexpr int GR = BT / TPR;
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -105,9 +108,8 @@ __device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* o
 
 
 // Calls f(TPR, NV) for a row of nvt vectors: the smallest power of two of lanes
-// up to a wave with one vector each, then two vectors each, then 256 lanes
-// with one or two, 512 with two or (4-element vectors only) four.
-// MIN_TPR: rows as narrow as a part of a wave are not split further than this.
+// with one vector each, 1024 with two beyond.  MIN_TPR: rows as narrow as a part
+// of a wave are not split further than this.
 template <int MIN_TPR, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
 #define LAYER_CASE(T, N) return f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
     if constexpr (MIN_TPR < 64) {
@@ -116,17 +118,23 @@ template <int MIN_TPR, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
         if (nvt <= 32) LAYER_CASE(32, 1);
     }
     if (nvt <= 64) LAYER_CASE(64, 1);
-    if (nvt <= 128) LAYER_CASE(64, 2);
+    if (nvt <= 128) LAYER_CASE(128, 1);
     if (nvt <= 256) LAYER_CASE(256, 1);
-    if (nvt <= 512) LAYER_CASE(256, 2);
+    if (nvt <= 512) LAYER_CASE(512, 1);
     if constexpr (VEC == 4) {
-        if (nvt > 1024) LAYER_CASE(512, 4);
+        if (nvt > 1024) LAYER_CASE(1024, 2);
     }
-    LAYER_CASE(512, 2);
+    LAYER_CASE(1024, 1);
 #undef LAYER_CASE
 }
 
-constexpr int MAX_BWD_BLOCKS = 512;   // two workgroups of eight waves per CU
+// Workgroups of a launch: enough to fill the chip several times over where each
+// is short-lived (8192 against one for every row: 68 and 71 us for the gated norm
+// at T=32768 H=16 D=128), and what the chip holds where each keeps weight
+// gradients and reads ahead (512 against 1024: 145 and 152 us for the add norm's
+// backward at 16384 x 4096).
+constexpr int MAX_FWD_BLOCKS = 8192, MAX_BWD_BLOCKS = 512;
+constexpr int BWD_THREADS = 512;   // of a backward workgroup, at least
 
 inline int grid_rows(long rows, int per, long most) {
     const long n = (rows + per - 1) / per;

@@ -695,8 +695,7 @@ def _state(B, T=3000, D=256):
              gf=dict(h=e(T, D, t=bf), ht=e(3, D), states=e(B.glr_num_states(T), D)),
              gb=dict(dx=e(T, D, t=bf), dg=e(T, D), dh0=e(3, D)))
     n = B.norm_workspace_size(T, D, bf)
-    p, _ = B._glr_problem(d["x"], d["cu"], cuh, 1)
-    m = max(1, int(B.lib.glr_workspace_size(p)))
+    m = B.glr_workspace_size(T, D, bf, cu_seqlens_host=cuh)
     ws = [e(n, t=torch.uint8), e(n, t=torch.uint8), e(m, t=torch.uint8), e(m, t=torch.uint8)]
     return d, ws
 
