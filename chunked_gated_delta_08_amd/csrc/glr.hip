@@ -646,7 +646,8 @@ __global__ __launch_bounds__(256) void glr_pass_kernel(const float* in, float* o
     if (i < n) out[i] = in ? in[i] : 0.f;
 }
 
-constexpr int CH = 2;   // channels of a lane
+// Channels of a lane: two, but one where a wave then covers the row alone.
+int width(const GlrArgs& a) { return a.D > 64 ? 2 : 1; }
 // Tiles of a segment.  More of them make fewer segments wait for one another, but
 // a workgroup needs its waves at once: two workgroups of 12 waves fill what the
 // forward's 80 registers a lane leave (fp32 x takes 16 more: 8 waves), two of 8
@@ -656,7 +657,7 @@ int tiles_of(const GlrArgs& a, bool bwd) { return bwd ? WB : a.dtype == GDR_F32 
 
 int segments(const GlrArgs& a, int w) { return (int)((a.ntok + w * L - 1) / (w * L)); }
 int blocks(const GlrArgs& a) {
-    const int c = 64 * (a.D >= CH ? CH : 1);
+    const int c = 64 * width(a);
     return (a.D + c - 1) / c;
 }
 // Whether a segment of w tiles may begin inside a sequence.
@@ -686,7 +687,7 @@ template <class E, int C> hipError_t run(const GlrArgs& a, bool bwd, hipStream_t
     return hipGetLastError();
 }
 template <class E> hipError_t by_width(const GlrArgs& a, bool bwd, hipStream_t s) {
-    return a.D >= CH ? run<E, CH>(a, bwd, s) : run<E, 1>(a, bwd, s);
+    return width(a) == 2 ? run<E, 2>(a, bwd, s) : run<E, 1>(a, bwd, s);
 }
 hipError_t by_type(const GlrArgs& a, bool bwd, hipStream_t s) {
     switch (a.dtype) {

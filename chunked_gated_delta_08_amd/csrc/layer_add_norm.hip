@@ -101,7 +101,7 @@ __global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
     Rows<E, R, VEC, NV> in, next;
     load_rows<E, R, VEC, TPR, NV, SCALE>(in, a, (long)blockIdx.x * GR + grp, lane);
     for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
-        load_rows<E, R, VEC, TPR, NV, SCALE>(next, a, r0 + (long)gridDim.x * GR + grp, lane);
+        if constexpr (NV == 1) load_rows<E, R, VEC, TPR, NV, SCALE>(next, a, r0 + (long)gridDim.x * GR + grp, lane);
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; i++)
@@ -135,7 +135,8 @@ __global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
                 if (a.dx) store_vec<E, VEC>((E*)a.dx + off, c, D, dx);
             }
         }
-        in = next;
+        if constexpr (NV == 1) in = next;
+        else load_rows<E, R, VEC, TPR, NV, SCALE>(in, a, r0 + (long)gridDim.x * GR + grp, lane);   // no registers to read ahead
     }
     float* part = a.part + (long)blockIdx.x * D * (SCALE ? 2 : 1);
     write_part<VEC, TPR, NV, BT>(dw, part, D, lds);

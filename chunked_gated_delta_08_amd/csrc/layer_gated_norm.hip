@@ -105,7 +105,7 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
     Rows<E, VEC, NV> in, next;
     load_rows<E, VEC, TPR, NV, GATE, true>(in, a, (long)blockIdx.x * GR + grp, lane);
     for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
-        load_rows<E, VEC, TPR, NV, GATE, true>(next, a, r0 + (long)gridDim.x * GR + grp, lane);
+        if constexpr (NV == 1) load_rows<E, VEC, TPR, NV, GATE, true>(next, a, r0 + (long)gridDim.x * GR + grp, lane);
         float s[2] = {0.f, 0.f}, sg[GATE ? NV : 1][VEC];   // sg: the gate's sigmoid, formed once
 #pragma unroll
         for (int i = 0; i < NV; i++)
@@ -146,7 +146,8 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
                 if constexpr (GATE) store_vec<E, VEC>((E*)a.dz + off, c, D, dz);
             }
         }
-        in = next;
+        if constexpr (NV == 1) in = next;
+        else load_rows<E, VEC, TPR, NV, GATE, true>(in, a, r0 + (long)gridDim.x * GR + grp, lane);   // no registers to read ahead
     }
     write_part<VEC, TPR, NV, BT>(dw, a.part + (long)blockIdx.x * D, D, lds);
 }

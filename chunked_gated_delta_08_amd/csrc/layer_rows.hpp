@@ -87,25 +87,30 @@ __device__ __forceinline__ void row_sum(float (&s)[NVAL], float* lds, int phase)
 
 
 
-// Adds the groups' column sums in group order and writes them to part[which].
+// Joins the groups' column sums pairwise and writes them to `out`.
 template <int VEC, int TPR, int NV, int BT>
 __device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* out, int D, float* lds) {
     constexpr int GR = BT / TPR;
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    float* mine = lds + (grp * TPR + lane) * VEC;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < VEC; e++) lds[(grp * TPR + lane) * VEC + e] = acc[i][e];
+        for (int e = 0; e < VEC; e++) mine[e] = acc[i][e];
         __syncthreads();
-        for (int c = threadIdx.x; c < TPR * VEC; c += BT) {
-            float t = 0.f;
-            for (int k = 0; k < GR; k++) t += lds[k * TPR * VEC + c];
-            if (i * TPR * VEC + c < D) out[i * TPR * VEC + c] = t;
+        for (int m = GR / 2; m >= 1; m /= 2) {
+            if (grp < m)
+#pragma unroll
+                for (int e = 0; e < VEC; e++) mine[e] += mine[m * TPR * VEC + e];
+            __syncthreads();
+        }
+        if (grp == 0) {
+            const int c = (i * TPR + lane) * VEC;
+            for (int e = 0; e < VEC && c + e < D; e++) out[c + e] = mine[e];
         }
     }
 }
-
 
 // Calls f(TPR, NV) for a row of nvt vectors: the smallest power of two of lanes
 // with one vector each, 1024 with two beyond.  MIN_TPR: rows as narrow as a part
@@ -113,6 +118,9 @@ __device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* o
 template <int MIN_TPR, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
 #define LAYER_CASE(T, N) return f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
     if constexpr (MIN_TPR < 64) {
+        if (nvt <= 1) LAYER_CASE(1, 1);
+        if (nvt <= 2) LAYER_CASE(2, 1);
+        if (nvt <= 4) LAYER_CASE(4, 1);
         if (nvt <= 8) LAYER_CASE(8, 1);
         if (nvt <= 16) LAYER_CASE(16, 1);
         if (nvt <= 32) LAYER_CASE(32, 1);

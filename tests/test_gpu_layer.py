@@ -103,7 +103,7 @@ def gated_ref(x, z, w, dy, act, dtype):
     return ref, tol
 
 
-NORM_SHAPES = [(1, 1), (5, 3), (17, 64), (33, 100), (64, 128), (7, 257), (9, 512), (130, 500), (3, 1000), (5, 2048),
+NORM_SHAPES = [(1, 1), (5, 3), (700, 7), (300, 8), (77, 16), (50, 20), (17, 64), (33, 100), (64, 128), (7, 257), (9, 512), (130, 500), (3, 1000), (5, 2048),
                (4, 2500), (3, 4096), (2, 5001), (3, 8192)]
 
 
