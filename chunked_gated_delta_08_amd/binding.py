@@ -121,7 +121,7 @@ def _need(t, name, dtype=None, shape=None, cuda=True, optional=False):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -531,13 +531,16 @@ lib.gdr_step.argtypes = [_i] * 5 + [_i64, _f, _i] + [_vp] * 9
 
 
 def _same_device(first, *others):
-    dev = first.device
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
 
 
-# the current stream's handle, without the Stream object around it where torch offers that
+# the current device and its current stream's handle, without the checks and the
+# Stream object around them where torch offers that (a GPU tensor is at hand, so
+# torch has been initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -545,7 +548,8 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 def _launch(dev, stream, temps, call, *args):
     """call(*args, stream handle) with `dev` current.  `temps`: tensors allocated for this
     call on the current stream; the allocator is told when another one uses them."""
-    handle = _current_stream(dev.index)
+    index = dev.index
+    handle = _current_stream(index)
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
@@ -554,7 +558,7 @@ def _launch(dev, stream, temps, call, *args):
                 if t is not None:
                     t.record_stream(stream)
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == index:
         code = call(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -600,15 +604,15 @@ def norm_workspace_size(rows, D, dtype):
     return _norm_sizes(rows, D, 0.0, dtype, dtype, "silu")[1]
 
 
-def _workspace(workspace, size, dev):
-    """(the workspace, the tensor allocated for it or None); no workspace for a size of 0."""
+def _workspace(workspace, size, like):
+    """(the workspace, its bytes, the tensor allocated for it or None), on the device of the
+    fp32 tensor `like`; no workspace for a size of 0."""
     if workspace is None:
-        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-        return ws, ws
+        ws = like.new_empty((size + 3) // 4) if size else None
+        return ws, size, ws
     _need(workspace, "workspace", torch.uint8)
-    if workspace.device != dev:
-        raise ValueError(f"workspace on {workspace.device}, the tensors on {dev}")
-    return workspace, None
+    _same_device(like, workspace)
+    return workspace, workspace.numel(), None
 
 
 def gated_norm_fwd(x, z, w, eps=1e-5, act="silu", out=None, stream=None):
@@ -639,10 +643,10 @@ def gated_norm_bwd(x, z, w, dy, eps=1e-5, act="silu", out=None, workspace=None, 
         _same_device(x, *out.values())
     dz = None if z is None else out["dz"]
     p, size = _norm_problem(x, eps, act=act)
-    ws, mine = _workspace(workspace, size, x.device)
+    ws, size, mine = _workspace(workspace, size, w)
     own.append(mine)
     _launch(x.device, stream, own, lib.gated_norm_bwd, p, _p(x), _p(z), _p(w), _p(dy), _p(out["dx"]), _p(dz),
-            _p(out["dw"]), _p(ws), ws.numel())
+            _p(out["dw"]), _p(ws), size)
     return out
 
 
@@ -708,10 +712,10 @@ def add_norm_bwd(dy, dres, res, w, x=None, scale=None, eps=1e-5, out=None, works
     dx = None if scale is None and out["dx"] is out["dres"] else out["dx"]
     ds = None if scale is None else out["dscale"]
     p, size = _norm_problem(dy, eps, res.dtype)
-    ws, mine = _workspace(workspace, size, dy.device)
+    ws, size, mine = _workspace(workspace, size, w)
     own.append(mine)
     _launch(dy.device, stream, own, lib.add_norm_bwd, p, _p(dy), _p(dres), _p(res), _p(w), _p(x), _p(scale), _p(dx),
-            _p(out["dres"]), _p(out["dw"]), _p(ds), _p(ws), ws.numel())
+            _p(out["dres"]), _p(out["dw"]), _p(ds), _p(ws), size)
     return out
 
 
@@ -790,9 +794,8 @@ def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=T
     own = []
     if out is None:
         out = {"h": torch.empty_like(x),
-               "ht": torch.empty((N, D), dtype=torch.float32, device=dev) if want_ht else None,
-               "states": torch.empty((glr_num_states(ntok), D), dtype=torch.float32, device=dev) if want_states
-               else None}
+               "ht": g.new_empty((N, D)) if want_ht else None,
+               "states": g.new_empty((glr_num_states(ntok), D)) if want_states else None}
         own += out.values()
     else:
         _need(out["h"], "h", x.dtype, x.shape)
@@ -800,10 +803,10 @@ def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=T
         _need(out["states"], "states", torch.float32, (glr_num_states(ntok), D), optional=True)
         _same_device(x, *out.values())
     p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
-    ws, mine = _workspace(workspace, size, dev)
+    ws, size, mine = _workspace(workspace, size, g)
     own.append(mine)
     _launch(dev, stream, own, lib.glr_fwd, p, _p(x), _p(g), _p(h0), _p(out["h"]), _p(out["ht"]), _p(out["states"]),
-            _p(ws), 0 if ws is None else ws.numel())
+            _p(ws), size)
     del keep
     return out
 
@@ -817,7 +820,7 @@ def glr_bwd(x, g, dh, states, dht=None, h0=None, cu_seqlens=None, cu_seqlens_hos
     own = []
     if out is None:
         out = {"dx": torch.empty_like(x), "dg": torch.empty_like(g),
-               "dh0": torch.empty((N, D), dtype=torch.float32, device=dev) if want_dh0 else None}
+               "dh0": g.new_empty((N, D)) if want_dh0 else None}
         own += out.values()
     else:
         _need(out["dx"], "dx", x.dtype, x.shape)
@@ -825,17 +828,17 @@ def glr_bwd(x, g, dh, states, dht=None, h0=None, cu_seqlens=None, cu_seqlens_hos
         _need(out["dh0"], "dh0", torch.float32, (N, D), optional=True)
         _same_device(x, *out.values())
     p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
-    ws, mine = _workspace(workspace, size, dev)
+    ws, size, mine = _workspace(workspace, size, g)
     own.append(mine)
     _launch(dev, stream, own, lib.glr_bwd, p, _p(x), _p(g), _p(h0), _p(states), _p(dh), _p(dht), _p(out["dx"]),
-            _p(out["dg"]), _p(out["dh0"]), _p(ws), 0 if ws is None else ws.numel())
+            _p(out["dg"]), _p(out["dh0"]), _p(ws), size)
     del keep
     return out
 
 
 def _check_pool(state, slots, n, shape, cuda):
     _need(state, "state", torch.float32, cuda=cuda)
-    if state.dim() != 1 + len(shape) or tuple(state.shape[1:]) != tuple(shape):
+    if state.shape[1:] != shape:
         raise ValueError(f"state has shape {tuple(state.shape)}, expected [slots, {', '.join(map(str, shape))}]")
     _need(slots, "slots", torch.int32, (n,), cuda=cuda, optional=True)
     if slots is None and n > state.shape[0]:

@@ -107,7 +107,14 @@ __device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* o
         }
         if (grp == 0) {
             const int c = (i * TPR + lane) * VEC;
-            for (int e = 0; e < VEC && c + e < D; e++) out[c + e] = mine[e];
+            if (c + VEC <= D) {
+                typename VecU<float, VEC>::t t;
+#pragma unroll
+                for (int e = 0; e < VEC; e++) t[e] = mine[e];
+                *(typename VecU<float, VEC>::t*)(out + c) = t;
+            } else {
+                for (int e = 0; c + e < D; e++) out[c + e] = mine[e];
+            }
         }
     }
 }
