@@ -79,13 +79,16 @@ class AddRMSNorm(torch.autograd.Function):
         scale = None if scale is None else scale.contiguous()
         out = binding.add_norm_fwd(x, res, w, scale=scale, eps=eps)
         ctx.save_for_backward(None if scale is None else x, out["res"], w, scale)
-        ctx.eps = eps
+        ctx.cfg = (eps, x.dtype)
+        ctx.set_materialize_grads(False)   # an unused residual stream has no gradient to read
         return out["y"], out["res"]
 
     @staticmethod
     def backward(ctx, dy, dres):
         x, res, w, scale = ctx.saved_tensors
-        r = binding.add_norm_bwd(dy.contiguous(), dres.contiguous(), res, w, x=x, scale=scale, eps=ctx.eps)
+        dy = torch.zeros_like(res, dtype=ctx.cfg[1]) if dy is None else dy.contiguous()
+        dres = None if dres is None else dres.contiguous()
+        r = binding.add_norm_bwd(dy, dres, res, w, x=x, scale=scale, eps=ctx.cfg[0])
         return r["dx"], r["dres"], r["dw"], r["dscale"], None
 
 
@@ -106,12 +109,15 @@ class GatedLinearRecurrence(torch.autograd.Function):
                               want_states=True)
         ctx.save_for_backward(x, g, h0, out["states"], cu_seqlens, cu_seqlens_host)
         ctx.B = B
+        ctx.set_materialize_grads(False)   # an unused final state has no gradient to read
         return out["h"], out["ht"]
 
     @staticmethod
     def backward(ctx, dh, dht):
         x, g, h0, states, cu_seqlens, cu_seqlens_host = ctx.saved_tensors
-        r = binding.glr_bwd(x, g, dh.contiguous(), states, dht=dht.contiguous(), h0=h0, cu_seqlens=cu_seqlens,
+        dh = torch.zeros_like(x) if dh is None else dh.contiguous()
+        dht = None if dht is None else dht.contiguous()
+        r = binding.glr_bwd(x, g, dh, states, dht=dht, h0=h0, cu_seqlens=cu_seqlens,
                             cu_seqlens_host=cu_seqlens_host, B=ctx.B,
                             want_dh0=h0 is not None and ctx.needs_input_grad[2])
         return r["dx"], r["dg"], r["dh0"], None, None, None

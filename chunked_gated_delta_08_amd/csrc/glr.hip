@@ -58,12 +58,15 @@ __device__ __forceinline__ u64 peek(const u64* p) {
 }
 
 // ------------------------------------------------------------- sequences
-// Sequence n is tokens [first(n), first(n + 1)); all values are uniform.
+// Sequence n is tokens [first(n), first(n + 1)); all values are uniform.  What
+// the device's cu_seqlens holds is kept within the tokens and sequences there
+// are, so that a copy that differs from the host's gives wrong results and not
+// accesses out of bounds.
 struct Seqs {
     const int32_t* cu;
-    int T, nseq;
+    int T, nseq, ntok;
     __device__ __forceinline__ int first(int n) const {
-        return cu ? __builtin_amdgcn_readfirstlane(cu[n]) : n * T;
+        return cu ? min(max(__builtin_amdgcn_readfirstlane(cu[n]), 0), ntok) : n * T;
     }
     // the (non-empty) sequence of token t
     __device__ __forceinline__ int of(int t) const {
@@ -78,14 +81,14 @@ struct Seqs {
     }
     // from sequence n the next one, or the one before, that has tokens
     __device__ __forceinline__ int next(int n) const {
-        do n++;
-        while (n + 1 < nseq && first(n + 1) == first(n));
-        return n;
+        while (++n + 1 < nseq && first(n + 1) == first(n)) {
+        }
+        return min(n, nseq - 1);
     }
     __device__ __forceinline__ int prev(int n) const {
-        do n--;
-        while (n > 0 && first(n + 1) == first(n));
-        return n;
+        while (--n > 0 && first(n + 1) == first(n)) {
+        }
+        return max(n, 0);
     }
 };
 
@@ -104,8 +107,8 @@ struct Tile {
         int n = q.of(t0);
         n0 = n;
         if (q.first(n) == t0) begins = 1;
-        for (int e = q.first(n + 1); e < t0 + nt; e = q.first(n + 1)) {
-            begins |= 1u << (e - t0);
+        for (int e = q.first(n + 1); n + 1 < q.nseq && e < t0 + nt; e = q.first(n + 1)) {
+            begins |= 1u << ((e - t0) & 31);
             n = q.next(n);
         }
         n1 = n;
@@ -428,7 +431,7 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 4 ? 4 : 6) void glr_fwd_kernel
     const Ws ws = carve(a.ws, nseg, a.D);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.D;
     const int ntok = (int)a.ntok;
-    const Seqs q{a.cu, a.T, a.nseq};
+    const Seqs q{a.cu, a.T, a.nseq, ntok};
     const int own = blockIdx.x / nblk, blk = blockIdx.x % nblk;
     for (int seg = own;;) {
         const unsigned ch = channel<C>(blk, D);
@@ -525,7 +528,7 @@ __global__ __launch_bounds__(64 * W, 4) void glr_bwd_kernel(GlrArgs a, int nblk,
     const Ws ws = carve(a.ws, nseg, a.D);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.D;
     const int ntok = (int)a.ntok, pw = W - 1 - w;   // pw: the tile's place in processing order
-    const Seqs q{a.cu, a.T, a.nseq};
+    const Seqs q{a.cu, a.T, a.nseq, ntok};
     const int own = blockIdx.x / nblk, blk = blockIdx.x % nblk;
     for (int idx = own;;) {
         const int seg = nseg - 1 - idx;

@@ -185,7 +185,7 @@ int glr_fwd(const glr_problem* p, const void* x, const float* g, const float* h0
     const size_t need = layer::glr_ws_bytes(a);
     if ((st = check_ws(ws, ws_bytes, need)) != GDR_OK) return st;
     const size_t es = size_of(a.dtype), n = (size_t)a.ntok * a.D, c = 4 * (size_t)a.nseq * a.D;
-    if (!buffers_ok({{x, n * es, es}, {g, 4 * n, 4}, {h0, c, 4}},
+    if (!buffers_ok({{x, n * es, es}, {g, 4 * n, 4}, {h0, c, 4}, {a.cu, 4 * (size_t)(a.nseq + 1), 4}},
                     {{{h, n * es, es}, 0}, {{ht, c, 4}, 0}, {{states, 4 * (size_t)tiles(a) * a.D, 4}, 0},
                      {{ws, need, 16}, 0}}))
         return GDR_ERR_INVALID;
@@ -204,7 +204,7 @@ int glr_bwd(const glr_problem* p, const void* x, const float* g, const float* h0
     if ((st = check_ws(ws, ws_bytes, need)) != GDR_OK) return st;
     const size_t es = size_of(a.dtype), n = (size_t)a.ntok * a.D, c = 4 * (size_t)a.nseq * a.D;
     if (!buffers_ok({{x, n * es, es}, {g, 4 * n, 4}, {h0, c, 4}, {states, 4 * (size_t)tiles(a) * a.D, 4},
-                     {dh, n * es, es}, {dht, c, 4}},
+                     {dh, n * es, es}, {dht, c, 4}, {a.cu, 4 * (size_t)(a.nseq + 1), 4}},
                     {{{dx, n * es, es}, 0}, {{dg, 4 * n, 4}, 0}, {{dh0, c, 4}, 0}, {{ws, need, 16}, 0}}))
         return GDR_ERR_INVALID;
     a.x = x; a.g = g; a.h0 = h0; a.states = (float*)states; a.dh = dh; a.dht = dht; a.dx = dx; a.dg = dg; a.dh0 = dh0;

@@ -664,6 +664,93 @@ def test_layer_forward_and_gradients(B, monkeypatch):
         assert rel(got[n], want[n]) <= 1e-4, (n, rel(got[n], want[n]))
 
 
+def test_unused_outputs_have_no_gradient(B):
+    """One of two outputs used: the other's gradient is taken as zero."""
+    from chunked_gated_delta_08_amd import autograd as A
+    x, res, g = rnd(1, 40, 32).cuda(), rnd(2, 40, 32).cuda(), -torch.exp(rnd(3, 40, 32)).cuda()
+    w, d = 1 + 0.1 * rnd(4, 32).cuda(), rnd(5, 40, 32).cuda()
+    for pick in (0, 1):
+        a, b = x.clone().requires_grad_(), res.clone().requires_grad_()
+        (A.add_rms_norm(a, b, w)[pick] * d).sum().backward()
+        zero = torch.zeros_like(d)
+        f = B.add_norm_fwd(x, res, w)
+        r = B.add_norm_bwd(d if pick == 0 else zero, zero if pick == 0 else d, f["res"], w)
+        assert torch.equal(a.grad, r["dx"]) and torch.equal(b.grad, r["dres"])
+        a = x.clone().requires_grad_()
+        out = A.gated_linear_recurrence(a, g)[pick]
+        dd = d if pick == 0 else d[:1]
+        (out * dd).sum().backward()
+        f = B.glr_fwd(x, g, want_states=True)
+        r = B.glr_bwd(x, g, d if pick == 0 else zero, f["states"], dht=None if pick == 0 else dd.contiguous())
+        assert torch.equal(a.grad, r["dx"])
+
+
+# --------------------------------------------------------------- far offsets
+
+def test_far_offsets_norms(B):
+    """Rows beyond 2^32 bytes and 2^31 elements: the last ones are the ones a short call gives."""
+    D = 128
+    rows = (1 << 31) // D + 1000
+    x = torch.empty(rows, D, dtype=torch.bfloat16, device="cuda")
+    x.fill_(1.0)
+    x[-500:] = rnd(1, 500, D).bfloat16().cuda()
+    w = 1 + 0.1 * rnd(2, D).cuda()
+    y = B.gated_norm_fwd(x, x, w)
+    assert torch.equal(y[-500:], B.gated_norm_fwd(x[-500:].clone(), x[-500:].clone(), w))
+    del y
+    g = B.gated_norm_bwd(x, None, w, x)
+    assert torch.equal(g["dx"][-500:], B.gated_norm_bwd(x[-500:].clone(), None, w, x[-500:].clone())["dx"])
+    del g
+    f = B.add_norm_fwd(x, x, w)
+    assert torch.equal(f["y"][-500:], B.add_norm_fwd(x[-500:].clone(), x[-500:].clone(), w)["y"])
+    r = B.add_norm_bwd(x, x, f["res"], w)["dres"]
+    t = x[-500:].clone()
+    assert torch.equal(r[-500:], B.add_norm_bwd(t, t, f["res"][-500:].clone(), w)["dres"])
+
+
+def test_far_offsets_steps(B):
+    """Pools beyond 2^32 bytes and 2^31 elements."""
+    i = step_inputs(7, 3, 1, 2, 128, "f32", S=1)
+    S = (1 << 31) // (2 * 128 * 128) + 9
+    d = {k: t.cuda() for k, t in i.items()}
+    pool = torch.empty(S, 2, 128, 128, device="cuda")
+    slots = torch.tensor([S - 1, 0, S - 3], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = d["state"]
+    small = d["state"].expand(3, -1, -1, -1).contiguous()
+    args = [d[k] for k in ("q", "k", "v", "g", "beta")]
+    assert torch.equal(B.gdr_step(*args, pool, slots=slots), B.gdr_step(*args, small))
+    assert torch.equal(pool[slots.long()], small)
+    x, g = rnd(1, 3, 4099).cuda(), -torch.exp(rnd(2, 3, 4099)).cuda()
+    S = (1 << 31) // 4099 + 9
+    pool = pool.view(-1)[:S * 4099].view(S, 4099) if pool.numel() >= S * 4099 else torch.empty(S, 4099, device="cuda")
+    slots = torch.tensor([S - 1, 0, S - 3], dtype=torch.int32, device="cuda")
+    small = rnd(3, 3, 4099).cuda()
+    pool[slots.long()] = small
+    assert torch.equal(B.glr_step(x, g, pool, slots=slots), B.glr_step(x, g, small))
+    assert torch.equal(pool[slots.long()], small)
+
+
+def test_far_offsets_glr(B):
+    """Tokens times channels beyond 2^32 elements: the last tokens of a slab of channels, whose gates forget the rest,
+    are the ones that the slab alone gives.  The two calls cut the tokens into tiles differently: with gates of 0.4 and
+    |x| of 1 the states' magnitudes stay below 10, so they differ by less than 10 * 16 u * 5 tokens < 1e-4, and two
+    roundings to bf16 of such values by a step of 2^-8; dg is a product of two."""
+    T, D, n = 66000, 1 << 16, 300
+    x = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").fill_(1.0)
+    g = torch.empty(T, D, device="cuda").fill_(-0.5)
+    xs, gs = rnd(1, n, 200).bfloat16().cuda(), -torch.exp(rnd(2, n, 200)).cuda()
+    gs[0] = float("-inf")      # nothing from before reaches past here
+    x[-n:, -200:], g[-n:, -200:] = xs, gs
+    f = B.glr_fwd(x, g, want_states=True)
+    want = B.glr_fwd(xs, gs, want_states=True)
+    close("h", f["h"][-n:, -200:], f64(want["h"]), f64(want["h"]).abs() * 2.0 ** -8 + 1e-4)
+    close("ht", f["ht"][:, -200:], f64(want["ht"]), f64(want["ht"]).abs() * 1e-4 + 1e-5)
+    b = B.glr_bwd(x, g, x, f["states"], want_dh0=False)
+    bw = B.glr_bwd(xs, gs, xs, want["states"], want_dh0=False)
+    close("dx", b["dx"][-n:, -200:], f64(bw["dx"]), f64(bw["dx"]).abs() * 2.0 ** -8 + 1e-4)
+    close("dg", b["dg"][-n:, -200:], f64(bw["dg"]), f64(bw["dg"]).abs() * 1e-3 + 1e-4)
+
+
 # ------------------------------------------------- streams, graphs, workspaces
 
 def _everything(B, d, ws):
