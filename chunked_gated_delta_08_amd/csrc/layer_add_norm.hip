@@ -19,19 +19,8 @@ template <class E, class R, int VEC, int NV> struct Rows {   // a row as loaded:
 template <class T, int VEC, int TPR, int NV>
 __device__ __forceinline__ void load_row(Raw<T, VEC> (&r)[NV], const void* p, long off, int lane, int D) {
 #pragma unroll
-    for (int i = 0; i < NV; i++) load_raw<true>(r[i], (const T*)p + off, (i * TPR + lane) * VEC, D);
+    for (int i = 0; i < NV; i++) load_raw<TPR>(r[i], (const T*)p + off, i, lane, D);
 }
-template <int VEC, int TPR, int NV>
-__device__ __forceinline__ void load_weights(float (&w)[NV][VEC], const float* p, int lane, int D) {
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        Raw<float, VEC> t;
-        load_raw<false>(t, p, (i * TPR + lane) * VEC, D);
-#pragma unroll
-        for (int e = 0; e < VEC; e++) w[i][e] = t.v[e];
-    }
-}
-
 template <class E, class R, int VEC, int TPR, int NV, bool SCALE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void add_norm_fwd_kernel(NormArgs a) {
     constexpr int NT = TPR > 256 ? TPR : 256, GR = NT / TPR;
@@ -175,7 +164,7 @@ __global__ void zero_kernel(float* a, float* b, int n) {
 
 template <class E, class R> hipError_t add_fwd(const NormArgs& a, hipStream_t s) {
     constexpr int VEC = sizeof(R) == 4 ? 4 : 8;
-    return split_rows<64, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+    return split_rows<false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, NT = TPR > 256 ? TPR : 256;
         const dim3 grid(grid_rows(a.rows, NT / TPR, MAX_FWD_BLOCKS));
         if (a.scale) hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV, true>), grid, dim3(NT), 0, s, a);
@@ -188,7 +177,7 @@ template <class E, class R> hipError_t add_bwd(const NormArgs& a0, hipStream_t s
     constexpr int VEC = sizeof(R) == 4 ? 4 : 8;
     NormArgs a = a0;
     int blocks = 1;
-    const hipError_t e = split_rows<64, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+    const hipError_t e = split_rows<false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
         blocks = grid_rows(a.rows, BT / TPR, MAX_BWD_BLOCKS);
         if (blocks == 1 && !a.scale) a.part = a.dw;

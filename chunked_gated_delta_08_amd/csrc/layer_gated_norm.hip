@@ -27,23 +27,11 @@ __device__ __forceinline__ void load_rows(Rows<E, VEC, NV>& r, const NormArgs& a
     const long off = (row < a.rows ? row : a.rows - 1) * a.D;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const int c = (i * TPR + lane) * VEC;
-        load_raw<true>(r.x[i], (const E*)a.x + off, c, a.D);
-        if constexpr (GATE) load_raw<true>(r.z[i], (const E*)a.z + off, c, a.D);
-        if constexpr (BWD) load_raw<true>(r.g[i], (const E*)a.dy + off, c, a.D);
+        load_raw<TPR>(r.x[i], (const E*)a.x + off, i, lane, a.D);
+        if constexpr (GATE) load_raw<TPR>(r.z[i], (const E*)a.z + off, i, lane, a.D);
+        if constexpr (BWD) load_raw<TPR>(r.g[i], (const E*)a.dy + off, i, lane, a.D);
     }
 }
-template <int VEC, int TPR, int NV>
-__device__ __forceinline__ void load_weights(float (&w)[NV][VEC], const float* p, int lane, int D) {
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        Raw<float, VEC> t;
-        load_raw<false>(t, p, (i * TPR + lane) * VEC, D);
-#pragma unroll
-        for (int e = 0; e < VEC; e++) w[i][e] = t.v[e];
-    }
-}
-
 // One pass: many short-lived workgroups, whose next rows' loads overlap by themselves.
 template <class E, int VEC, int TPR, int NV, bool GATE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void gated_norm_fwd_kernel(NormArgs a) {
@@ -154,7 +142,7 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
 
 template <class E> hipError_t gated_fwd(const NormArgs& a, hipStream_t s) {
     constexpr int VEC = sizeof(E) == 4 ? 4 : 8;
-    return split_rows<8, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+    return split_rows<true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, NT = TPR > 256 ? TPR : 256;
         const dim3 grid(grid_rows(a.rows, NT / TPR, MAX_FWD_BLOCKS));
         if (a.z) hipLaunchKernelGGL((gated_norm_fwd_kernel<E, VEC, TPR, NV, true>), grid, dim3(NT), 0, s, a);
@@ -167,7 +155,7 @@ template <class E> hipError_t gated_bwd(const NormArgs& a0, hipStream_t s) {
     constexpr int VEC = sizeof(E) == 4 ? 4 : 8;
     NormArgs a = a0;
     int blocks = 1;
-    const hipError_t e = split_rows<8, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+    const hipError_t e = split_rows<true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
         blocks = grid_rows(a.rows, BT / TPR, MAX_BWD_BLOCKS);
         if (blocks == 1) a.part = a.dw;

@@ -24,18 +24,71 @@ template <class E, int VEC> struct Raw {
     typename VecU<E, VEC>::t v;   // as loaded; widened to fp32 where it is used
 };
 
-// VEC elements of a row from column c; columns past D read as zero.
-// NT: read once in the launch, not kept in the caches (what every row reads, the
-// weights, is: non-temporal reads of those doubled the add norm's backward).
-template <bool NT, class E, int VEC>
-__device__ __forceinline__ void load_raw(Raw<E, VEC>& r, const E* row, int c, int D) {
-    if (c + VEC <= D) {
-        auto p = (const typename VecU<E, VEC>::t*)(row + c);
-        r.v = NT ? __builtin_nontemporal_load(p) : *p;
+// 16 bytes moved down by `bytes` (uniform, below 16), zeros above.
+template <class V> __device__ __forceinline__ V move_down(V v, int bytes) {
+    static_assert(sizeof(V) == 16 || sizeof(V) == 8, "a vector load");
+    typedef unsigned long long u64;
+    u64 lo, hi = 0;
+    if constexpr (sizeof(V) == 16) {
+        u64 u[2];
+        __builtin_memcpy(u, &v, 16);
+        lo = u[0], hi = u[1];
+        if (bytes >= 8) lo = hi, hi = 0, bytes -= 8;
+        if (bytes > 0) lo = lo >> 8 * bytes | hi << (64 - 8 * bytes), hi >>= 8 * bytes;
+        u[0] = lo, u[1] = hi;
+        __builtin_memcpy(&v, u, 16);
+    } else {
+        __builtin_memcpy(&lo, &v, 8);
+        lo >>= 8 * bytes;
+        __builtin_memcpy(&v, &lo, 8);
+    }
+    return v;
+}
+
+// A lane's i-th VEC elements of a row of a stream; columns past D read as zero.
+// The vector that a row ends in is read from the row's last VEC elements and
+// moved down (one load for all lanes; element by element only where D < VEC).
+// Non-temporal: every element is read once in the launch.
+template <int TPR, class E, int VEC>
+__device__ __forceinline__ void load_raw(Raw<E, VEC>& r, const E* row, int i, int lane, int D) {
+    using V = typename VecU<E, VEC>::t;
+    const int rem = D % VEC, c = (i * TPR + lane) * VEC;
+    if (rem == 0 || D > VEC) {
+        const bool tail = c + VEC > D && c < D;
+        V v;
+#pragma unroll
+        for (int e = 0; e < VEC; e++) v[e] = (E)0.f;
+        if (c < D) v = __builtin_nontemporal_load((const V*)(row + (tail ? D - VEC : c)));
+        if (rem != 0 && (i + 1) * TPR * VEC > D) {   // the row ends here, in one of the lanes
+            const V m = move_down<V>(v, (VEC - rem) * (int)sizeof(E));
+            v = tail ? m : v;
+        }
+        r.v = v;
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; e++) r.v[e] = c + e < D ? row[c + e] : (E)0.f;
     }
+}
+// The same of a weight, which every row reads (non-temporal reads of those doubled
+// the add norm's backward).
+template <int VEC>
+__device__ __forceinline__ void load_weight(float (&w)[VEC], const float* p, int c, int D) {
+#pragma unroll
+    for (int e = 0; e < VEC; e++) w[e] = 0.f;
+    if (c + VEC <= D) {
+        const auto t = *(const typename VecU<float, VEC>::t*)(p + c);
+#pragma unroll
+        for (int e = 0; e < VEC; e++) w[e] = t[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e++)
+            if (c + e < D) w[e] = p[c + e];
+    }
+}
+template <int VEC, int TPR, int NV>
+__device__ __forceinline__ void load_weights(float (&w)[NV][VEC], const float* p, int lane, int D) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) load_weight<VEC>(w[i], p, (i * TPR + lane) * VEC, D);
 }
 template <class E, int VEC>
 __device__ __forceinline__ void store_vec(E* row, int c, int D, const float (&x)[VEC]) {
@@ -120,16 +173,24 @@ __device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* o
 }
 
 // Calls f(TPR, NV) for a row of nvt vectors: the smallest power of two of lanes
-// with one vector each, 1024 with two beyond.  MIN_TPR: rows as narrow as a part
-// of a wave are not split further than this.
-template <int MIN_TPR, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
+// with one vector each, 1024 with two beyond.  FINE: every power of two, and 16
+// lanes with three vectors each instead of a wave where those suffice (a wave
+// against 16 lanes at 2^18 rows of 257 bf16 elements: 124 and 106 us forward, 289 and 221
+// backward; 4 and 8 lanes with three each were slower than 16 and 32 with one);
+// else every second power below a wave.
+template <bool FINE, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
 #define LAYER_CASE(T, N) return f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
-    if constexpr (MIN_TPR < 64) {
+    if constexpr (FINE) {
         if (nvt <= 1) LAYER_CASE(1, 1);
         if (nvt <= 2) LAYER_CASE(2, 1);
         if (nvt <= 4) LAYER_CASE(4, 1);
         if (nvt <= 8) LAYER_CASE(8, 1);
         if (nvt <= 16) LAYER_CASE(16, 1);
+        if (nvt <= 32) LAYER_CASE(32, 1);
+        if (nvt <= 48) LAYER_CASE(16, 3);
+    } else {
+        if (nvt <= 2) LAYER_CASE(2, 1);
+        if (nvt <= 8) LAYER_CASE(8, 1);
         if (nvt <= 32) LAYER_CASE(32, 1);
     }
     if (nvt <= 64) LAYER_CASE(64, 1);
