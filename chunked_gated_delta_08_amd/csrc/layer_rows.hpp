@@ -90,17 +90,32 @@ __device__ __forceinline__ void load_weights(float (&w)[NV][VEC], const float* p
 #pragma unroll
     for (int i = 0; i < NV; i++) load_weight<VEC>(w[i], p, (i * TPR + lane) * VEC, D);
 }
+// N elements of x, from element O on, to p + O.
+template <int O, int N, class E, int VEC> __device__ __forceinline__ void store_part(E* p, const float (&x)[VEC]) {
+    if constexpr (O + N <= VEC) {
+        typename VecU<E, N>::t t;
+#pragma unroll
+        for (int e = 0; e < N; e++) t[e] = (E)x[O + e];
+        __builtin_nontemporal_store(t, (typename VecU<E, N>::t*)(p + O));
+    }
+}
+// VEC elements of a row from column c, those before D; the vector that an odd row
+// ends in in pieces of 4, 2 and 1.
 template <class E, int VEC>
 __device__ __forceinline__ void store_vec(E* row, int c, int D, const float (&x)[VEC]) {
+    E* p = row + c;
     if (c + VEC <= D) {
-        typename VecU<E, VEC>::t t;
-#pragma unroll
-        for (int e = 0; e < VEC; e++) t[e] = (E)x[e];
-        __builtin_nontemporal_store(t, (typename VecU<E, VEC>::t*)(row + c));
-    } else {
-#pragma unroll
-        for (int e = 0; e < VEC; e++)
-            if (c + e < D) row[c + e] = (E)x[e];
+        store_part<0, VEC>(p, x);
+    } else if (c < D) {
+        switch (D % VEC) {   // uniform
+            case 1: store_part<0, 1>(p, x); break;
+            case 2: store_part<0, 2>(p, x); break;
+            case 3: store_part<0, 2>(p, x); store_part<2, 1>(p, x); break;
+            case 4: store_part<0, 4>(p, x); break;
+            case 5: store_part<0, 4>(p, x); store_part<4, 1>(p, x); break;
+            case 6: store_part<0, 4>(p, x); store_part<4, 2>(p, x); break;
+            case 7: store_part<0, 4>(p, x); store_part<4, 2>(p, x); store_part<6, 1>(p, x); break;
+        }
     }
 }
 
@@ -175,7 +190,7 @@ __device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* o
 // Calls f(TPR, NV) for a row of nvt vectors: the smallest power of two of lanes
 // with one vector each, 1024 with two beyond.  FINE: every power of two, and 16
 // lanes with three vectors each instead of a wave where those suffice (a wave
-// against 16 lanes at 2^18 rows of 257 bf16 elements: 124 and 106 us forward, 289 and 221
+// against 16 lanes at 2^18 rows of 257 bf16 elements: 124 and 101 us forward, 289 and 208
 // backward; 4 and 8 lanes with three each were slower than 16 and 32 with one);
 // else every second power below a wave.
 template <bool FINE, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
