@@ -494,7 +494,9 @@ def bigdn_bwd(qkv, beta, decay, qw, kw, cos, sin, dout, F, S, k_scale=1.0, norm_
 # Layer operators (include/gdn_layer.h): gated RMSNorm, residual add with
 # RMSNorm, gated linear recurrence, single-token steps.  Every tensor of a call
 # is on one device, which need not be the current one; `stream` (default: that
-# device's current stream) belongs to it.  Preallocated outputs are checked like
+# device's current stream) belongs to it; where a call allocates its outputs or
+# workspace, that stream first waits for the current one, whose memory they may
+# reuse (give `out` and `workspace` to overlap the two).  Preallocated outputs are checked like
 # inputs; which of them may be an input's own buffer is said in the header.
 
 class NormProblem(ctypes.Structure):
@@ -547,16 +549,19 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 def _launch(dev, stream, temps, call, *args):
     """call(*args, stream handle) with `dev` current.  `temps`: tensors allocated for this
-    call on the current stream; the allocator is told when another one uses them."""
+    call on the current stream.  Another one that uses them waits for the current stream,
+    which may still work on that memory, and the allocator is told of it."""
     index = dev.index
     handle = _current_stream(index)
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
         if stream.cuda_stream != handle:
+            temps = [t for t in temps if t is not None]
+            if temps:
+                stream.wait_stream(torch.cuda.current_stream(dev))
             for t in temps:
-                if t is not None:
-                    t.record_stream(stream)
+                t.record_stream(stream)
         handle = stream.cuda_stream
     if _current_device() == index:
         code = call(*args, handle)
@@ -786,7 +791,8 @@ def glr_num_states(ntok):
 def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=True, want_states=False, out=None,
             workspace=None, stream=None, polls=0):
     """Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t over [B*T, D].  Returns dict
-    h (x's dtype), ht [N, D] fp32, states (for glr_bwd, when wanted).  Give
+    h (x's dtype), ht [N, D] fp32, states (for glr_bwd, when wanted).  Sums of g over
+    consecutive tokens must stay below 80.  Give
     cu_seqlens_host (the CPU copy of cu_seqlens) to avoid a copy and its wait."""
     N = check_glr_args(x, g, h0, cu_seqlens, cu_seqlens_host, B)
     ntok, D = x.shape

@@ -26,6 +26,20 @@
 // were its own (both give the same bits), and then begins its own again.  The
 // first segment that is not finished waits for nothing, so it is finished by
 // whoever has it, or by one that waits for it.
+// A product P of gates may overflow where the state itself would not, if gates
+// above 1 follow one another (include/gdn_layer.h bounds them); where it
+// underflows, what it multiplies is lost too.
+// Measured (bf16, D = 2048): one sequence of 32768 tokens 117 us forward, 4.6
+// TB/s of the 537 MB that it needs; 94 to 100 us with segments that do not wait
+// for one another (wrong results, the same traffic), so a fifth of the time is the
+// exchange: some 6 of the 17 us that a workgroup lives, two hops of 3.5 us from
+// one workgroup's store to another's load.  Forward and backward of twelve
+// sequences, 65536 tokens: 595 us (4.95 TB/s).  Without it, per step: whole rows
+// polled instead of one element 136 against 126 us; 8 tiles a segment against 12,
+// 125 against 118 us; a counter handing out segments (so that no workgroup could
+// wait for one that has not started) 6 to 8 % more, one per channel block 705
+// against 595 us forward and backward, since the blocks' rows then drift apart in
+// time; four channels a lane 165 us (168 registers).
 // The state is carried in fp32 throughout; h and dx are rounded once.  The
 // backward recomputes h_{t-1} from the states that the forward saved at every
 // tile, not from the rounded h: dg is an fp32 output.
@@ -135,7 +149,8 @@ template <int C> __device__ __forceinline__ void seq_row(const float* s, int n, 
 // Sequences without tokens before token t, at which one begins (or the end of
 // all): their output row is their input row.
 template <int C>
-__device__ __forceinline__ void pass_empty(const Seqs& q, int n, int t, const float* in, float* out, int D, unsigned ch) {
+__device__ __forceinline__ void pass_empty(const Seqs& q, int n, int t, const float* in, float* out, int D,
+                                           unsigned ch) {
     for (int m = n - 1; m >= 0 && q.first(m) == t; m--) {
         float v[C];
         seq_row<C>(in, m, D, ch, v);
@@ -189,8 +204,8 @@ template <int W, int C> using Maps = float[W][2][64 * C];
 // `cut`: the tile does not depend on what enters it.  Returns whether (P, H) so
 // composed does not.
 template <int W, int C>
-__device__ __forceinline__ bool tiles_before(Maps<W, C>& mp, Maps<W, C>& qi, unsigned* cuts, int w, bool cut, float (&P)[C],
-                                             float (&H)[C]) {
+__device__ __forceinline__ bool tiles_before(Maps<W, C>& mp, Maps<W, C>& qi, unsigned* cuts, int w, bool cut,
+                                             float (&P)[C], float (&H)[C]) {
     const int l = gdr::lane_o();
 #pragma unroll
     for (int c = 0; c < C; c++) mp[w][0][l * C + c] = P[c], mp[w][1][l * C + c] = H[c];
@@ -219,7 +234,6 @@ __device__ __forceinline__ void enter_tile(const Maps<W, C>& qi, unsigned cuts_b
         in[c] = cuts_before ? I : qi[w][0][l * C + c] * in[c] + I;
     }
 }
-
 
 // Waits until the maps at `a` and `b` (uniform; NULL: none) are there and leaves
 // them in LDS.  Both are read at once, so what is there costs one round trip; what
@@ -252,8 +266,9 @@ __device__ __forceinline__ bool await(const u64* a, const u64* b, unsigned ch, i
     const int l = gdr::lane_o();
 #pragma unroll
     for (int c = 0; c < C; c++) {
-        if (a) ea[w][0][l * C + c] = __uint_as_float((unsigned)(u[c] >> 32)), ea[w][1][l * C + c] = __uint_as_float((unsigned)u[c]);
-        if (b) eb[w][0][l * C + c] = __uint_as_float((unsigned)(v[c] >> 32)), eb[w][1][l * C + c] = __uint_as_float((unsigned)v[c]);
+        const int i = l * C + c;
+        if (a) ea[w][0][i] = __uint_as_float((unsigned)(u[c] >> 32)), ea[w][1][i] = __uint_as_float((unsigned)u[c]);
+        if (b) eb[w][0][i] = __uint_as_float((unsigned)(v[c] >> 32)), eb[w][1][i] = __uint_as_float((unsigned)v[c]);
     }
     return all;
 }
@@ -284,8 +299,9 @@ __device__ __forceinline__ void publish_row(u64* p, unsigned ch, const float (&P
 // that it waits for.
 template <int W, int C>
 __device__ __forceinline__ bool exchange(const Ws& ws, int idx, int nseg, int src, int D, unsigned ch, int w, int polls,
-                                         bool cut, const float (&P)[C], const float (&H)[C], Maps<W, C>& ea, Maps<W, C>& eb,
-                                         float (*tot)[64 * C], unsigned (*votes)[W], float (&in)[C]) {
+                                         bool cut, const float (&P)[C], const float (&H)[C], Maps<W, C>& ea,
+                                         Maps<W, C>& eb, float (*tot)[64 * C], unsigned (*votes)[W],
+                                         float (&in)[C]) {
     const int l = gdr::lane_o();
     const bool entered = src < idx, later = idx + 1 < nseg, tells = w == W - 1 && later;
     const bool closes = later && idx % G == G - 1;
@@ -358,9 +374,8 @@ __device__ __forceinline__ int first_missing(const Ws& ws, int idx, int D, unsig
 }
 
 // exp(g), off by at most (|g| + 3) 2^-24 of itself: the exponent's one rounding,
-// log2(e)'s, and two for exp2; zero below 2^-126.  The library's expf is within 2 2^-24, but its
-// range checks hold 64-bit masks for every element of the tile in scalar
-// registers, which then spill.  What the state loses to it is little: a token
+// log2(e)'s, and two for exp2; zero below 2^-126.  (expf is within 2 2^-24 at some
+// ten operations instead of two.)  What the state loses to it is little: a token
 // with a large |g| hardly passes the state on, and over the tokens that do the
 // |g| add up to about one.
 __device__ __forceinline__ float gate(float g) { return __builtin_amdgcn_exp2f(1.44269504f * g); }
@@ -421,7 +436,8 @@ __device__ __forceinline__ void store_nt(E* row, unsigned ch, typename VecU<E, C
 }
 
 template <class E, int C, int W>
-__global__ __launch_bounds__(64 * W, sizeof(E) == 4 ? 4 : 6) void glr_fwd_kernel(GlrArgs a, int nblk, int nseg, bool chain) {
+__global__ __launch_bounds__(64 * W, sizeof(E) == 4 ? 4 : 6) void glr_fwd_kernel(GlrArgs a, int nblk, int nseg,
+                                                                               bool chain) {
     static_assert(G <= W, "one wave reads one map of a row");
     constexpr int SEG = W * L;   // tokens of a segment
     __shared__ Maps<W, C> mp, ea, eb, qi;
@@ -475,7 +491,8 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 4 ? 4 : 6) void glr_fwd_kernel
         bool got = true;
         if (chain) {
             const int s0 = q.first(q.of(T0));   // where the sequence that enters began
-            got = exchange<W, C>(ws, seg, nseg, s0 < T0 ? s0 / SEG : seg, D, ch, w, a.polls, cut, P, H, ea, eb, tot, votes,
+            const int from = s0 < T0 ? s0 / SEG : seg;
+            got = exchange<W, C>(ws, seg, nseg, from, D, ch, w, a.polls, cut, P, H, ea, eb, tot, votes,
                               in);
         }
         if (got && tile.nt > 0) {
@@ -489,7 +506,8 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 4 ? 4 : 6) void glr_fwd_kernel
             for (int i = 0; i < L; i++, out += D) {
                 if (begins >> i & 1) {
                     if (i > 0) {
-                        if (a.ht) store_row<C>(gdr::at32(a.ht + (long)n * D, ch), in);   // the state that the sequence ends with
+                        // the state that the sequence ends with
+                        if (a.ht) store_row<C>(gdr::at32(a.ht + (long)n * D, ch), in);
                         n = q.next(n);
                     }
                     if (a.ht) pass_empty<C>(q, n, tile.t0 + i, a.h0, a.ht, D, ch);
@@ -595,8 +613,8 @@ __global__ __launch_bounds__(64 * W, 4) void glr_bwd_kernel(GlrArgs a, int nblk,
         bool got = true;
         if (chain) {
             const int e0 = q.first(q.of(T1 - 1) + 1);   // where the sequence that enters from the right ends
-            got = exchange<W, C>(ws, idx, nseg, e0 > T1 ? nseg - 1 - (e0 - 1) / SEG : idx, D, ch, pw, a.polls, cut, P, M, ea,
-                              eb, tot, votes, in);
+            const int from = e0 > T1 ? nseg - 1 - (e0 - 1) / SEG : idx;
+            got = exchange<W, C>(ws, idx, nseg, from, D, ch, pw, a.polls, cut, P, M, ea, eb, tot, votes, in);
         }
         if (got && tile.nt > 0) {
             as_loaded<E, C>(dh);

@@ -8,6 +8,9 @@
 // backward (x^2 and dn x) need no r, so it has one reduction per row too.  dw
 // stays in registers over all rows of a persistent workgroup; the workgroups'
 // partial sums are joined in a fixed order by a second launch.
+// Measured (bf16, D = 128): 2^19 rows forward 67 us (6.0 TB/s of 403 MB), 2^21 rows
+// backward 519 us (5.2 TB/s of 2.68 GB, a large copy's rate); 128 rows 3 us, which
+// is the launch.
 #include "layer_rows.hpp"
 
 namespace layer {
@@ -135,7 +138,8 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
             }
         }
         if constexpr (NV == 1) in = next;
-        else load_rows<E, VEC, TPR, NV, GATE, true>(in, a, r0 + (long)gridDim.x * GR + grp, lane);   // no registers to read ahead
+        else   // no registers to read ahead
+            load_rows<E, VEC, TPR, NV, GATE, true>(in, a, r0 + (long)gridDim.x * GR + grp, lane);
     }
     write_part<VEC, TPR, NV, BT>(dw, a.part + (long)blockIdx.x * D, D, lds);
 }
@@ -159,7 +163,8 @@ template <class E> hipError_t gated_bwd(const NormArgs& a0, hipStream_t s) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
         blocks = grid_rows(a.rows, BT / TPR, MAX_BWD_BLOCKS);
         if (blocks == 1) a.part = a.dw;
-        if (a.z) hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
+        if (a.z)
+            hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
         else hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);
         return hipGetLastError();
     });

@@ -6,6 +6,9 @@ Subcommands (run with ``python -m chunked_gated_delta_08_amd.profiling``):
       Runs a plain elementwise device copy of known size (reads M MiB, writes M
       MiB, fp32, ``torch.mul(src, 1, out=dst)``) a few times: the calibration
       kernel for the FETCH_SIZE / WRITE_SIZE counters.
+  layer --case NAME [--reps R]
+      Runs one listed case of perf/operators.py (an operator of the layer around
+      the gated delta rule) R times over three sets of inputs.
   stats --csv <prefix>_kernel_stats.csv --out <txt> --cmd "<command>"
       Writes a short text table of per-kernel dispatch counts and durations.
   traffic --fetch CSV --write CSV --copy-fetch CSV --copy-write CSV
@@ -50,6 +53,14 @@ _BIGDN = [_CS + "bigdn.hip", _CS + "bigdn_launch.hpp"] + _COMMON
 for _k in ("bigdn_stats_kernel", "bigdn_phase_a_kernel", "bigdn_scan_kernel", "bigdn_phase_c_kernel",
            "bigdn_abar_kernel", "bigdn_rms_bwd_kernel", "bigdn_wsum_kernel"):
     KERNEL_SOURCES[_k] = _BIGDN
+_ROWS = [_CS + "layer_rows.hpp", _CS + "layer_launch.hpp"] + _COMMON
+for _k, _f in (("gated_norm_fwd_kernel", "layer_gated_norm"), ("gated_norm_bwd_kernel", "layer_gated_norm"),
+               ("add_norm_fwd_kernel", "layer_add_norm"), ("add_norm_bwd_kernel", "layer_add_norm"),
+               ("norm_wsum_kernel", "layer_add_norm")):
+    KERNEL_SOURCES[_k] = [_CS + _f + ".hip"] + _ROWS
+for _k, _f in (("glr_fwd_kernel", "glr"), ("glr_bwd_kernel", "glr"), ("glr_clear_kernel", "glr"),
+               ("gdr_step_kernel", "layer_step"), ("glr_step_kernel", "layer_step")):
+    KERNEL_SOURCES[_k] = [_CS + _f + ".hip", _CS + "layer_launch.hpp"] + _COMMON
 
 
 def _code_of(text):
@@ -91,6 +102,22 @@ def _copy(args):
         torch.mul(src, 1.0, out=dst)
     torch.cuda.synchronize()
     print(f"copy: {args.reps} x {args.mib} MiB read + {args.mib} MiB written", flush=True)
+
+
+def _layer(args):
+    import importlib.util
+    import torch
+    sys.path.insert(0, ROOT)
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    cases = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(cases)
+    cases.own = True
+    case = {c["name"]: c for c in cases.listed()}[args.case]
+    states = [cases.prepare(case, seed) for seed in range(3)]
+    for i in range(args.reps):
+        cases.run(states[i % 3])
+    torch.cuda.synchronize()
+    print(f"layer: {args.case} x {args.reps}, work {cases.work(case)}", flush=True)
 
 
 def _stats(args):
@@ -166,6 +193,9 @@ def main(argv=None):
     c = sub.add_parser("copy")
     c.add_argument("--mib", type=int, default=1024)
     c.add_argument("--reps", type=int, default=3)
+    y = sub.add_parser("layer")
+    y.add_argument("--case", required=True)
+    y.add_argument("--reps", type=int, default=12)
     s = sub.add_parser("stats")
     s.add_argument("--csv", required=True)
     s.add_argument("--out", required=True)
@@ -176,7 +206,7 @@ def main(argv=None):
         t.add_argument(a, required=True)
     t.add_argument("--copy-mib", type=int, default=1024)
     args = ap.parse_args(argv)
-    {"copy": _copy, "stats": _stats, "traffic": _traffic}[args.cmd_name](args)
+    {"copy": _copy, "layer": _layer, "stats": _stats, "traffic": _traffic}[args.cmd_name](args)
 
 
 if __name__ == "__main__":

@@ -118,7 +118,10 @@ size_t glr_workspace_size(const glr_problem *p);
 
 /*
  * glr_fwd -- h_t = exp(g_t) h_{t-1} + x_t in each sequence, channel by channel.
- *   x [B*T, D] dtype    g [B*T, D] fp32  the log-gate, any value (-inf: the state is dropped)
+ *   x [B*T, D] dtype
+ *   g [B*T, D] fp32     the log-gate, as a rule <= 0 (-inf: the state is dropped).  Values above 0 are
+ *                       taken, but the sum of g over consecutive tokens of a sequence must stay
+ *                       below 80: products of gates are formed over up to 12288 tokens in fp32
  *   h0 [N, D] fp32      states before the first tokens, NULL = zero
  * Outputs:
  *   h [B*T, D] dtype

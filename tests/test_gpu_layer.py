@@ -350,6 +350,20 @@ def test_glr_long(B):
     assert all(torch.equal(f[k], f2[k]) for k in f) and all(torch.equal(b[k], b2[k]) for k in b)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_glr_gates_above_one(B, dtype):
+    """Log-gates of both signs whose sum over a sequence reaches some 45: products of gates grow to e^45."""
+    lens, D = [9000], 70
+    x, dh = rnd(1, 9000, D).to(DT[dtype]), rnd(2, 9000, D).to(DT[dtype])
+    g = 0.005 + 0.05 * rnd(3, 9000, D)
+    ref, err = glr_ref(x, g, None, lens, dh)
+    f = B.glr_fwd(x.cuda(), g.cuda(), want_states=True)
+    b = B.glr_bwd(x.cuda(), g.cuda(), dh.cuda(), f["states"])
+    for k, v in {"h": f["h"], "ht": f["ht"], **b}.items():
+        t = dtype if k in ("h", "dx") else "f32"
+        close(k, v, ref[k], err[k] + half(t) * ref[k].abs() + TINY[t])
+
+
 @pytest.mark.parametrize("lens,D", [([3000], 130), ([700, 1, 0, 1500, 40], 64), ([9000], 2)])
 def test_glr_without_patience(B, lens, D):
     """Workgroups that hardly look for the others' results before they compute them themselves give the same bits."""
@@ -861,3 +875,21 @@ def test_given_stream(B):
         del junk
         assert all(torch.equal(got[k], want[k]) for k in want)
         assert all(torch.equal(gotb[k], wantb[k]) for k in wantb)
+
+
+def test_given_stream_waits_for_what_it_allocates(B):
+    """What the call allocates was just freed on the current stream, which still writes there."""
+    d, _ = _state(B, T=20000, D=512)
+    want = B.gated_norm_bwd(d["x"], d["z"], d["w"], d["dy"])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = [torch.empty_like(d["x"]) for _ in range(4)]
+        for _ in range(100):
+            for t in old:
+                t.fill_(7.0)
+        del old, t
+        got = B.gated_norm_bwd(d["x"], d["z"], d["w"], d["dy"], stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want)
+        del got
