@@ -130,33 +130,37 @@ __global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
         else   // no registers to read ahead
             load_rows<E, R, VEC, TPR, NV, SCALE>(in, a, r0 + (long)gridDim.x * GR + grp, lane);
     }
-    float* part = a.part + (long)blockIdx.x * D * (SCALE ? 2 : 1);
-    write_part<VEC, TPR, NV, BT>(dw, part, D, lds);
-    if constexpr (SCALE) write_part<VEC, TPR, NV, BT>(ds, part + D, D, lds);
+    const long at = (long)blockIdx.x * a.pitch;
+    write_part<VEC, TPR, NV, BT>(dw, a.part + at, D, lds);
+    if constexpr (SCALE) write_part<VEC, TPR, NV, BT>(ds, a.part_s + at, D, lds);
 }
 
 // out[c] = sum over the partial rows in a fixed order: 16 columns per
-// workgroup, 64 row slices, joined pairwise.  Column c < D goes to dw, the
-// others to dscale.
+// workgroup, 64 row slices, joined pairwise within a wave, then over the waves.
+// Column c < D goes to dw, the others to dscale.
 __global__ __launch_bounds__(1024) void norm_wsum_kernel(const float* part, int blocks, int n, int D, float* dw,
                                                          float* dscale) {
-    __shared__ float lds[64][17];
-    const int c = blockIdx.x * 16 + (threadIdx.x & 15), sl = threadIdx.x >> 4;
-    float t = 0.f;
-    if (c < n)
-        for (int b = sl; b < blocks; b += 64) t += part[(long)b * n + c];
-    lds[sl][threadIdx.x & 15] = t;
-    __syncthreads();
-    for (int m = 32; m >= 1; m /= 2) {
-        if (sl < m) lds[sl][threadIdx.x & 15] += lds[sl + m][threadIdx.x & 15];
-        __syncthreads();
+    __shared__ float lds[16][17];
+    const int k = threadIdx.x & 15, c = blockIdx.x * 16 + k, sl = threadIdx.x >> 4;
+    float v[MAX_BWD_BLOCKS / 64], t = 0.f;   // all loads on their way at once
+#pragma unroll
+    for (int i = 0; i < MAX_BWD_BLOCKS / 64; i++) {
+        const int b = sl + 64 * i;
+        v[i] = b < blocks && c < n ? part[(long)b * n + c] : 0.f;
     }
-    if (sl == 0 && c < n) {
-        if (c < D) dw[c] = lds[0][threadIdx.x & 15];
-        else dscale[c - D] = lds[0][threadIdx.x & 15];
+#pragma unroll
+    for (int i = 0; i < MAX_BWD_BLOCKS / 64; i++) t += v[i];
+    t += __shfl_xor(t, 16);
+    t += __shfl_xor(t, 32);
+    if ((threadIdx.x & 63) < 16) lds[threadIdx.x >> 6][k] = t;
+    __syncthreads();
+    if (threadIdx.x < 16 && c < n) {
+        t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; i++) t += lds[i][k];
+        (c < D ? dw[c] : dscale[c - D]) = t;
     }
 }
-
 
 __global__ void zero_kernel(float* a, float* b, int n) {
     const int i = blockIdx.x * 256 + threadIdx.x;
@@ -182,27 +186,36 @@ template <class E, class R> hipError_t add_bwd(const NormArgs& a0, hipStream_t s
     int blocks = 1;
     const hipError_t e = split_rows<false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
-        blocks = grid_rows(a.rows, BT / TPR, MAX_BWD_BLOCKS);
-        if (blocks == 1 && !a.scale) a.part = a.dw;
+        blocks = bwd_blocks(a, BT / TPR);
         if (a.scale)
             hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
         else
             hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);
         return hipGetLastError();
     });
-    return e != hipSuccess ? e : norm_wsum(a, blocks, a.D * (a.scale ? 2 : 1), s);
+    return e != hipSuccess ? e : norm_wsum(a, blocks, s);
 }
 
 }  // namespace
 
-size_t norm_part_floats(long rows, int D) {   // at least one row of partial sums per workgroup of BT / 512 rows or more
-    return (size_t)grid_rows(rows > 0 ? rows : 1, 1, MAX_BWD_BLOCKS) * D * 2;
+// Enough for every type and both norms: with vectors of 4 a row has the most lanes,
+// and a workgroup the fewest rows at a time.
+size_t norm_part_floats(long rows, int D) {
+    int per = 1;
+    (void)split_rows<false, 4>((D + 3) / 4, [&](auto T, auto) {
+        constexpr int TPR = decltype(T)::value;
+        per = (TPR > BWD_THREADS ? TPR : BWD_THREADS) / TPR;
+        return hipSuccess;
+    });
+    const long n = (rows + per - 1) / per;
+    if (n <= SOLO) return 0;
+    return (size_t)grid_rows(rows, 1, MAX_BWD_BLOCKS) * D * 2;
 }
 
-hipError_t norm_wsum(const NormArgs& a, int blocks, int n, hipStream_t s) {
-    if (blocks == 1 && n == a.D) return hipSuccess;   // the only workgroup wrote dw itself
-    hipLaunchKernelGGL(norm_wsum_kernel, dim3((n + 15) / 16), dim3(1024), 0, s, a.part, blocks, n, a.D, a.dw,
-                       a.dscale);
+hipError_t norm_wsum(const NormArgs& a, int blocks, hipStream_t s) {
+    if (blocks == 1) return hipSuccess;
+    hipLaunchKernelGGL(norm_wsum_kernel, dim3((a.pitch + 15) / 16), dim3(1024), 0, s, a.part, blocks, a.pitch, a.D,
+                       a.dw, a.dscale);
     return hipGetLastError();
 }
 hipError_t norm_zero_grads(const NormArgs& a, hipStream_t s) {   // no rows: the column sums are zero

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
         else   // no registers to read ahead
             load_rows<E, VEC, TPR, NV, GATE, true>(in, a, r0 + (long)gridDim.x * GR + grp, lane);
     }
-    write_part<VEC, TPR, NV, BT>(dw, a.part + (long)blockIdx.x * D, D, lds);
+    write_part<VEC, TPR, NV, BT>(dw, a.part + (long)blockIdx.x * a.pitch, D, lds);
 }
 
 template <class E> hipError_t gated_fwd(const NormArgs& a, hipStream_t s) {
@@ -161,14 +161,13 @@ template <class E> hipError_t gated_bwd(const NormArgs& a0, hipStream_t s) {
     int blocks = 1;
     const hipError_t e = split_rows<true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
-        blocks = grid_rows(a.rows, BT / TPR, MAX_BWD_BLOCKS);
-        if (blocks == 1) a.part = a.dw;
+        blocks = bwd_blocks(a, BT / TPR);
         if (a.z)
             hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
         else hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);
         return hipGetLastError();
     });
-    return e != hipSuccess ? e : norm_wsum(a, blocks, a.D, s);
+    return e != hipSuccess ? e : norm_wsum(a, blocks, s);
 }
 
 }  // namespace

@@ -18,8 +18,9 @@ struct NormArgs {
     const void* res; const void* dy; const void* dres;
     void* y; void* res_out;       // forward
     void* dx; void* dz; void* dres_out;
-    float* part;                  // backward: [blocks][1 or 2][D] partial column sums
     float* dw; float* dscale;
+    float* part; float* part_s;   // backward: the workgroups' column sums for dw and dscale, `pitch` floats apart
+    int pitch;
 };
 
 // Floats of `part` that either backward may use.

@@ -232,8 +232,24 @@ inline int grid_rows(long rows, int per, long most) {
     return (int)(n < most ? n : most);
 }
 
-// Joins the backward's partial column sums (layer_add_norm.hip).
-hipError_t norm_wsum(const NormArgs& a, int blocks, int n, hipStream_t s);
+// Workgroups of a backward whose workgroups take `per` rows at a time, and where
+// they leave their column sums: one workgroup writes dw and dscale itself and takes
+// up to SOLO times `per` rows, which spares the launch that joins them and the
+// workspace (us on the GPU alone and with the second launch, add norm D = 4096 fp32:
+// 1 row 5.6 and 8.2, 4 rows 12.1 and 9.1; gated norm D = 128: 64 rows, two turns,
+// 6.1 and 7.0, 128 rows 8.8 and 7.1); else every workgroup has about as many rows as
+// the others.
+constexpr int SOLO = 2;
+inline int bwd_blocks(NormArgs& a, int per) {
+    const long n = (a.rows + per - 1) / per, turns = n <= SOLO ? n : (n + MAX_BWD_BLOCKS - 1) / MAX_BWD_BLOCKS;
+    const int blocks = (int)((n + turns - 1) / turns);
+    a.pitch = a.scale ? 2 * a.D : a.D;
+    if (blocks == 1) a.part = a.dw, a.part_s = a.dscale;
+    else a.part_s = a.part + a.D;
+    return blocks;
+}
+// Joins them in a second launch (layer_add_norm.hip).
+hipError_t norm_wsum(const NormArgs& a, int blocks, hipStream_t s);
 hipError_t norm_zero_grads(const NormArgs& a, hipStream_t s);
 
 }  // namespace layer

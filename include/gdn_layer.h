@@ -45,7 +45,8 @@ typedef struct norm_problem {
     gdn_act act;         /* gated norm: the gate's function; not read by the add norm */
 } norm_problem;
 
-/* Bytes of workspace gated_norm_bwd and add_norm_bwd need; 0 if the problem is invalid. */
+/* Bytes of workspace gated_norm_bwd and add_norm_bwd need; 0 if the problem is invalid or so small that they
+ * need none. */
 size_t norm_workspace_size(const norm_problem *p);
 
 /*
