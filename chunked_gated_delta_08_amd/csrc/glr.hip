@@ -36,10 +36,10 @@
 // one workgroup's store to another's load.  Forward and backward of twelve
 // sequences, 65536 tokens: 595 us (4.95 TB/s).  Without it, per step: whole rows
 // polled instead of one element 136 against 126 us; 8 tiles a segment against 12,
-// 125 against 118 us; a counter handing out segments (so that no workgroup could
+// 126 against 118 us; a counter handing out segments (so that no workgroup could
 // wait for one that has not started) 6 to 8 % more, one per channel block 705
 // against 595 us forward and backward, since the blocks' rows then drift apart in
-// time; four channels a lane 165 us (168 registers).
+// time; four channels a lane 190 against 140 us (154 registers, one workgroup a CU).
 // The state is carried in fp32 throughout; h and dx are rounded once.  The
 // backward recomputes h_{t-1} from the states that the forward saved at every
 // tile, not from the rounded h: dg is an fp32 output.
@@ -492,8 +492,7 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 4 ? 4 : 6) void glr_fwd_kernel
         if (chain) {
             const int s0 = q.first(q.of(T0));   // where the sequence that enters began
             const int from = s0 < T0 ? s0 / SEG : seg;
-            got = exchange<W, C>(ws, seg, nseg, from, D, ch, w, a.polls, cut, P, H, ea, eb, tot, votes,
-                              in);
+            got = exchange<W, C>(ws, seg, nseg, from, D, ch, w, a.polls, cut, P, H, ea, eb, tot, votes, in);
         }
         if (got && tile.nt > 0) {
             as_loaded<E, C>(x);
