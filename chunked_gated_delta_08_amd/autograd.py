@@ -12,6 +12,10 @@ step runs in the library's kernels.
 Layouts follow the C ABI (token axis flattened over the batch):
   q, k [B*T, HK, K]   v [B*T, HV, V]   g (raw log-gate) [B*T, HV] fp32
   beta [B*T, HV]      initial_state [N, HV, K, V] fp32
+
+A training step may be captured into a graph (give cu_seqlens_host, so that nothing
+is copied to the host).  Let go of the outputs of earlier eager passes over the same
+leaves first: torch ties a leaf's gradient to the stream of the graph that is alive.
 """
 import torch
 

@@ -893,3 +893,83 @@ def test_given_stream_waits_for_what_it_allocates(B):
         torch.cuda.synchronize()
         assert all(torch.equal(got[k], want[k]) for k in want)
         del got
+
+
+def _capture(run):
+    """run() warmed up on a side stream and captured there; returns the graph and what run() gave."""
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+        with torch.cuda.graph(graph, stream=side):
+            out = run()
+    torch.cuda.current_stream().wait_stream(side)
+    return graph, out
+
+
+def test_captured_training_step(B):
+    """Forward and backward through autograd in one graph: on new inputs the eager bits each time."""
+    from chunked_gated_delta_08_amd import autograd as A
+    T, D = 700, 130
+    cu = torch.tensor([0, 1, 1, 400, T], dtype=torch.int32)
+    dev = cu.cuda()
+    rows = {n: rnd(i, T, D).cuda().requires_grad_() for i, n in enumerate("xrgz")}
+    vecs = {n: (1 + 0.1 * rnd(9 + i, D)).cuda().requires_grad_() for i, n in enumerate("wsv")}
+    dy, dr = rnd(20, T, D).cuda(), rnd(21, T, D).cuda()
+
+    def run():
+        y, res = A.add_rms_norm(rows["x"], rows["r"], vecs["w"], vecs["s"])
+        h, _ = A.gated_linear_recurrence(y, -torch.exp(rows["g"]), cu_seqlens=dev, cu_seqlens_host=cu)
+        o = A.gated_rms_norm(h, rows["z"], vecs["v"])
+        grads = torch.autograd.grad((o, res), [*rows.values(), *vecs.values()], (dy, dr))
+        return (o.detach(), res.detach()) + grads   # no autograd graph outlives its pass
+    graph, out = _capture(run)
+    for i in range(4):
+        with torch.no_grad():
+            for n, t in enumerate(rows.values()):
+                t.copy_(rnd(100 + 10 * i + n, T, D))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_captured_decoding(B):
+    """A decode step of a layer in one graph, replayed token by token while sequences come and go: states and
+    outputs as eager steps give them."""
+    N, H, K, D = 5, 2, 64, 128
+    t = dict(x=torch.zeros(N, D), q=torch.zeros(N, H, K), k=torch.zeros(N, H, K), g=torch.zeros(N, H),
+             beta=torch.zeros(N, H), a=torch.zeros(N, D))
+    t = {n: v.cuda() for n, v in t.items()}
+    slots = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    w, wn = (1 + 0.1 * rnd(1, D)).cuda(), (1 + 0.1 * rnd(2, K)).cuda()
+    pool, diag = torch.zeros(7, H, K, K, device="cuda"), torch.zeros(7, D, device="cuda")
+
+    def run():
+        f = B.add_norm_fwd(t["x"], t["a"], w)
+        o = B.gdr_step(t["q"], t["k"], f["y"].view(N, H, K), t["g"], t["beta"], pool, slots)
+        o = B.gated_norm_fwd(o, f["y"].view(N, H, K), wn)
+        return o, B.glr_step(o.view(N, D), -f["res"].abs(), diag, slots)
+    graph, out = _capture(run)
+    want_pool, want_diag = rnd(3, 7, H, K, K).cuda(), rnd(4, 7, D).cuda()
+    pool.copy_(want_pool)
+    diag.copy_(want_diag)
+    for i, s in enumerate(([0, 1, 2, -1, -1], [0, 2, 6, 5, 3], [6, 0, 0, 1, 7], [-1] * 5, [4, 3, 2, 1, 0])):
+        for n, (name, v) in enumerate(t.items()):
+            v.copy_(rnd(50 + 10 * i + n, *v.shape) * (-1 if name == "g" else 1))
+        t["g"].copy_(-t["g"].abs())
+        t["k"].copy_(torch.nn.functional.normalize(t["k"], dim=-1))
+        t["beta"].sigmoid_()
+        slots.copy_(torch.tensor(s, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got, have = [v.clone() for v in out], (pool.clone(), diag.clone())
+        pool.copy_(want_pool)
+        diag.copy_(want_diag)
+        want = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(have[0], pool) and torch.equal(have[1], diag)
+        want_pool, want_diag = pool.clone(), diag.clone()
