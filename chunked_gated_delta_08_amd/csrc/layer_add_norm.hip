@@ -186,7 +186,7 @@ template <class E, class R> hipError_t add_bwd(const NormArgs& a0, hipStream_t s
     int blocks = 1;
     const hipError_t e = split_rows<false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
-        blocks = bwd_blocks(a, BT / TPR);
+        blocks = bwd_blocks(a, BT / TPR, BT);
         if (a.scale)
             hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
         else

@@ -161,7 +161,7 @@ template <class E> hipError_t gated_bwd(const NormArgs& a0, hipStream_t s) {
     int blocks = 1;
     const hipError_t e = split_rows<true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
-        blocks = bwd_blocks(a, BT / TPR);
+        blocks = bwd_blocks(a, BT / TPR, BT);
         if (a.z)
             hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
         else hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);

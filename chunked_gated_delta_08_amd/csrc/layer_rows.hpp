@@ -238,10 +238,16 @@ inline int grid_rows(long rows, int per, long most) {
 // workspace (us on the GPU alone and with the second launch, add norm D = 4096 fp32:
 // 1 row 5.6 and 8.2, 4 rows 12.1 and 9.1; gated norm D = 128: 64 rows, two turns,
 // 6.1 and 7.0, 128 rows 8.8 and 7.1); else every workgroup has about as many rows as
-// the others.
-constexpr int SOLO = 2;
-inline int bwd_blocks(NormArgs& a, int per) {
-    const long n = (a.rows + per - 1) / per, turns = n <= SOLO ? n : (n + MAX_BWD_BLOCKS - 1) / MAX_BWD_BLOCKS;
+// the others.  Half of MAX_BWD_BLOCKS where that many fill the chip (workgroups of
+// 1024) and up to 1024 turns in all, since each workgroup's sums are 8 D bytes to
+// write and to read again (512 and 256, add norm bf16: 300 x 4096 19.4 and 14.7 us, 900
+// x 2048 17.0 and 14.1, fp32 residual 2400 x 4096 52.6 and 46.1; fp32 1313 x 1024 15.1
+// and 16.4, 8192 x 8192 320 and 326).
+constexpr int SOLO = 2, FEW = 1024;
+inline int bwd_blocks(NormArgs& a, int per, int threads) {
+    const long n = (a.rows + per - 1) / per;
+    const long most = threads > BWD_THREADS || n <= FEW ? MAX_BWD_BLOCKS / 2 : MAX_BWD_BLOCKS;
+    const long turns = n <= SOLO ? n : (n + most - 1) / most;
     const int blocks = (int)((n + turns - 1) / turns);
     a.pitch = a.scale ? 2 * a.D : a.D;
     if (blocks == 1) a.part = a.dw, a.part_s = a.dscale;
