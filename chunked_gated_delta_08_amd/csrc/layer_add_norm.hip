@@ -171,7 +171,7 @@ __global__ void zero_kernel(float* a, float* b, int n) {
 
 template <class E, class R> hipError_t add_fwd(const NormArgs& a, hipStream_t s) {
     constexpr int VEC = sizeof(R) == 4 ? 4 : 8;
-    return split_rows<false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+    return split_rows<false, false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, NT = TPR > 256 ? TPR : 256;
         const dim3 grid(grid_rows(a.rows, NT / TPR, MAX_FWD_BLOCKS));
         if (a.scale) hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV, true>), grid, dim3(NT), 0, s, a);
@@ -184,9 +184,9 @@ template <class E, class R> hipError_t add_bwd(const NormArgs& a0, hipStream_t s
     constexpr int VEC = sizeof(R) == 4 ? 4 : 8;
     NormArgs a = a0;
     int blocks = 1;
-    const hipError_t e = split_rows<false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+    const hipError_t e = split_rows<false, true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
-        blocks = bwd_blocks(a, BT / TPR, BT);
+        blocks = bwd_blocks(a, BT / TPR, TPR * NV > 512);
         if (a.scale)
             hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
         else
@@ -202,7 +202,7 @@ template <class E, class R> hipError_t add_bwd(const NormArgs& a0, hipStream_t s
 // and a workgroup the fewest rows at a time.
 size_t norm_part_floats(long rows, int D) {
     int per = 1;
-    (void)split_rows<false, 4>((D + 3) / 4, [&](auto T, auto) {
+    (void)split_rows<false, true, 4>((D + 3) / 4, [&](auto T, auto) {
         constexpr int TPR = decltype(T)::value;
         per = (TPR > BWD_THREADS ? TPR : BWD_THREADS) / TPR;
         return hipSuccess;

@@ -146,7 +146,7 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
 
 template <class E> hipError_t gated_fwd(const NormArgs& a, hipStream_t s) {
     constexpr int VEC = sizeof(E) == 4 ? 4 : 8;
-    return split_rows<true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+    return split_rows<true, false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, NT = TPR > 256 ? TPR : 256;
         const dim3 grid(grid_rows(a.rows, NT / TPR, MAX_FWD_BLOCKS));
         if (a.z) hipLaunchKernelGGL((gated_norm_fwd_kernel<E, VEC, TPR, NV, true>), grid, dim3(NT), 0, s, a);
@@ -159,9 +159,9 @@ template <class E> hipError_t gated_bwd(const NormArgs& a0, hipStream_t s) {
     constexpr int VEC = sizeof(E) == 4 ? 4 : 8;
     NormArgs a = a0;
     int blocks = 1;
-    const hipError_t e = split_rows<true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
+    const hipError_t e = split_rows<true, true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
-        blocks = bwd_blocks(a, BT / TPR, BT);
+        blocks = bwd_blocks(a, BT / TPR, TPR * NV > 512);
         if (a.z)
             hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
         else hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);

@@ -188,12 +188,17 @@ __device__ __forceinline__ void write_part(const float (&acc)[NV][VEC], float* o
 }
 
 // Calls f(TPR, NV) for a row of nvt vectors: the smallest power of two of lanes
-// with one vector each, 1024 with two beyond.  FINE: every power of two, and 16
-// lanes with three vectors each instead of a wave where those suffice (a wave
-// against 16 lanes at 2^18 rows of 257 bf16 elements: 124 and 101 us forward, 289 and 208
-// backward; 4 and 8 lanes with three each were slower than 16 and 32 with one);
-// else every second power below a wave.
-template <bool FINE, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
+// with one vector each, 1024 with two beyond.  Rows of more than 512 vectors take 512
+// lanes with two each (1024 with one: forward 8000 x 5000 bf16 89 and 73 us, 8000 x
+// 4096 fp32 83 and 70, gated backward 30000 x 8192 bf16 584 and 446), but in the
+// backward with vectors of 4 (5000 x 4096 fp32: 98 and 107); there 1024 lanes have
+// room to read ahead.  In the forward with vectors of 4 more than 256 take 256 lanes
+// (8000 x 2048: 40 and 36; vectors of 8, 30000 x 4096: 160 and 163).  FINE: every
+// power of two, and 16 lanes with three vectors each instead of a wave where those
+// suffice (a wave against 16 lanes at 2^18 rows of 257 bf16 elements: 124 and 101 us
+// forward, 289 and 208 backward; 4 and 8 lanes with three each were slower than 16
+// and 32 with one); else every second power below a wave.
+template <bool FINE, bool BWD, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
 #define LAYER_CASE(T, N) return f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
     if constexpr (FINE) {
         if (nvt <= 1) LAYER_CASE(1, 1);
@@ -211,11 +216,11 @@ template <bool FINE, int VEC, class F> hipError_t split_rows(int nvt, F&& f) {
     if (nvt <= 64) LAYER_CASE(64, 1);
     if (nvt <= 128) LAYER_CASE(128, 1);
     if (nvt <= 256) LAYER_CASE(256, 1);
-    if (nvt <= 512) LAYER_CASE(512, 1);
+    if (nvt <= 512) LAYER_CASE((VEC == 4 && !BWD ? 256 : 512), (VEC == 4 && !BWD ? 2 : 1));
     if constexpr (VEC == 4) {
         if (nvt > 1024) LAYER_CASE(1024, 2);
     }
-    LAYER_CASE(1024, 1);
+    LAYER_CASE((VEC == 4 && BWD ? 1024 : 512), (VEC == 4 && BWD ? 1 : 2));
 #undef LAYER_CASE
 }
 
@@ -238,15 +243,15 @@ inline int grid_rows(long rows, int per, long most) {
 // workspace (us on the GPU alone and with the second launch, add norm D = 4096 fp32:
 // 1 row 5.6 and 8.2, 4 rows 12.1 and 9.1; gated norm D = 128: 64 rows, two turns,
 // 6.1 and 7.0, 128 rows 8.8 and 7.1); else every workgroup has about as many rows as
-// the others.  Half of MAX_BWD_BLOCKS where that many fill the chip (workgroups of
-// 1024) and up to 1024 turns in all, since each workgroup's sums are 8 D bytes to
-// write and to read again (512 and 256, add norm bf16: 300 x 4096 19.4 and 14.7 us, 900
-// x 2048 17.0 and 14.1, fp32 residual 2400 x 4096 52.6 and 46.1; fp32 1313 x 1024 15.1
-// and 16.4, 8192 x 8192 320 and 326).
+// the others.  Half of MAX_BWD_BLOCKS where that many fill the chip (`wide`: rows of
+// more than 512 vectors) and up to 1024 turns in all, since each workgroup's sums are
+// 8 D bytes to write and to read again (512 and 256, add norm bf16: 300 x 4096 19.4
+// and 14.7 us, 900 x 2048 17.0 and 14.1, 8000 x 8192 167 and 154, with an fp32 residual
+// 2400 x 4096 52.6 and 46.1; fp32 1313 x 1024 15.1 and 16.4, 8192 x 8192 320 and 326).
 constexpr int SOLO = 2, FEW = 1024;
-inline int bwd_blocks(NormArgs& a, int per, int threads) {
+inline int bwd_blocks(NormArgs& a, int per, bool wide) {
     const long n = (a.rows + per - 1) / per;
-    const long most = threads > BWD_THREADS || n <= FEW ? MAX_BWD_BLOCKS / 2 : MAX_BWD_BLOCKS;
+    const long most = wide || n <= FEW ? MAX_BWD_BLOCKS / 2 : MAX_BWD_BLOCKS;
     const long turns = n <= SOLO ? n : (n + most - 1) / most;
     const int blocks = (int)((n + turns - 1) / turns);
     a.pitch = a.scale ? 2 * a.D : a.D;

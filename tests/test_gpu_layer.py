@@ -973,3 +973,31 @@ def test_captured_decoding(B):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.equal(have[0], pool) and torch.equal(have[1], diag)
         want_pool, want_diag = pool.clone(), diag.clone()
+
+
+@pytest.mark.parametrize("rows,D,dtype,rdtype", [(600, 8192, "bf16", "bf16"), (1100, 4100, "f16", "f32"), (530, 8192, "f32", "f32"),
+                                                 (1030, 1500, "f32", "f32"), (300, 4500, "f16", "f16")])
+def test_norms_many_wide_rows(B, rows, D, dtype, rdtype):
+    """Rows of many lanes, several to a workgroup of the backward; in place too."""
+    x, z, res = rnd(1, rows, D).to(DT[dtype]), rnd(2, rows, D).to(DT[dtype]), rnd(3, rows, D, scale=2.0).to(DT[rdtype])
+    w, s = 1 + 0.1 * rnd(4, D), 0.5 + 0.2 * rnd(5, D)
+    dy, dres = rnd(6, rows, D).to(DT[dtype]), rnd(7, rows, D).to(DT[rdtype])
+    d = {k: t.cuda() for k, t in dict(x=x, z=z, res=res, w=w, s=s, dy=dy, dres=dres).items()}
+    ref, tol = gated_ref(x, z, w, dy, "silu", dtype)
+    g = B.gated_norm_bwd(d["x"], d["z"], d["w"], d["dy"], eps=EPS)
+    for k, v in {"y": B.gated_norm_fwd(d["x"], d["z"], d["w"], eps=EPS), **g}.items():
+        close(k, v, ref[k], tol[k])
+    f = B.add_norm_fwd(d["x"], d["res"], d["w"], scale=d["s"], eps=EPS)
+    ref, tol = add_ref(x, res, w, s, dtype, rdtype)
+    for k in ("y", "res"):
+        close(k, f[k], ref[k], tol[k])
+    a = B.add_norm_bwd(d["dy"], d["dres"], f["res"], d["w"], x=d["x"], scale=d["s"], eps=EPS)
+    ref, tol = add_bwd_ref(dy, dres, f["res"], w, x, s, dtype, rdtype)
+    for k in ref:
+        close(k, a[k], ref[k], tol[k])
+    b = {"dx": d["dy"].clone(), "dres": d["dres"].clone(), "dw": torch.empty_like(a["dw"]), "dscale": torch.empty_like(a["dw"])}
+    B.add_norm_bwd(b["dx"], b["dres"], f["res"], d["w"], x=d["x"], scale=d["s"], eps=EPS, out=b)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    c = {"dx": d["x"], "dz": d["z"], "dw": b["dw"]}
+    B.gated_norm_bwd(d["x"], d["z"], d["w"], d["dy"], eps=EPS, out=c)
+    assert all(torch.equal(g[k], c[k]) for k in g)
