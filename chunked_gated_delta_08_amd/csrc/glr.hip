@@ -22,10 +22,11 @@
 //     before, by a branch that is uniform over the wave (a product with zero
 //     would let another sequence's infinity or NaN through).
 // Waiting ends, whatever the order in which workgroups start: after `polls` tries
-// a workgroup takes up the first earlier segment whose map is not there, as if it
-// were its own (both give the same bits), and then begins its own again.  The
-// first segment that is not finished waits for nothing, so it is finished by
-// whoever has it, or by one that waits for it.
+// a workgroup takes up the first earlier segment that still owes a word of its own
+// (its map, its group's, its block's state), as if it were its own (both give the
+// same bits), and then begins its own again.  The first segment that is not finished
+// waits for nothing, so it is finished by whoever has it, or by one that waits for
+// it.  The rule is in glr_chain.hpp.
 // A product P of gates may overflow where the state itself would not, if gates
 // above 1 follow one another (include/gdn_layer.h bounds them); where it
 // underflows, what it multiplies is lost too.
@@ -45,15 +46,16 @@
 // tile, not from the rounded h: dg is an fp32 output.
 #include "../../include/gdn_layer.h"
 #include "gdr_device.hpp"
+#include "glr_chain.hpp"
 #include "layer_launch.hpp"
 
 namespace layer {
 namespace {
 
+using chain::G;
 using gdr::bf16;
 using gdr::f16;
 constexpr int L = GLR_TILE;
-constexpr int G = 8;            // segments of a group, groups of a block
 constexpr int SLEEP = 8;        // 64 clocks each between two looks
 
 template <class E, int N> struct VecU { typedef E t __attribute__((ext_vector_type(N), aligned(sizeof(E)))); };
@@ -302,12 +304,9 @@ __device__ __forceinline__ bool exchange(const Ws& ws, int idx, int nseg, int sr
                                          bool cut, const float (&P)[C], const float (&H)[C], Maps<W, C>& ea,
                                          Maps<W, C>& eb, float (*tot)[64 * C], unsigned (*votes)[W],
                                          float (&in)[C]) {
-    const int l = gdr::lane_o();
-    const bool entered = src < idx, later = idx + 1 < nseg, tells = w == W - 1 && later;
-    const bool closes = later && idx % G == G - 1;
-    const int g = idx / G, g0 = g * G, first = max(src, g0), na = entered ? idx - first : 0;
-    const bool outside = entered && src < g0, far = outside && src / G < g / G * G;
-    const int gfirst = far ? g / G * G : src / G, nb = outside ? g - gfirst + far : 0;
+    const int l = gdr::lane_o(), g = idx / G;
+    const bool later = idx + 1 < nseg, tells = w == W - 1 && later, closes = later && chain::closes_group(idx);
+    const auto [first, na, gfirst, nb, outside, far] = chain::reads(idx, src);
     const u64* a = w < na ? ws.map + (size_t)(first + w) * D : nullptr;
     const u64* b = w >= nb ? nullptr : far && w == 0 ? ws.state + (size_t)(g / G - 1) * D
                                                      : ws.group + (size_t)(gfirst + w - far) * D;
@@ -336,7 +335,7 @@ __device__ __forceinline__ bool exchange(const Ws& ws, int idx, int nseg, int sr
         }
         a = nullptr;
     }
-    if (entered) {
+    if (src < idx) {
         if (!all_waves<W>(await<W, C>(a, b, ch, w, polls, ea, eb), votes[1], w)) return false;
         float p[C];
 #pragma unroll
@@ -344,7 +343,7 @@ __device__ __forceinline__ bool exchange(const Ws& ws, int idx, int nseg, int sr
         through_tiles<C>(eb, far ? 0u : 1u, 0, nb, p, in);
         through_tiles<C>(ea, outside ? 0u : 1u, 0, na, p, in);
     }
-    if (tells && idx % (G * G) == G * G - 1) {
+    if (tells && chain::closes_block(idx)) {
         float p[C], h[C];
 #pragma unroll
         for (int c = 0; c < C; c++) {
@@ -357,18 +356,22 @@ __device__ __forceinline__ bool exchange(const Ws& ws, int idx, int nseg, int sr
     return true;
 }
 
-// The first segment before `idx` whose map is not there (idx: none), found by the
+// The first segment before `idx` that still owes a word (idx: none), found by the
 // first wave for all.
 template <int C>
-__device__ __forceinline__ int first_missing(const Ws& ws, int idx, int D, unsigned ch, int w, int& found) {
-    int j = 0;
-    for (; w == 0 && j < idx; j++) {
-        bool there = true;
+__device__ __forceinline__ int first_unfinished(const Ws& ws, int idx, int D, unsigned ch, int w, int& found) {
+    const auto there = [&](const u64* rows, int j) {
+        bool yes = true;
 #pragma unroll
-        for (int c = 0; c < C; c++) there = there && peek(gdr::at32(ws.map + (size_t)j * D, ch + c)) != NOT_YET;
-        if (!__all(there)) break;
+        for (int c = 0; c < C; c++) yes = yes && peek(gdr::at32(rows + (size_t)j * D, ch + c)) != NOT_YET;
+        return (bool)__all(yes);
+    };
+    if (w == 0) {
+        const int j = chain::first_unfinished(
+            idx, [&](int i) { return there(ws.map, i); }, [&](int i) { return there(ws.group, i); },
+            [&](int i) { return there(ws.state, i); });
+        if (threadIdx.x == 0) found = j;
     }
-    if (threadIdx.x == 0) found = j;
     gdr::lds_barrier();
     return __builtin_amdgcn_readfirstlane(found);
 }
@@ -528,7 +531,7 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 4 ? 4 : 6) void glr_fwd_kernel
         }
         if (got && seg == own) return;
         gdr::lds_barrier();   // what the next pass writes to LDS has been read
-        seg = got ? own : first_missing<C>(ws, own, D, ch, w, missing);
+        seg = got ? own : first_unfinished<C>(ws, own, D, ch, w, missing);
     }
 }
 
@@ -651,7 +654,7 @@ __global__ __launch_bounds__(64 * W, 4) void glr_bwd_kernel(GlrArgs a, int nblk,
         }
         if (got && idx == own) return;
         gdr::lds_barrier();   // what the next pass writes to LDS has been read
-        idx = got ? own : first_missing<C>(ws, own, D, ch, w, missing);
+        idx = got ? own : first_unfinished<C>(ws, own, D, ch, w, missing);
     }
 }
 

@@ -61,6 +61,8 @@ for _k, _f in (("gated_norm_fwd_kernel", "layer_gated_norm"), ("gated_norm_bwd_k
 for _k, _f in (("glr_fwd_kernel", "glr"), ("glr_bwd_kernel", "glr"), ("glr_clear_kernel", "glr"),
                ("gdr_step_kernel", "layer_step"), ("glr_step_kernel", "layer_step")):
     KERNEL_SOURCES[_k] = [_CS + _f + ".hip", _CS + "layer_launch.hpp"] + _COMMON
+    if _f == "glr":
+        KERNEL_SOURCES[_k].insert(1, _CS + "glr_chain.hpp")
 
 
 def _code_of(text):

@@ -1001,3 +1001,36 @@ def test_norms_many_wide_rows(B, rows, D, dtype, rdtype):
     c = {"dx": d["x"], "dz": d["z"], "dw": b["dw"]}
     B.gated_norm_bwd(d["x"], d["z"], d["w"], d["dy"], eps=EPS, out=c)
     assert all(torch.equal(g[k], c[k]) for k in g)
+
+
+# ------------------------------------------- the recurrence over many segments
+
+def chain_inputs(lens, D, dtype):
+    """Every even channel has gates of 1 and small whole numbers, so each of its sums is exact in fp32 (below 2^24
+    throughout) and a state that is lost or taken twice anywhere shows; the odd ones have time constants of some
+    thousand tokens."""
+    T, N = sum(lens), len(lens)
+    x, dh, h0, dht = rnd(1, T, D), rnd(2, T, D), rnd(3, N, D), rnd(4, N, D)
+    g = -torch.exp(0.5 * rnd(5, T, D) - 8)
+    for t in (x, dh, h0, dht):
+        t[:, ::2] = (t[:, ::2] * 2).round().clamp(-6, 6)
+    g[:, ::2] = 0.0
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+    d = {k: t.cuda() for k, t in dict(x=x.to(DT[dtype]), g=g, dh=dh.to(DT[dtype]), h0=h0, dht=dht).items()}
+    return d, dict(cu_seqlens=cu.cuda(), cu_seqlens_host=cu) if N > 1 else {}
+
+
+def chain_run(B, d, kw, polls=0):
+    f = B.glr_fwd(d["x"], d["g"], h0=d["h0"], want_states=True, polls=polls, **kw)
+    return {**f, **B.glr_bwd(d["x"], d["g"], d["dh"], f["states"], dht=d["dht"], h0=d["h0"], polls=polls, **kw)}
+
+
+@pytest.mark.parametrize("lens,D,dtype", [([27000], 66, "bf16"), ([27000], 3, "f16"), ([17500], 70, "f32")])
+def test_glr_many_blocks_without_patience(B, lens, D, dtype):
+    """Chains of more than two blocks of 64 segments (192 tokens each in the 16-bit forward, else 128) whose
+    workgroups take up one another's segments: the same bits."""
+    d, kw = chain_inputs(lens, D, dtype)
+    want = chain_run(B, d, kw)
+    for polls in (1, 2, 9):
+        got = chain_run(B, d, kw, polls)
+        assert all(torch.equal(got[k], want[k]) for k in want), polls
