@@ -16,10 +16,40 @@ Layouts follow the C ABI (token axis flattened over the batch):
 A training step may be captured into a graph (give cu_seqlens_host, so that nothing
 is copied to the host).  Let go of the outputs of earlier eager passes over the same
 leaves first: torch ties a leaf's gradient to the stream of the graph that is alive.
+
+The operators have first derivatives only: gradients taken with create_graph=True are
+the same, and differentiating them again raises.
 """
 import torch
 
 from . import binding
+
+
+class _FirstOrder(torch.autograd.Function):
+    """Hands the gradients t[n:] on; they depend on t[:n], and to differentiate them raises."""
+    @staticmethod
+    def forward(ctx, op, n, *t):
+        ctx.op = op
+        return t[n:]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.op} has no second derivative (its gradients were differentiated)")
+
+
+def _first_order(op, ctx, incoming, grads):
+    """A backward's results.  The kernels that made them are unknown to torch, so under
+    create_graph=True they would count as constants and second derivatives lack their terms."""
+    if not torch.is_grad_enabled():
+        return grads
+    needs = [t for t in (*ctx.saved_tensors, *incoming) if t is not None and t.requires_grad]
+    out = iter(_FirstOrder.apply(op, len(needs), *needs, *(g for g in grads if g is not None)))
+    return tuple(None if g is None else next(out) for g in grads)
+
+
+def _contiguous(*tensors):
+    """Outside the functions, so that what they save is connected to what they are given."""
+    return [None if t is None else t.contiguous() for t in tensors]
 
 
 class ChunkGatedDeltaRule(torch.autograd.Function):
@@ -32,6 +62,7 @@ class ChunkGatedDeltaRule(torch.autograd.Function):
                                     seg_chunks=seg_chunks)
         ctx.save_for_backward(q, k, v, g_cum, beta, h0, cu_seqlens)
         ctx.cfg = (scale, B, BT, seg_chunks)
+        ctx.g = g   # not read again, and so free to be overwritten; _first_order asks whether it needs a gradient
         return out["o"], out["ht"]
 
     @staticmethod
@@ -41,7 +72,8 @@ class ChunkGatedDeltaRule(torch.autograd.Function):
         r = binding.gdr_chunk_bwd(q, k, v, g_cum, beta, do.contiguous(), dht=None if dht is None else dht.contiguous(),
                                   h0=h0, cu_seqlens=cu_seqlens, B=B, scale=scale, BT=BT,
                                   want_dh0=h0 is not None and ctx.needs_input_grad[5], seg_chunks=seg_chunks)
-        return r["dq"], r["dk"], r["dv"], r["dg"], r["dbeta"].to(beta.dtype), r["dh0"], None, None, None, None, None
+        return _first_order("chunk_gated_delta_rule", ctx, (do, dht, ctx.g),
+                            (r["dq"], r["dk"], r["dv"], r["dg"], r["dbeta"].to(beta.dtype), r["dh0"]) + (None,) * 5)
 
 
 def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=None, B=1, BT=64,
@@ -50,7 +82,7 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, cu_
 
     Differentiable in q, k, v, g, beta and initial_state.  cu_seqlens: int32 CUDA
     tensor [N+1] (varlen; then the batch is 1) or None.  The final state is fp32."""
-    return ChunkGatedDeltaRule.apply(q, k, v, g, beta, initial_state, scale, cu_seqlens, B, BT, seg_chunks)
+    return ChunkGatedDeltaRule.apply(*_contiguous(q, k, v, g, beta, initial_state), scale, cu_seqlens, B, BT, seg_chunks)
 
 
 class GatedRMSNorm(torch.autograd.Function):
@@ -66,14 +98,14 @@ class GatedRMSNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, z, w = ctx.saved_tensors
         r = binding.gated_norm_bwd(x, z, w, dy.contiguous(), eps=ctx.cfg[0], act=ctx.cfg[1])
-        return r["dx"], r["dz"], r["dw"], None, None
+        return _first_order("gated_rms_norm", ctx, (dy,), (r["dx"], r["dz"], r["dw"], None, None))
 
 
 def gated_rms_norm(x, z, weight, eps=1e-5, act="silu"):
     """RMSNorm of x [..., D] times weight [D] (fp32) times the gate act(z); z None: no gate.
 
     Differentiable in x, z and weight.  act is "silu" or "sigmoid"."""
-    return GatedRMSNorm.apply(x, z, weight, eps, act)
+    return GatedRMSNorm.apply(*_contiguous(x, z, weight), eps, act)
 
 
 class AddRMSNorm(torch.autograd.Function):
@@ -90,10 +122,11 @@ class AddRMSNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, dres):
         x, res, w, scale = ctx.saved_tensors
+        incoming = (dy, dres)
         dy = torch.zeros_like(res, dtype=ctx.cfg[1]) if dy is None else dy.contiguous()
         dres = None if dres is None else dres.contiguous()
         r = binding.add_norm_bwd(dy, dres, res, w, x=x, scale=scale, eps=ctx.cfg[0])
-        return r["dx"], r["dres"], r["dw"], r["dscale"], None
+        return _first_order("add_rms_norm", ctx, incoming, (r["dx"], r["dres"], r["dw"], r["dscale"], None))
 
 
 def add_rms_norm(x, res, weight, scale=None, eps=1e-5):
@@ -101,7 +134,7 @@ def add_rms_norm(x, res, weight, scale=None, eps=1e-5):
 
     Differentiable in x, res, weight and scale ([D] fp32, None: 1).  res is in x's
     type or fp32; the gradients are taken at the stored res'."""
-    return AddRMSNorm.apply(x, res, weight, scale, eps)
+    return AddRMSNorm.apply(*_contiguous(x, res, weight, scale), eps)
 
 
 class GatedLinearRecurrence(torch.autograd.Function):
@@ -119,12 +152,13 @@ class GatedLinearRecurrence(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dh, dht):
         x, g, h0, states, cu_seqlens, cu_seqlens_host = ctx.saved_tensors
+        incoming = (dh, dht)
         dh = torch.zeros_like(x) if dh is None else dh.contiguous()
         dht = None if dht is None else dht.contiguous()
         r = binding.glr_bwd(x, g, dh, states, dht=dht, h0=h0, cu_seqlens=cu_seqlens,
                             cu_seqlens_host=cu_seqlens_host, B=ctx.B,
                             want_dh0=h0 is not None and ctx.needs_input_grad[2])
-        return r["dx"], r["dg"], r["dh0"], None, None, None
+        return _first_order("gated_linear_recurrence", ctx, incoming, (r["dx"], r["dg"], r["dh0"], None, None, None))
 
 
 def gated_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, cu_seqlens_host=None, B=1):
@@ -133,4 +167,4 @@ def gated_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, cu_seqlen
     Differentiable in x, g and initial_state ([N, D] fp32).  cu_seqlens as for
     chunk_gated_delta_rule; cu_seqlens_host, its CPU copy, avoids a copy in each pass.
     The final state is fp32."""
-    return GatedLinearRecurrence.apply(x, g, initial_state, cu_seqlens, cu_seqlens_host, B)
+    return GatedLinearRecurrence.apply(*_contiguous(x, g, initial_state), cu_seqlens, cu_seqlens_host, B)

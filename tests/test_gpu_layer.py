@@ -1034,3 +1034,23 @@ def test_glr_many_blocks_without_patience(B, lens, D, dtype):
     for polls in (1, 2, 9):
         got = chain_run(B, d, kw, polls)
         assert all(torch.equal(got[k], want[k]) for k in want), polls
+
+
+def test_second_derivatives_raise(B):
+    """create_graph leaves the gradients as they are; differentiating them again raises instead of leaving the
+    operators' terms out."""
+    from chunked_gated_delta_08_amd import autograd as A
+    x, z, g = (rnd(i, 40, 32).cuda().requires_grad_() for i in range(3))
+    w = (1 + 0.1 * rnd(4, 32)).cuda().requires_grad_()
+    q, k, v = (rnd(i, 40, 1, 64).cuda().requires_grad_() for i in range(5, 8))
+    a, b = (-torch.rand(40, 1, device="cuda")).requires_grad_(), torch.rand(40, 1, device="cuda", requires_grad=True)
+    for run, args in ((lambda: A.gated_rms_norm(x, z, w), (x, z, w)), (lambda: A.add_rms_norm(x, z, w)[1], (x, z)),
+                      (lambda: A.add_rms_norm(x, z, w, w)[0], (x, z, w)),
+                      (lambda: A.gated_linear_recurrence(x, -g.exp())[0], (x, g)),
+                      (lambda: A.chunk_gated_delta_rule(q, k, v, a, b)[0], (q, k, v, a, b))):
+        plain = torch.autograd.grad(run().sum(), args)
+        grads = torch.autograd.grad(run().sum(), args, create_graph=True)
+        assert all(torch.equal(s, t) for s, t in zip(plain, grads))
+        for t, arg in zip(grads, args):
+            with pytest.raises(RuntimeError, match="no second derivative"):
+                torch.autograd.grad(t.sum() + arg.square().sum(), arg, retain_graph=True)
