@@ -377,11 +377,15 @@ __device__ __forceinline__ int first_unfinished(const Ws& ws, int idx, int D, un
 }
 
 // exp(g), off by at most (|g| + 3) 2^-24 of itself: the exponent's one rounding,
-// log2(e)'s, and two for exp2; zero below 2^-126.  (expf is within 2 2^-24 at some
-// ten operations instead of two.)  What the state loses to it is little: a token
-// with a large |g| hardly passes the state on, and over the tokens that do the
-// |g| add up to about one.
-__device__ __forceinline__ float gate(float g) { return __builtin_amdgcn_exp2f(1.44269504f * g); }
+// |g| 2^-24, and one unit in the last place, 2 2^-24, for exp2 (log2(e) in two
+// parts: its one-part rounding alone adds 0.22 |g|); zero below 2^-126.  (expf is
+// within 2 2^-24 at some ten operations instead of three.)  Where g is large the
+// state hardly passes on; where it is small, the state that passes n tokens is off
+// by up to 2 n 2^-24 of itself from the gates' last places, as any gate held in
+// fp32 is by a part of that.
+__device__ __forceinline__ float gate(float g) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(g, 0x1.715476p+0f, g * 0x1.4ae0cp-26f));
+}
 
 // Keeps a value as it was loaded: its widening to fp32 is not carried from one
 // pass over the tile to the next in twice the registers.

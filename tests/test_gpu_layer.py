@@ -1054,3 +1054,19 @@ def test_second_derivatives_raise(B):
         for t, arg in zip(grads, args):
             with pytest.raises(RuntimeError, match="no second derivative"):
                 torch.autograd.grad(t.sum() + arg.square().sum(), arg, retain_graph=True)
+
+
+def test_glr_gate_error(B):
+    """exp(g) as both directions form it: (|g| + 3) u over the range of fp32, |g| u of it the rounding of the
+    exponent's argument, zero below 2^-126.  One token from the state 1 shows it unrounded."""
+    D = 1 << 20
+    g = -torch.from_numpy(np.exp(np.random.default_rng(1).uniform(-9, np.log(89), (1, D))).astype(np.float32))
+    g[0, :4] = torch.tensor([0.0, -0.0, float("-inf"), 70.0])
+    zero, one = torch.zeros(1, D, device="cuda"), torch.ones(1, D, device="cuda")
+    ref = f64(g).exp()
+    tol = torch.where(torch.isfinite(g), (g.abs() + 3) * U * ref, 0.0) + GATE0
+    f = B.glr_fwd(zero, g.cuda(), h0=one, want_states=True)
+    b = B.glr_bwd(zero, g.cuda(), zero, f["states"], dht=one, h0=one)
+    close("ht", f["ht"], ref, tol)
+    close("dh0", b["dh0"], ref, tol)
+    assert f["ht"][0, 0] == 1 and f["ht"][0, 2] == 0
