@@ -119,10 +119,13 @@ __device__ __forceinline__ void store_vec(E* row, int c, int D, const float (&x)
     }
 }
 
-// sigmoid in fp32: relative error below (|z| + 4) 2^-24 (the exponent's argument
-// is rounded once, exp2 and rcp are within one unit in the last place).
+// sigmoid in fp32, off by at most (|z| + 5) 2^-24 of itself: the exponent's one
+// rounding, |z| 2^-24 (log2(e) in two parts: its one-part rounding adds 0.22 |z|),
+// one unit in the last place, 2 2^-24, each for exp2 and rcp, and the sum's
+// rounding; zero below 2^-126.
 __device__ __forceinline__ float sigmoid_f(float z) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896f * z));
+    const float t = __builtin_fmaf(-z, 0x1.715476p+0f, -z * 0x1.4ae0cp-26f);
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t));
 }
 
 // Sum over the TPR lanes of a row; for TPR = 256 over the four waves of the

@@ -1070,3 +1070,15 @@ def test_glr_gate_error(B):
     close("ht", f["ht"], ref, tol)
     close("dh0", b["dh0"], ref, tol)
     assert f["ht"][0, 0] == 1 and f["ht"][0, 2] == 0
+
+
+def test_sigmoid_error(B):
+    """The gate's sigmoid over its range: (|z| + 5) u, |z| u of it the rounding of the exponent's argument.  Rows of
+    ones show it: their mean of squares is 1 exactly, its rsqrt is off by 2 u and the product by u; the sigmoid is
+    zero below 2^-126."""
+    z = torch.from_numpy(np.random.default_rng(1).uniform(-90, 30, (1 << 13, 128)).astype(np.float32))
+    z[0, :4] = torch.tensor([0.0, -0.0, 200.0, -200.0])
+    one = torch.ones_like(z).cuda()
+    s = 1 / (1 + (-f64(z)).exp())
+    y = B.gated_norm_fwd(one, z.cuda(), one[0].contiguous(), eps=0.0, act="sigmoid")
+    close("y", y, s, (z.abs().double() + 8) * U * s + 2.0 ** -126)
