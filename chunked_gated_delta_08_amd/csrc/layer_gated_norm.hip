@@ -16,11 +16,26 @@
 namespace layer {
 namespace {
 
-// act(z) and its derivative, from s = sigmoid(z).
+// act(z) from s = sigmoid(z).
 __device__ __forceinline__ float act_of(float z, float s, bool silu) { return silu ? z * s : s; }
-__device__ __forceinline__ float act_slope(float z, float s, bool silu) {
-    return silu ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
-}
+// act(z) and its derivative for the backward, from one value that is held in between.
+// silu, s (1 + z (1 - s)): s itself.  Where s is near one, 1 - s has few digits, but it
+// is small next to 1.  sigmoid, s (1 - s): there every digit of the smaller factor
+// counts (s is 1 in fp32 from z = 17 on), so that is held, sigmoid(-|z|) with z's sign.
+template <int ACT> struct Gate {
+    float v;
+    __device__ __forceinline__ void of(float z) {
+        v = ACT == GDN_ACT_SILU ? sigmoid_f(z) : copysignf(sigmoid_f(-fabsf(z)), z);
+    }
+    __device__ __forceinline__ float act(float z) const {
+        return ACT == GDN_ACT_SILU ? z * v : (__float_as_int(v) < 0 ? 0.f : 1.f) - v;
+    }
+    __device__ __forceinline__ float slope(float z) const {
+        const float p = fabsf(v);
+        return ACT == GDN_ACT_SILU ? v * (1.f + z * (1.f - v)) : p * (1.f - p);
+    }
+};
+constexpr int NO_GATE = -1;
 
 template <class E, int VEC, int NV> struct Rows {   // a row of x, z and dy as loaded
     Raw<E, VEC> x[NV], z[NV], g[NV];
@@ -78,14 +93,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void gated_norm_fwd_kernel(N
 }
 
 // A workgroup takes rows in turn, the next one's on their way meanwhile.
-template <class E, int VEC, int TPR, int NV, bool GATE, int BT>
+template <class E, int VEC, int TPR, int NV, int ACT, int BT>
 __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
     constexpr int GR = BT / TPR;
+    constexpr bool GATE = ACT != NO_GATE;
     __shared__ float lds[BT * VEC];
     __shared__ float red[TPR > 64 ? 2 * 2 * (BT / 64) : 1];
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, D = a.D;
     const float inv = 1.f / (float)D;
-    const bool silu = a.act == GDN_ACT_SILU;
     float w[NV][VEC], dw[NV][VEC];
     load_weights<VEC, TPR, NV>(w, a.w, lane, D);
 #pragma unroll
@@ -97,7 +112,8 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
     load_rows<E, VEC, TPR, NV, GATE, true>(in, a, (long)blockIdx.x * GR + grp, lane);
     for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
         if constexpr (NV == 1) load_rows<E, VEC, TPR, NV, GATE, true>(next, a, r0 + (long)gridDim.x * GR + grp, lane);
-        float s[2] = {0.f, 0.f}, sg[GATE ? NV : 1][VEC];   // sg: the gate's sigmoid, formed once
+        float s[2] = {0.f, 0.f};
+        Gate<ACT> gate[GATE ? NV : 1][VEC];   // formed once
 #pragma unroll
         for (int i = 0; i < NV; i++)
 #pragma unroll
@@ -106,8 +122,8 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
                 float dn = (float)in.g[i].v[e] * w[i][e];
                 if constexpr (GATE) {
                     const float z = (float)in.z[i].v[e];
-                    sg[i][e] = sigmoid_f(z);
-                    dn *= act_of(z, sg[i][e], silu);
+                    gate[i][e].of(z);
+                    dn *= gate[i][e].act(z);
                 }
                 s[0] += x * x;
                 s[1] += dn * x;
@@ -125,9 +141,9 @@ __global__ __launch_bounds__(BT) void gated_norm_bwd_kernel(NormArgs a) {
                     const float n = (float)in.x[i].v[e] * r, g = (float)in.g[i].v[e];
                     float dn = g * w[i][e], t = g * n;   // t = dy n
                     if constexpr (GATE) {
-                        const float z = (float)in.z[i].v[e], f = act_of(z, sg[i][e], silu);
+                        const float z = (float)in.z[i].v[e], f = gate[i][e].act(z);
                         dn *= f;
-                        dz[e] = t * w[i][e] * act_slope(z, sg[i][e], silu);
+                        dz[e] = t * w[i][e] * gate[i][e].slope(z);
                         t *= f;
                     }
                     dw[i][e] += t;
@@ -162,9 +178,10 @@ template <class E> hipError_t gated_bwd(const NormArgs& a0, hipStream_t s) {
     const hipError_t e = split_rows<true, true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
         blocks = bwd_blocks(a, BT / TPR, TPR * NV > 512);
-        if (a.z)
-            hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
-        else hipLaunchKernelGGL((gated_norm_bwd_kernel<E, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);
+        const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(BT), 0, s, a); };
+        if (!a.z) run(gated_norm_bwd_kernel<E, VEC, TPR, NV, NO_GATE, BT>);
+        else if (a.act == GDN_ACT_SILU) run(gated_norm_bwd_kernel<E, VEC, TPR, NV, GDN_ACT_SILU, BT>);
+        else run(gated_norm_bwd_kernel<E, VEC, TPR, NV, GDN_ACT_SIGMOID, BT>);
         return hipGetLastError();
     });
     return e != hipSuccess ? e : norm_wsum(a, blocks, s);

@@ -1082,3 +1082,21 @@ def test_sigmoid_error(B):
     s = 1 / (1 + (-f64(z)).exp())
     y = B.gated_norm_fwd(one, z.cuda(), one[0].contiguous(), eps=0.0, act="sigmoid")
     close("y", y, s, (z.abs().double() + 8) * U * s + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gate_slope_of_open_and_shut_gates(B, act, dtype):
+    """dz where the gate is nearly open or shut: its slope s c (1 + z c for silu) falls like exp(-|z|), and every digit
+    of it counts.  s and c = 1 - s are each off by (|z| + 6) u (the sigmoid's |z| + 5, or that of the smaller one
+    and one subtraction), the rest of dz by NORM_OPS operations; below 2^-126 they are zero."""
+    rows, D = 400, 128
+    x, dy, w = rnd(1, rows, D).to(DT[dtype]), rnd(2, rows, D).to(DT[dtype]), 1 + 0.1 * rnd(3, D)
+    z = torch.from_numpy(np.random.default_rng(4).uniform(-80, 80, (rows, D)).astype(np.float32)).to(DT[dtype])
+    g = B.gated_norm_bwd(*(t.cuda() for t in (x, z, w, dy)), eps=EPS, act=act)
+    x, z, w, dy = f64(x), f64(z), f64(w), f64(dy)
+    s, c = 1 / (1 + (-z).exp()), 1 / (1 + z.exp())
+    t = dy * w * x * (x.square().mean(-1, keepdim=True) + EPS).rsqrt()
+    one = (NORM_OPS + z.abs() + 6) * U
+    ref, err = (t * s * c, 2 * one * s * c) if act == "sigmoid" else (t * s * (1 + z * c), 2 * one * s * (1 + z.abs() * c))
+    close("dz", g["dz"], ref, half(dtype) * ref.abs() + t.abs() * (err + 2.0 ** -126) + TINY[dtype])
