@@ -218,7 +218,8 @@ int glr_step(int N, int D, int64_t nslots, gdr_dtype dtype, const void* x, const
     int st = check_step(N, nslots, dtype, slots);
     if (st != GDR_OK) return st;
     if (D < 1) return GDR_ERR_INVALID;
-    if (D > (1 << 20) || (int64_t)N * ((D + 255) / 256) > INT32_MAX / 256) return GDR_ERR_UNSUPPORTED;
+    // a launch has fewer than 2^32 threads: 128 for every 512 channels of a row
+    if (D > (1 << 20) || (int64_t)N * ((D + 511) / 512) >= 1 << 25) return GDR_ERR_UNSUPPORTED;
     if (N == 0) return GDR_OK;
     if (!x || !g || !h || (nslots > 0 && !state)) return GDR_ERR_INVALID;
     const size_t es = size_of(dtype), n = (size_t)N * D;
@@ -237,8 +238,8 @@ int gdr_step(int N, int HK, int HV, int K, int V, int64_t nslots, float scale, g
     int st = check_step(N, nslots, dtype, slots);
     if (st != GDR_OK) return st;
     if (HK < 1 || HV < 1 || HV % HK != 0 || K < 1 || V < 1 || isnan(scale) || isinf(scale)) return GDR_ERR_INVALID;
-    if (K != V || (K != 64 && K != 128) || HV > 1024 || (int64_t)N * HV > INT32_MAX / 2048)
-        return GDR_ERR_UNSUPPORTED;
+    // a launch has fewer than 2^32 threads: 256 for every head where there are thousands of them
+    if (K != V || (K != 64 && K != 128) || HV > 1024 || (int64_t)N * HV >= 1 << 24) return GDR_ERR_UNSUPPORTED;
     if (N == 0) return GDR_OK;
     if (!q || !k || !v || !g || !beta || !o || (nslots > 0 && !state)) return GDR_ERR_INVALID;
     const size_t es = size_of(dtype), nk = (size_t)N * HK * K * es, nv = (size_t)N * HV * V * es, nh = (size_t)N * HV;

@@ -153,7 +153,10 @@ int glr_bwd(const glr_problem *p, const void *x, const float *g, const float *h0
  *       Rows with the same slot are successive tokens of that state, in the order of the rows.
  *   state [nslots, D] fp32    read and updated in place
  *   h [N, D] dtype            may be x
- * 0 <= N <= 65536, 1 <= D <= 2^20.
+ * 0 <= N <= 65536, 1 <= D <= 2^20, N * ceil(D / 512) < 2^25.
+ * With slots each row looks through those of all others (64 at a time): little up to a thousand
+ * rows, most of the call beyond (D = 2048 bf16, us with slots and without: 1024 rows 11 and 9,
+ * 4096 rows 88 and 21, 16384 rows 1070 and 86).
  */
 int glr_step(int N, int D, int64_t nslots, gdr_dtype dtype, const void *x, const float *g, const int32_t *slots,
              float *state, void *h, hipStream_t stream);
@@ -165,7 +168,9 @@ int glr_step(int N, int D, int64_t nslots, gdr_dtype dtype, const void *x, const
  *   slots [N] int32 or NULL     as for glr_step
  *   state [nslots, HV, K, V] fp32   read and updated in place (gdr_chunk_fwd's ht_out, sequence by sequence)
  *   o [N, HV, V] dtype          may be v
- * scale <= 0 selects 1/sqrt(K).  0 <= N <= 65536; K = V in {64, 128}; HV % HK == 0, HV <= 1024.
+ * scale <= 0 selects 1/sqrt(K).  0 <= N <= 65536; K = V in {64, 128}; HV % HK == 0, HV <= 1024,
+ * N * HV < 2^24.  Many rows with slots as for glr_step (HV = 32, K = 128: 1024 rows 805 and 768 us,
+ * 4096 rows 4790 and 3170).
  */
 int gdr_step(int N, int HK, int HV, int K, int V, int64_t nslots, float scale, gdr_dtype dtype, const void *q,
              const void *k, const void *v, const float *g, const void *beta, const int32_t *slots, float *state,

@@ -1100,3 +1100,22 @@ def test_gate_slope_of_open_and_shut_gates(B, act, dtype):
     one = (NORM_OPS + z.abs() + 6) * U
     ref, err = (t * s * c, 2 * one * s * c) if act == "sigmoid" else (t * s * (1 + z * c), 2 * one * s * (1 + z.abs() * c))
     close("dz", g["dz"], ref, half(dtype) * ref.abs() + t.abs() * (err + 2.0 ** -126) + TINY[dtype])
+
+
+def test_steps_of_many_rows(B):
+    """2^20 heads in one rule step, 2^22 workgroups in one step of the recurrence: the last rows as a short call gives them."""
+    N, H, K, n = 65536, 16, 64, 40
+    i = {k: t.cuda() for k, t in step_inputs(7, n, 2, H, K, "bf16", S=n).items()}
+    big = {}
+    for k, t in i.items():
+        big[k] = torch.zeros(N, *t.shape[1:], dtype=t.dtype, device="cuda")
+        big[k][-n:] = t
+    assert torch.equal(B.gdr_step(**big)[-n:], B.gdr_step(**i))
+    assert torch.equal(big["state"][-n:], i["state"]) and not big["state"][:-n].any()
+    del big
+    D = 32768
+    x, g, st = rnd(1, n, D).bfloat16().cuda(), -torch.exp(rnd(2, n, D)).cuda(), rnd(3, n, D).cuda()
+    bx, bg, bs = (torch.zeros(N, D, dtype=t.dtype, device="cuda") for t in (x, g, st))
+    bx[-n:], bg[-n:], bs[-n:] = x, g, st
+    assert torch.equal(B.glr_step(bx, bg, bs)[-n:], B.glr_step(x, g, st))
+    assert torch.equal(bs[-n:], st) and not bs[:-n].any()

@@ -293,3 +293,15 @@ def test_gpu_tensors_are_needed(B):
         B.gated_norm_fwd(Z(4, 8), None, Z(8))
     with pytest.raises(ValueError):
         B.glr_fwd(Z(4, 8), Z(4, 8))
+
+
+def test_steps_as_large_as_the_header_says(B):
+    """What the header allows gets past the limits (a missing tensor is then what is refused), the next size does not."""
+    for N, D in ((65536, 32768), (65536, 511 * 512), (32, 1 << 20), (16383, 1 << 20)):
+        assert step(B, N=N, D=D, slots=N, x=None) == -1, (N, D)
+    for N, D in ((65536, 511 * 512 + 1), (16384, 1 << 20)):
+        assert step(B, N=N, D=D, slots=N, x=None) == -2, (N, D)
+    for N, HV in ((65536, 16), (65536, 255), (16383, 1024)):
+        assert rule(B, N=N, HV=HV, slots=N, q=None) == -1, (N, HV)
+    for N, HV in ((65536, 256), (16384, 1024)):
+        assert rule(B, N=N, HV=HV, slots=N, q=None) == -2, (N, HV)
