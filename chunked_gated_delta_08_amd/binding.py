@@ -762,14 +762,18 @@ def _glr_sizes(B, T, D, dtype, polls):
     return p, int(lib.glr_workspace_size(ctypes.byref(p)))
 
 
-def _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls=0):
+def _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls=0, stream=None):
     """The problem struct, the workspace it needs and what has to outlive its use.
     Without a host mirror cu_seqlens is copied to the host, which waits for the
-    current stream."""
+    current stream and for a given one, either of which may still write it."""
     ntok, D = x.shape
     if cu_seqlens is None:
         return (*_glr_sizes(B, ntok // B, D, x.dtype, polls), None)
-    host = cu_seqlens.detach().cpu() if cu_seqlens_host is None else cu_seqlens_host
+    host = cu_seqlens_host
+    if host is None:
+        if stream is not None:
+            stream.synchronize()
+        host = cu_seqlens.detach().cpu()
     p = GlrProblem(1, ntok, D, host.numel() - 1, cu_seqlens.data_ptr(), host.data_ptr(), _DT[x.dtype], polls)
     return p, int(lib.glr_workspace_size(ctypes.byref(p))), host
 
@@ -808,7 +812,7 @@ def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=T
         _need(out["ht"], "ht", torch.float32, (N, D), optional=True)
         _need(out["states"], "states", torch.float32, (glr_num_states(ntok), D), optional=True)
         _same_device(x, *out.values())
-    p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
+    p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls, stream)
     ws, size, mine = _workspace(workspace, size, g)
     own.append(mine)
     _launch(dev, stream, own, lib.glr_fwd, p, _p(x), _p(g), _p(h0), _p(out["h"]), _p(out["ht"]), _p(out["states"]),
@@ -833,7 +837,7 @@ def glr_bwd(x, g, dh, states, dht=None, h0=None, cu_seqlens=None, cu_seqlens_hos
         _need(out["dg"], "dg", torch.float32, x.shape)
         _need(out["dh0"], "dh0", torch.float32, (N, D), optional=True)
         _same_device(x, *out.values())
-    p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls)
+    p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls, stream)
     ws, size, mine = _workspace(workspace, size, g)
     own.append(mine)
     _launch(dev, stream, own, lib.glr_bwd, p, _p(x), _p(g), _p(h0), _p(states), _p(dh), _p(dht), _p(out["dx"]),

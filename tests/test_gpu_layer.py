@@ -1119,3 +1119,26 @@ def test_steps_of_many_rows(B):
     bx[-n:], bg[-n:], bs[-n:] = x, g, st
     assert torch.equal(B.glr_step(bx, bg, bs)[-n:], B.glr_step(x, g, st))
     assert torch.equal(bs[-n:], st) and not bs[:-n].any()
+
+
+def test_given_stream_writes_cu_seqlens(B):
+    """Without a host mirror cu_seqlens is copied once the given stream has written it."""
+    T, D = 300, 64
+    right = torch.tensor([0, 100, T], dtype=torch.int32).cuda()
+    x, g, dh = rnd(1, T, D).cuda(), -torch.exp(rnd(2, T, D)).cuda(), rnd(3, T, D).cuda()
+    want = B.glr_fwd(x, g, cu_seqlens=right, want_states=True)
+    wantb = B.glr_bwd(x, g, dh, want["states"], cu_seqlens=right)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for bwd in (False, True):
+        cu = torch.zeros_like(right)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)
+            cu.copy_(right)
+        if bwd:
+            got, ref = B.glr_bwd(x, g, dh, want["states"], cu_seqlens=cu, stream=s), wantb
+        else:
+            got, ref = B.glr_fwd(x, g, cu_seqlens=cu, want_states=True, stream=s), want
+        s.synchronize()
+        assert all(torch.equal(got[k], ref[k]) for k in ref)
