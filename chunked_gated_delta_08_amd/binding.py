@@ -497,7 +497,8 @@ def bigdn_bwd(qkv, beta, decay, qw, kw, cos, sin, dout, F, S, k_scale=1.0, norm_
 # device's current stream) belongs to it; where a call allocates its outputs or
 # workspace, that stream first waits for the current one, whose memory they may
 # reuse (give `out` and `workspace` to overlap the two).  Preallocated outputs are checked like
-# inputs; which of them may be an input's own buffer is said in the header.
+# inputs; which of them may be an input's own buffer is said in the header.  In `out` an output
+# that a call may skip (the header's NULL) is None or not there.
 
 class NormProblem(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
@@ -642,9 +643,9 @@ def gated_norm_bwd(x, z, w, dy, eps=1e-5, act="silu", out=None, workspace=None, 
         out = {"dx": torch.empty_like(x), "dz": None if z is None else torch.empty_like(z), "dw": torch.empty_like(w)}
         own += out.values()
     else:
-        _need(out["dx"], "dx", x.dtype, x.shape)
-        _need(out["dw"], "dw", torch.float32, w.shape)
-        _need(out["dz"], "dz", x.dtype, x.shape, optional=z is None)
+        _need(out.get("dx"), "dx", x.dtype, x.shape)
+        _need(out.get("dw"), "dw", torch.float32, w.shape)
+        _need(out.get("dz"), "dz", x.dtype, x.shape, optional=z is None)
         _same_device(x, *out.values())
     dz = None if z is None else out["dz"]
     p, size = _norm_problem(x, eps, act=act)
@@ -679,8 +680,8 @@ def add_norm_fwd(x, res, w, scale=None, eps=1e-5, out=None, stream=None):
         out = {"y": torch.empty_like(x), "res": torch.empty_like(res)}
         own = out.values()
     else:
-        _need(out["y"], "y", x.dtype, x.shape)
-        _need(out["res"], "res", res.dtype, x.shape)
+        _need(out.get("y"), "y", x.dtype, x.shape)
+        _need(out.get("res"), "res", res.dtype, x.shape)
         _same_device(x, *out.values())
     p, _ = _norm_problem(x, eps, res.dtype)
     _launch(x.device, stream, own, lib.add_norm_fwd, p, _p(x), _p(res), _p(w), _p(scale), _p(out["y"]), _p(out["res"]))
@@ -709,12 +710,14 @@ def add_norm_bwd(dy, dres, res, w, x=None, scale=None, eps=1e-5, out=None, works
                "dw": torch.empty_like(w), "dscale": None if scale is None else torch.empty_like(scale)}
         own += out.values()
     else:
-        _need(out["dres"], "dres", res.dtype, res.shape)
-        _need(out["dx"], "dx", dy.dtype, dy.shape)
-        _need(out["dw"], "dw", torch.float32, w.shape)
-        _need(out["dscale"], "dscale", torch.float32, w.shape, optional=scale is None)
+        _need(out.get("dres"), "dres", res.dtype, res.shape)
+        _need(out.get("dx"), "dx", dy.dtype, dy.shape, optional=scale is None)
+        _need(out.get("dw"), "dw", torch.float32, w.shape)
+        _need(out.get("dscale"), "dscale", torch.float32, w.shape, optional=scale is None)
         _same_device(dy, *out.values())
-    dx = None if scale is None and out["dx"] is out["dres"] else out["dx"]
+    dx = out.get("dx")
+    if scale is None and dx is out["dres"]:
+        dx = None
     ds = None if scale is None else out["dscale"]
     p, size = _norm_problem(dy, eps, res.dtype)
     ws, size, mine = _workspace(workspace, size, w)
@@ -808,15 +811,15 @@ def glr_fwd(x, g, h0=None, cu_seqlens=None, cu_seqlens_host=None, B=1, want_ht=T
                "states": g.new_empty((glr_num_states(ntok), D)) if want_states else None}
         own += out.values()
     else:
-        _need(out["h"], "h", x.dtype, x.shape)
-        _need(out["ht"], "ht", torch.float32, (N, D), optional=True)
-        _need(out["states"], "states", torch.float32, (glr_num_states(ntok), D), optional=True)
+        _need(out.get("h"), "h", x.dtype, x.shape)
+        _need(out.get("ht"), "ht", torch.float32, (N, D), optional=True)
+        _need(out.get("states"), "states", torch.float32, (glr_num_states(ntok), D), optional=True)
         _same_device(x, *out.values())
     p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls, stream)
     ws, size, mine = _workspace(workspace, size, g)
     own.append(mine)
-    _launch(dev, stream, own, lib.glr_fwd, p, _p(x), _p(g), _p(h0), _p(out["h"]), _p(out["ht"]), _p(out["states"]),
-            _p(ws), size)
+    _launch(dev, stream, own, lib.glr_fwd, p, _p(x), _p(g), _p(h0), _p(out["h"]), _p(out.get("ht")),
+            _p(out.get("states")), _p(ws), size)
     del keep
     return out
 
@@ -833,15 +836,15 @@ def glr_bwd(x, g, dh, states, dht=None, h0=None, cu_seqlens=None, cu_seqlens_hos
                "dh0": g.new_empty((N, D)) if want_dh0 else None}
         own += out.values()
     else:
-        _need(out["dx"], "dx", x.dtype, x.shape)
-        _need(out["dg"], "dg", torch.float32, x.shape)
-        _need(out["dh0"], "dh0", torch.float32, (N, D), optional=True)
+        _need(out.get("dx"), "dx", x.dtype, x.shape)
+        _need(out.get("dg"), "dg", torch.float32, x.shape)
+        _need(out.get("dh0"), "dh0", torch.float32, (N, D), optional=True)
         _same_device(x, *out.values())
     p, size, keep = _glr_problem(x, cu_seqlens, cu_seqlens_host, B, polls, stream)
     ws, size, mine = _workspace(workspace, size, g)
     own.append(mine)
     _launch(dev, stream, own, lib.glr_bwd, p, _p(x), _p(g), _p(h0), _p(states), _p(dh), _p(dht), _p(out["dx"]),
-            _p(out["dg"]), _p(out["dh0"]), _p(ws), size)
+            _p(out["dg"]), _p(out.get("dh0")), _p(ws), size)
     del keep
     return out
 

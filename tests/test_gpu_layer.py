@@ -1142,3 +1142,24 @@ def test_given_stream_writes_cu_seqlens(B):
             got, ref = B.glr_fwd(x, g, cu_seqlens=cu, want_states=True, stream=s), want
         s.synchronize()
         assert all(torch.equal(got[k], ref[k]) for k in ref)
+
+
+def test_out_without_what_is_skipped(B):
+    """Outputs that a call may skip need not be in `out`; one that it needs is named."""
+    T, D = 300, 64
+    x, z, r, g = (rnd(i, T, D).cuda() for i in range(4))
+    w, g = 1 + 0.1 * rnd(5, D).cuda(), -torch.exp(g)
+    e = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    for args, call, keys in (((x, None, w, z), B.gated_norm_bwd, ("dx", "dw")), ((z, r, x, w), B.add_norm_bwd, ("dres", "dw")),
+                             ((z, r, x, w), B.add_norm_bwd, ("dres", "dw", "dx")), ((x, r, w), B.add_norm_fwd, ("y", "res")),
+                             ((x, g), B.glr_fwd, ("h",)), ((x, g), B.glr_fwd, ("h", "ht")),
+                             ((x, g, z, B.glr_fwd(x, g, want_states=True)["states"]), B.glr_bwd, ("dx", "dg"))):
+        want = call(*args)
+        out = {k: torch.empty_like(want[k]) for k in keys}
+        got = call(*args, out=out)
+        assert got is out and set(out) == set(keys) and all(torch.equal(got[k], want[k]) for k in keys)
+        with pytest.raises(ValueError, match="required"):
+            call(*args, out={k: out[k] for k in keys[1:]})
+    half_x = x.bfloat16()       # x's gradient skipped where it has a type of its own
+    got = B.add_norm_bwd(half_x, r, x, w, out={"dres": e(T, D), "dw": e(D)})
+    assert torch.equal(got["dres"], B.add_norm_bwd(half_x, r, x, w)["dres"])
