@@ -1163,3 +1163,20 @@ def test_out_without_what_is_skipped(B):
     half_x = x.bfloat16()       # x's gradient skipped where it has a type of its own
     got = B.add_norm_bwd(half_x, r, x, w, out={"dres": e(T, D), "dw": e(D)})
     assert torch.equal(got["dres"], B.add_norm_bwd(half_x, r, x, w)["dres"])
+
+
+@pytest.mark.parametrize("lens,D,dtype", [([27000], 3, "bf16"), ([27000], 66, "f16"), ([17500], 2, "f32"), ([17500], 70, "f32"),
+                                          ([13000, 1, 0, 30000, 77], 66, "bf16"), ([5000, 21000], 3, "f32")])
+def test_glr_many_blocks(B, lens, D, dtype):
+    """Every value of chains of more than two blocks of 64 segments (192 tokens each in the 16-bit forward, else 128),
+    from the start of a block or its middle on.  Channels with gates of 1 are exact: equal but for an output's rounding."""
+    d, kw = chain_inputs(lens, D, dtype)
+    got = chain_run(B, d, kw)
+    ref, err = glr_ref(*(d[k] for k in ("x", "g", "h0")), lens, d["dh"], d["dht"])
+    assert max(float(r[:, ::2].abs().max()) for r in ref.values()) < 2.0 ** 24
+    for k in ref:
+        t = dtype if k in ("h", "dx") else "f32"
+        close(k, got[k], ref[k], err[k] + half(t) * ref[k].abs())
+        assert torch.equal(got[k][:, ::2].cpu(), ref[k][:, ::2].to(DT[t])), k
+        if k in ("h", "dx"):   # what a lost state would change is far above what may be off
+            assert float((err[k][:, 1::2] / ref[k][:, 1::2].abs().mean()).median()) < 0.2, k
