@@ -47,7 +47,10 @@ template <class V> __device__ __forceinline__ V move_down(V v, int bytes) {
 
 // A lane's i-th VEC elements of a row of a stream; columns past D read as zero.
 // The vector that a row ends in is read from the row's last VEC elements and
-// moved down (one load for all lanes; element by element only where D < VEC).
+// moved down (one load for all lanes; element by element only where D < VEC).  The
+// elements before the vector's own are another lane's, of another wave perhaps, which
+// may be writing them already where an output replaces this input: whatever is read
+// there, the move drops it.  Its own elements only this lane writes, after their use.
 // Non-temporal: every element is read once in the launch.
 template <int TPR, class E, int VEC>
 __device__ __forceinline__ void load_raw(Raw<E, VEC>& r, const E* row, int i, int lane, int D) {
@@ -128,8 +131,8 @@ __device__ __forceinline__ float sigmoid_f(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t));
 }
 
-// Sum over the TPR lanes of a row; for TPR = 256 over the four waves of the
-// group through `lds` (one float per wave of the workgroup and value, used
+// Sum over the TPR lanes of a row; for TPR above 64 over the group's waves
+// through `lds` (one float per wave of the workgroup and value, used
 // alternately by `phase` so that one barrier per row is enough).
 template <int TPR, int NVAL, int THREADS>
 __device__ __forceinline__ void row_sum(float (&s)[NVAL], float* lds, int phase) {

@@ -1180,3 +1180,34 @@ def test_glr_many_blocks(B, lens, D, dtype):
         assert torch.equal(got[k][:, ::2].cpu(), ref[k][:, ::2].to(DT[t])), k
         if k in ("h", "dx"):   # what a lost state would change is far above what may be off
             assert float((err[k][:, 1::2] / ref[k][:, 1::2].abs().mean()).median()) < 0.2, k
+
+
+@pytest.mark.parametrize("dtype,base", [("bf16", 512), ("bf16", 1024), ("f32", 256), ("f32", 1024)])
+def test_odd_wide_rows_in_place(B, dtype, base):
+    """A row whose last vector begins a wave's columns is read from columns of the wave before, which may be writing
+    them already when an output replaces that input: what is read of those is dropped."""
+    vec = 8 if dtype == "bf16" else 4
+    for D in range(base + 1, base + vec):
+        rows = 1300
+        t = {k: rnd(i, rows, D).to(DT[dtype]).cuda() for i, k in enumerate(("x", "z", "dy", "res", "dres"))}
+        w, s = 1 + 0.1 * rnd(7, D).cuda(), 0.5 + 0.2 * rnd(8, D).cuda()
+        new = lambda: {k: v.clone() for k, v in t.items()}  # noqa: E731
+        y = B.gated_norm_fwd(t["x"], t["z"], w)
+        for k in ("x", "z"):
+            c = new()
+            assert torch.equal(B.gated_norm_fwd(c["x"], c["z"], w, out=c[k]), y), (D, k)
+        g = B.gated_norm_bwd(t["x"], t["z"], w, t["dy"])
+        for dx, dz in (("x", "z"), ("dy", "z"), ("x", "dy")):
+            c = new()
+            o = B.gated_norm_bwd(c["x"], c["z"], w, c["dy"], out={"dx": c[dx], "dz": c[dz], "dw": torch.empty_like(w)})
+            assert all(torch.equal(o[k], g[k]) for k in g), (D, dx, dz)
+        f = B.add_norm_fwd(t["x"], t["res"], w, scale=s)
+        c = new()
+        o = B.add_norm_fwd(c["x"], c["res"], w, scale=s, out={"y": c["x"], "res": c["res"]})
+        assert all(torch.equal(o[k], f[k]) for k in f), D
+        a = B.add_norm_bwd(t["dy"], t["dres"], t["res"], w, x=t["x"], scale=s)
+        for dx, dres in (("dy", "dres"), ("x", "res"), ("dy", "res"), ("x", "dres")):
+            c = new()
+            o = B.add_norm_bwd(c["dy"], c["dres"], c["res"], w, x=c["x"], scale=s,
+                               out={"dx": c[dx], "dres": c[dres], "dw": torch.empty_like(w), "dscale": torch.empty_like(w)})
+            assert all(torch.equal(o[k], a[k]) for k in a), (D, dx, dres)
