@@ -10,7 +10,9 @@ Subcommands (run with ``python -m chunked_gated_delta_08_amd.profiling``):
       Runs one listed case of perf/operators.py (an operator of the layer around
       the gated delta rule) R times over three sets of inputs.
   stats --csv <prefix>_kernel_stats.csv --out <txt> --cmd "<command>"
-      Writes a short text table of per-kernel dispatch counts and durations.
+      Writes a short text table of per-kernel dispatch counts and durations.  With
+      rocprofv3's --mangled-kernels the names are demangled here (its own demangling
+      does not know the 16-bit types).
   traffic --fetch CSV --write CSV --copy-fetch CSV --copy-write CSV
           --copy-mib M --workload W --cmd "<command>" --outdir DIR
       Turns per-dispatch FETCH_SIZE / WRITE_SIZE (KiB) of the library kernels
@@ -28,6 +30,8 @@ import hashlib
 import re
 import json
 import os
+import shutil
+import subprocess
 import sys
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -94,6 +98,16 @@ def short_name(full):
     return None
 
 
+def readable(name):
+    """A mangled kernel name in clear; other names as they are.  The demanglers at hand do not
+    know the 16-bit types (DF16_, DF16b), so two builtin types that no kernel has stand in."""
+    if not name.startswith("_Z") or shutil.which("c++filt") is None:
+        return name
+    name = re.sub(r"DF16_|DF16b", lambda m: {"DF16_": "e", "DF16b": "g"}[m[0]], name)
+    name = subprocess.run(["c++filt", name], capture_output=True, text=True, check=True).stdout.strip()
+    return name.replace("long double", "half").replace("__float128", "bf16")
+
+
 def _copy(args):
     import torch
     n = args.mib * (1 << 20) // 4
@@ -133,13 +147,13 @@ def _stats(args):
         nm = short_name(r["Name"])
         if nm is None and "FillFunctor" in r["Name"]:
             nm, evict = "bench_evict_fill", True
-        nm = nm or r["Name"][:28]
+        nm = nm or readable(r["Name"])[:28]
         lines.append(f"{nm:<28} {int(r['Calls']):>6} {float(r['AverageNs']) / 1e3:>10.1f} "
                      f"{float(r['MinNs']) / 1e3:>10.1f} {float(r['MaxNs']) / 1e3:>10.1f} "
                      f"{float(r['Percentage']):>8.2f}")
     if evict:
         lines += ["", "bench_evict_fill: bench.py's 512 MiB cache-evicting write before each call (outside the call)"]
-    lines += ["", "full kernel names:"] + [f"  {r['Name']}" for r in rows if short_name(r["Name"])]
+    lines += ["", "full kernel names:"] + [f"  {readable(r['Name'])}" for r in rows if short_name(r["Name"])]
     with open(args.out, "w") as fh:
         fh.write("\n".join(lines) + "\n")
     print("\n".join(lines))

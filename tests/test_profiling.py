@@ -1,6 +1,10 @@
 """CPU tests of the profile bookkeeping: a traffic summary stays valid while
 its kernel's code is unchanged (comments and layout do not count) and is
 ignored once the code changes."""
+import shutil
+
+import pytest
+
 from chunked_gated_delta_08_amd import profiling
 
 
@@ -24,3 +28,15 @@ def test_code_digest_follows_the_files(tmp_path, monkeypatch):
     assert profiling.source_digest(["k.hip"]) == d1
     f.write_text("__global__ void k() { int x = 0; }\n")
     assert profiling.source_digest(["k.hip"]) != d1
+
+
+@pytest.mark.skipif(shutil.which("c++filt") is None, reason="names stay as they are without c++filt")
+def test_kernel_names_in_clear():
+    name = "_ZN5layer12_GLOBAL__N_114glr_fwd_kernelI%sLi2ELi12EEEvNS_7GlrArgsEiib"
+    clear = "void layer::(anonymous namespace)::glr_fwd_kernel<%s, 2, 12>(layer::GlrArgs, int, int, bool)"
+    for code, t in (("DF16b", "bf16"), ("DF16_", "half"), ("f", "float")):
+        assert profiling.readable(name % code) == clear % t
+        assert profiling.short_name(name % code) == profiling.short_name(clear % t) == "glr_fwd_kernel"
+    both = "_ZN5layer12_GLOBAL__N_119add_norm_fwd_kernelIDF16bfLi4ELi256ELi2ELb1EEEvNS_8NormArgsE"
+    assert profiling.readable(both) == "void layer::(anonymous namespace)::add_norm_fwd_kernel<bf16, float, 4, 256, 2, true>(layer::NormArgs)"
+    assert profiling.readable(clear % "float") == clear % "float"
