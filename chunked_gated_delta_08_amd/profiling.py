@@ -145,7 +145,7 @@ def _stats(args):
     evict = False
     for r in rows:
         nm = short_name(r["Name"])
-        if nm is None and "FillFunctor" in r["Name"]:
+        if nm is None and "FillFunctor" in r["Name"] and "bench.py" in args.cmd:
             nm, evict = "bench_evict_fill", True
         nm = nm or readable(r["Name"])[:28]
         lines.append(f"{nm:<28} {int(r['Calls']):>6} {float(r['AverageNs']) / 1e3:>10.1f} "

@@ -40,3 +40,15 @@ def test_kernel_names_in_clear():
     both = "_ZN5layer12_GLOBAL__N_119add_norm_fwd_kernelIDF16bfLi4ELi256ELi2ELb1EEEvNS_8NormArgsE"
     assert profiling.readable(both) == "void layer::(anonymous namespace)::add_norm_fwd_kernel<bf16, float, 4, 256, 2, true>(layer::NormArgs)"
     assert profiling.readable(clear % "float") == clear % "float"
+
+
+def test_fills_are_the_evicting_write_in_the_bench_only(tmp_path):
+    fill = "void at::native::vectorized_elementwise_kernel<4, at::native::FillFunctor<float>, x>(int)"
+    csv = tmp_path / "k.csv"
+    csv.write_text("Name,Calls,TotalDurationNs,AverageNs,Percentage,MinNs,MaxNs\n" +
+                   f'"{fill}",3,5100,1700,50,1400,1900\n"layer::(anonymous namespace)::glr_clear_kernel(x)",3,5000,1700,50,1400,1900\n')
+    for cmd, evicts in (("python3 bench.py --steps 5", True), ("python3 -m x.profiling layer --case y", False)):
+        out = tmp_path / "out.txt"
+        profiling.main(["stats", "--csv", str(csv), "--out", str(out), "--cmd", cmd])
+        assert ("bench_evict_fill" in out.read_text()) == evicts
+        assert "glr_clear_kernel" in out.read_text()
