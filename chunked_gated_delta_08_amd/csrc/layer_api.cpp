@@ -84,7 +84,7 @@ int check_glr(const glr_problem* p, layer::GlrArgs* a) {
     *a = layer::GlrArgs{};
     a->ntok = (long)n; a->nseq = (int)nseq; a->T = p->T; a->D = p->D; a->dtype = p->dtype; a->cu = p->cu_seqlens;
     a->polls = p->polls > 0 ? p->polls : 4096;
-    // a launch has fewer than 2^32 threads
+    // a launch has fewer than 2^32 threads: 4 a token (of whole segments of 192 or 128) and 128 channels
     if (layer::glr_threads(*a) >= (int64_t)1 << 32 || (n == 0 && nseq * p->D >= (int64_t)1 << 31))
         return GDR_ERR_UNSUPPORTED;
     return GDR_OK;

@@ -98,7 +98,8 @@ int add_norm_bwd(const norm_problem *p, const void *dy, const void *dres, const 
  * batch, as in gdr.h: dense B sequences of T tokens, or (cu_seqlens != NULL,
  * B = 1) N sequences of T tokens in all, empty ones allowed. */
 typedef struct glr_problem {
-    int B, T;                       /* B >= 1, T >= 0, B*T <= 2^30 */
+    int B, T;                       /* B >= 1, T >= 0; B*T, rounded up to a multiple of 384, times
+                                       ceil(D / 128) < 2^30; without tokens N*D < 2^31 */
     int D;                          /* channels, 1 <= D <= 2^20 */
     int N;                          /* number of sequences when varlen; ignored when cu_seqlens == NULL */
     const int32_t *cu_seqlens;      /* device [N+1] or NULL (dense) */

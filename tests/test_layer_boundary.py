@@ -305,3 +305,18 @@ def test_steps_as_large_as_the_header_says(B):
         assert rule(B, N=N, HV=HV, slots=N, q=None) == -1, (N, HV)
     for N, HV in ((65536, 256), (16384, 1024)):
         assert rule(B, N=N, HV=HV, slots=N, q=None) == -2, (N, HV)
+
+
+def test_glr_as_large_as_the_header_says(B):
+    top = (1 << 30) // 384 * 384 - 384
+    for kw in (dict(T=top), dict(T=top - 1, D=128), dict(T=top // 8 // 384 * 384, D=1024), dict(T=1, D=1 << 20),
+               dict(Bb=1 << 10, T=96, D=1 << 20), dict(Bb=2047, T=0, D=1 << 20)):
+        for dtype in (0, 2):
+            p, _ = glr(B, dtype=dtype, **kw)
+            n = p.B * p.T
+            if n:
+                assert glr_fwd(B, p, x=None) == -1 and glr_bwd(B, p, x=None) == -1, kw
+            assert B.lib.glr_num_states(ctypes.byref(p)) == -(-n // 16), kw
+    for kw in (dict(T=1 << 30), dict(T=1 << 29, D=129), dict(T=1 << 27, D=1024), dict(Bb=2048, T=0, D=1 << 20)):
+        p, _ = glr(B, **kw)
+        assert glr_fwd(B, p) == -2 and glr_bwd(B, p) == -2 and B.lib.glr_num_states(ctypes.byref(p)) == -1, kw
