@@ -99,10 +99,12 @@ def short_name(full):
 
 
 def readable(name):
-    """A mangled kernel name in clear; other names as they are.  The demanglers at hand do not
-    know the 16-bit types (DF16_, DF16b), so two builtin types that no kernel has stand in."""
+    """A mangled kernel name (with or without the profiler's .kd) in clear; other names as they
+    are.  The demanglers at hand do not know the 16-bit types (DF16_, DF16b), so two builtin
+    types that no kernel has stand in."""
     if not name.startswith("_Z") or shutil.which("c++filt") is None:
         return name
+    name = name[:-3] if name.endswith(".kd") else name
     name = re.sub(r"DF16_|DF16b", lambda m: {"DF16_": "e", "DF16b": "g"}[m[0]], name)
     name = subprocess.run(["c++filt", name], capture_output=True, text=True, check=True).stdout.strip()
     return name.replace("long double", "half").replace("__float128", "bf16")

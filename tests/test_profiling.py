@@ -39,6 +39,7 @@ def test_kernel_names_in_clear():
         assert profiling.short_name(name % code) == profiling.short_name(clear % t) == "glr_fwd_kernel"
     both = "_ZN5layer12_GLOBAL__N_119add_norm_fwd_kernelIDF16bfLi4ELi256ELi2ELb1EEEvNS_8NormArgsE"
     assert profiling.readable(both) == "void layer::(anonymous namespace)::add_norm_fwd_kernel<bf16, float, 4, 256, 2, true>(layer::NormArgs)"
+    assert profiling.readable(both + ".kd") == profiling.readable(both)
     assert profiling.readable(clear % "float") == clear % "float"
 
 
