@@ -30,17 +30,20 @@
 // A product P of gates may overflow where the state itself would not, if gates
 // above 1 follow one another (include/gdn_layer.h bounds them); where it
 // underflows, what it multiplies is lost too.
-// Measured (bf16, D = 2048): one sequence of 32768 tokens 117 us forward, 4.6
-// TB/s of the 537 MB that it needs; 94 to 100 us with segments that do not wait
-// for one another (wrong results, the same traffic), so a fifth of the time is the
-// exchange: some 6 of the 17 us that a workgroup lives, two hops of 3.5 us from
-// one workgroup's store to another's load.  Forward and backward of twelve
-// sequences, 65536 tokens: 595 us (4.95 TB/s).  Without it, per step: whole rows
-// polled instead of one element 136 against 126 us; 8 tiles a segment against 12,
-// 126 against 118 us; a counter handing out segments (so that no workgroup could
+// Measured (bf16, D = 2048): one sequence of 32768 tokens 111 us forward and 6 to
+// clear the words, 4.6 TB/s of the 537 MB that it needs; 94 to 100 us with segments
+// that do not wait for one another (wrong results, the same traffic), so a fifth of
+// the time is the exchange: some 6 of the 17 us that a workgroup lives, two hops of
+// 3.5 us from one workgroup's store to another's load.  Forward and backward of
+// twelve sequences, 65536 tokens: 603 us (229 and 362, 11 to clear; 4.9 TB/s).
+// Tried, per step: whole rows polled instead of one element 136 against 126 us; 8
+// tiles a segment against 12, 126 against 118 us; a counter handing out segments (so that no workgroup could
 // wait for one that has not started) 6 to 8 % more, one per channel block 705
 // against 595 us forward and backward, since the blocks' rows then drift apart in
 // time; four channels a lane 190 against 140 us (154 registers, one workgroup a CU).
+// Registers: 80 a lane in the 16-bit forward of two channels a lane, whose bf16
+// instance spills one value more (8 bytes a lane); 36 to 70 uniform values of every kernel are
+// kept in lanes of vector registers.
 // The state is carried in fp32 throughout; h and dx are rounded once.  The
 // backward recomputes h_{t-1} from the states that the forward saved at every
 // tile, not from the rounded h: dg is an fp32 output.

@@ -7,8 +7,10 @@
 //   dx = s dh,  ds = sum_rows dh x,  dw = sum_rows dy n
 // y is formed from the unrounded h; the backward takes the stored res' for h.
 // Bound by HBM, built like the gated norm (layer_gated_norm.hip).  Measured:
-// forward 32768 x 2048 bf16 93 us (5.7 TB/s of 537 MB), backward 16384 x 4096 fp16
-// 148 us (5.4 TB/s of 805 MB), 5 x 2048 3 us, which is the launch.
+// forward 32768 x 2048 bf16 92 us (5.8 TB/s of 537 MB), backward 16384 x 4096 fp16
+// 142 us and 7 for the join (5.4 TB/s of 805 MB), 5 x 2048 3 to 4 us, which is the
+// launch.  No value is spilled but in the fp32 backward with a scale beyond D = 4096
+// (three).
 #include "layer_rows.hpp"
 
 namespace layer {

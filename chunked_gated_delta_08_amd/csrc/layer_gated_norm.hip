@@ -9,7 +9,8 @@
 // stays in registers over all rows of a persistent workgroup; the workgroups'
 // partial sums are joined in a fixed order by a second launch.
 // Measured (bf16, D = 128): 2^19 rows forward 67 us (6.0 TB/s of 403 MB), 2^21 rows
-// backward 519 us (5.2 TB/s of 2.68 GB, a large copy's rate); 128 rows 3 us, which
+// backward 521 us and 5 for the join (5.1 TB/s of 2.68 GB, near a large copy's rate;
+// 512 to 533 on other cards); 128 rows 3 to 4 us, which
 // is the launch.
 #include "layer_rows.hpp"
 
