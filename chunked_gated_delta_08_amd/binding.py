@@ -611,10 +611,10 @@ def norm_workspace_size(rows, D, dtype):
 
 
 def _workspace(workspace, size, like):
-    """(the workspace, its bytes, the tensor allocated for it or None), on the device of the
-    fp32 tensor `like`; no workspace for a size of 0."""
+    """(the workspace, its bytes, the tensor allocated for it or None), on the device of
+    the tensor `like`; no workspace for a size of 0."""
     if workspace is None:
-        ws = like.new_empty((size + 3) // 4) if size else None
+        ws = like.new_empty(-(-size // like.element_size())) if size else None
         return ws, size, ws
     _need(workspace, "workspace", torch.uint8)
     _same_device(like, workspace)
@@ -921,3 +921,111 @@ def gdr_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, stream=N
     _launch(v.device, stream, (o,) if out is None else (), lib.gdr_step, N, HK, HV, K, V, state.shape[0], scale or 0.0,
             _DT[v.dtype], _p(q), _p(k), _p(v), _p(g), _p(beta), _p(slots), _p(state), _p(o))
     return o
+
+
+# --------------------------------------------------------------------------
+# Gated feed-forward block (include/gdn_ffn.h).  Devices, streams, workspaces and
+# preallocated outputs as for the layer operators.
+
+class FfnProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int), ("F", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("act", ctypes.c_int)]
+
+
+FFN_ACTS = {"silu": 0, "sigmoid": 1, "gelu": 2}
+EXPORTED_FFN = ["ffn_workspace_size", "gated_ffn_fwd", "gated_ffn_bwd"]
+_fp = ctypes.POINTER(FfnProblem)
+lib.ffn_workspace_size.restype = _sz
+lib.ffn_workspace_size.argtypes = [_fp, _i]
+lib.gated_ffn_fwd.argtypes = [_fp] + [_vp] * 7 + [_sz, _vp]
+lib.gated_ffn_bwd.argtypes = [_fp] + [_vp] * 11 + [_sz, _vp]
+
+
+@functools.lru_cache(maxsize=1024)
+def _ffn_sizes(T, D, F, dtype, act):
+    """The struct of these sizes (calls only read it) and the workspaces it needs, forward and backward."""
+    p = FfnProblem(T, D, F, _DT[dtype], FFN_ACTS[act])
+    return p, tuple(int(lib.ffn_workspace_size(ctypes.byref(p), b)) for b in (0, 1))
+
+
+def ffn_workspace_size(T, D, F, dtype, bwd=False):
+    """Bytes of workspace gated_ffn_fwd (gated_ffn_bwd) needs."""
+    return _ffn_sizes(T, D, F, dtype, "silu")[1][bool(bwd)]
+
+
+def check_gated_ffn_args(x, w_gate, w_up, w_down, act="silu", saved=None, dy=None, bwd=False, cuda=True):
+    """x, dy [..., D]; w_gate, w_up [F, D]; w_down [D, F], all of one dtype; saved [T, 2F] fp32,
+    T the rows of x.  Returns T, D, F."""
+    _need(x, "x", cuda=cuda)
+    if x.dtype not in _DT:
+        raise TypeError(f"x has dtype {x.dtype}; expected one of {_FLOATS}")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., D]")
+    if act not in FFN_ACTS:
+        raise ValueError(f"act is {act!r}; expected one of {sorted(FFN_ACTS)}")
+    D = x.shape[-1]
+    T = x.numel() // D
+    _need(w_gate, "w_gate", x.dtype, cuda=cuda)
+    if w_gate.dim() != 2 or w_gate.shape[0] < 1 or w_gate.shape[1] != D:
+        raise ValueError(f"w_gate has shape {tuple(w_gate.shape)}, expected [F, {D}]")
+    F = w_gate.shape[0]
+    _need(w_up, "w_up", x.dtype, (F, D), cuda=cuda)
+    _need(w_down, "w_down", x.dtype, (D, F), cuda=cuda)
+    if bwd:
+        _need(saved, "saved", torch.float32, (T, 2 * F), cuda=cuda)
+        _need(dy, "dy", x.dtype, x.shape, cuda=cuda)
+    _same_device(x, w_gate, w_up, w_down, saved, dy)
+    piece = 16 // x.element_size()
+    if D % piece == 0 and F % piece == 0:
+        for t, name in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"), (dy, "dy")):
+            if t is not None and t.data_ptr() % 16:
+                raise ValueError(f"{name} must be aligned to 16 bytes (clone it)")
+    return T, D, F
+
+
+def gated_ffn_fwd(x, w_gate, w_up, w_down, act="silu", want_saved=False, out=None, workspace=None, stream=None):
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T over the last axis; act is "silu", "gelu"
+    (exact) or "sigmoid".  Returns dict y, saved (fp32 [T, 2F], what gated_ffn_bwd
+    needs, when wanted)."""
+    T, D, F = check_gated_ffn_args(x, w_gate, w_up, w_down, act)
+    own = []
+    if out is None:
+        out = {"y": torch.empty_like(x),
+               "saved": x.new_empty((T, 2 * F), dtype=torch.float32) if want_saved else None}
+        own += out.values()
+    else:
+        _need(out.get("y"), "y", x.dtype, x.shape)
+        _need(out.get("saved"), "saved", torch.float32, (T, 2 * F), optional=True)
+        _same_device(x, *out.values())
+    p, sizes = _ffn_sizes(T, D, F, x.dtype, act)
+    ws, size, mine = _workspace(workspace, sizes[0], x)
+    own.append(mine)
+    _launch(x.device, stream, own, lib.gated_ffn_fwd, p, _p(x), _p(w_gate), _p(w_up), _p(w_down), _p(out["y"]),
+            _p(out.get("saved")), _p(ws), size)
+    return out
+
+
+def gated_ffn_bwd(x, w_gate, w_up, w_down, saved, dy, act="silu", want_dx=True, want_dw=True, out=None,
+                  workspace=None, stream=None):
+    """Gradients of gated_ffn_fwd for dy of y; saved from gated_ffn_fwd(want_saved=True).
+    Returns dict dx, dw_gate, dw_up, dw_down, all in x's dtype (None where not wanted)."""
+    T, D, F = check_gated_ffn_args(x, w_gate, w_up, w_down, act, saved, dy, bwd=True)
+    own = []
+    if out is None:
+        out = {"dx": torch.empty_like(x) if want_dx else None,
+               "dw_gate": torch.empty_like(w_gate) if want_dw else None,
+               "dw_up": torch.empty_like(w_up) if want_dw else None,
+               "dw_down": torch.empty_like(w_down) if want_dw else None}
+        own += out.values()
+    else:
+        _need(out.get("dx"), "dx", x.dtype, x.shape, optional=True)
+        _need(out.get("dw_gate"), "dw_gate", x.dtype, w_gate.shape, optional=True)
+        _need(out.get("dw_up"), "dw_up", x.dtype, w_up.shape, optional=out.get("dw_gate") is None)
+        _need(out.get("dw_down"), "dw_down", x.dtype, w_down.shape, optional=True)
+        _same_device(x, *out.values())
+    p, sizes = _ffn_sizes(T, D, F, x.dtype, act)
+    ws, size, mine = _workspace(workspace, sizes[1], x)
+    own.append(mine)
+    _launch(x.device, stream, own, lib.gated_ffn_bwd, p, _p(x), _p(w_gate), _p(w_up), _p(w_down), _p(saved), _p(dy),
+            _p(out.get("dx")), _p(out.get("dw_gate")), _p(out.get("dw_up")), _p(out.get("dw_down")), _p(ws), size)
+    return out

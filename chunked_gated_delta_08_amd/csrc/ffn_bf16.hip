@@ -1,0 +1,8 @@
+// ffn_bf16.hip -- the feed-forward block's matrix products (ffn_gemm.hpp) in this type.
+#include "ffn_gemm.hpp"
+
+namespace ffn {
+hipError_t gemm_bf16(Kind kind, const GemmArgs& a, const Shape& sh, hipStream_t s) {
+    return run_gemm<bf16>(kind, a, sh.cfg, s);
+}
+}  // namespace ffn

@@ -1,0 +1,384 @@
+// ffn_gemm.hpp -- the matrix products of the gated feed-forward block
+// (include/gdn_ffn.h), compiled once for each type.
+//
+// out[m][n] = sum_k Q[m][k] P[n][k], P the first operand of the matrix
+// instruction, so that a lane holds four consecutive n of one m (element j of a
+// 16 x 16 block: n = 4g + j, m = r of lane 16g + r) and stores them at once.
+//
+// A workgroup owns a BM x BN tile.  Each step brings 128 bytes of k for its rows
+// (64 16-bit or 32 fp32 values) from memory straight into LDS, NST stages in a
+// ring, one barrier a step.  An operand lies in LDS as it lies in memory, k
+// contiguous ("direct") or k strided ("trans"), in pieces of 16 bytes whose place
+// in their row is permuted by the row so that fragment reads meet no bank twice:
+//   direct: [row][8 pieces], piece c at c ^ (row & 7); a fragment is one 16-byte read
+//   trans:  [k][row of the tile], piece c at c ^ swz(k); a 16-bit fragment is two
+//           transposing 8-byte reads, an fp32 one four 4-byte reads
+// The load's LDS side is fixed (lane i at 16 i), so it is the memory side that a
+// lane permutes.
+#pragma once
+#include "ffn_launch.hpp"
+#include "gdr_device.hpp"
+#include "layer_rows.hpp"
+#include "../../include/gdn_ffn.h"
+
+namespace ffn {
+using gdr::bf16;
+using gdr::f16;
+using gdr::f32x4;
+using gdr::i16x4;
+using gdr::i16x8;
+
+template <class E> struct Type {
+    static constexpr int CE = 16 / sizeof(E);    // elements in a piece of 16 bytes
+    static constexpr int KE = 128 / sizeof(E);   // k in a step
+    using frag = typename gdr::Mma<E>::frag;
+};
+template <> struct Type<float> {
+    static constexpr int CE = 4, KE = 32;
+    using frag = f32x4;
+};
+
+// Two fragments of a step cover its k: 32 16-bit values each (k = 32 s + 8 g + i), or 16 fp32
+// values each (k = 16 s + 4 g + j, element j in the j-th of four products).
+template <class E> __device__ __forceinline__ f32x4 mma(typename Type<E>::frag a, typename Type<E>::frag b, f32x4 c) {
+    if constexpr (sizeof(E) == 2) {
+        return gdr::Mma<E>::run(a, b, c);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) c = gdr::Mma<float>::run(a[j], b[j], c);
+        return c;
+    }
+}
+
+// The permutation of pieces of a "trans" row (see above); NC pieces a row.
+template <class E, int NC> __device__ __forceinline__ int swz(int k) {
+    const int x = sizeof(E) == 2 ? (2 * (k & 3)) ^ (8 * ((k >> 3) & 1)) : 4 * ((k >> 2) & 3);
+    return x & (NC - 1);
+}
+
+// 16 bytes of each lane from base + off to LDS at lds + 16 lane.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const char* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
+
+// One operand of a tile.  ROWS: BM or BN.  PAIR: rows of two matrices in turn, 16 of each.
+template <class E, int ROWS, int NW, bool TRANS, bool PAIR> struct Operand {
+    static constexpr int CE = Type<E>::CE, KE = Type<E>::KE;
+    static constexpr int UNITS = ROWS / 8, PER = (UNITS + NW - 1) / NW;   // KiB of a stage, of a wave's share
+    static constexpr int NC = TRANS ? ROWS * (int)sizeof(E) / 16 : 8;     // pieces in a row of LDS
+    static constexpr int BYTES = ROWS * 128;
+    static_assert(UNITS % NW == 0, "waves load alike");
+
+    uint32_t off[PER];      // of a lane's pieces from the base, for whole steps
+
+    __device__ __forceinline__ static int row_in(int u, int lane) { return (u * 64 + lane) / NC; }
+    __device__ __forceinline__ static int piece(int u, int lane) {
+        const int row = row_in(u, lane), slot = (u * 64 + lane) % NC;
+        return slot ^ (TRANS ? swz<E, NC>(row) : row & 7);
+    }
+    // first: the tile's first row (of each matrix of a pair); count: rows that exist
+    __device__ __forceinline__ void init(int first, int count, int64_t ld, int wave, int lane) {
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int u = wave + NW * i;
+            if constexpr (TRANS) {
+                int c = first + piece(u, lane) * CE;   // rows past the end: any that exist, their sums are not stored
+                c = c < count - CE ? c : count - CE;
+                off[i] = (uint32_t)((row_in(u, lane) * ld + c) * sizeof(E));
+            } else {
+                int r = PAIR ? (u / 4) * 16 + (u % 2) * 8 + lane / 8 : row_in(u, lane);
+                r = first + r < count ? r : count - 1 - first;
+                off[i] = (uint32_t)((r * ld + piece(u, lane) * CE) * sizeof(E));
+            }
+        }
+    }
+    // Loads step kt (k from kt KE on) into LDS at `lds`; p0, p1: the matrices, from row `first` on if direct.
+    __device__ __forceinline__ void load(uint32_t lds, const char* p0, const char* p1, int psplit, int64_t ld, int kt,
+                                         int K, int wave, int lane) const {
+        const int left = K - kt * KE;   // a last step may be short: k past the end are read at the last k
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int u = wave + NW * i;
+            const char* base;
+            uint32_t o = off[i];
+            if constexpr (TRANS) {
+                const int k0 = kt * KE + u * 64 / NC;
+                const bool second = p1 && k0 >= psplit;   // uniform: a unit's rows are on one side
+                base = (second ? p1 : p0) + (int64_t)(second ? kt * KE - psplit : kt * KE) * ld * (int64_t)sizeof(E);
+                if (left < KE) {
+                    const int over = row_in(u, lane) - (left - 1);
+                    if (over > 0) o -= (uint32_t)(over * ld * sizeof(E));
+                }
+            } else {
+                base = (PAIR && (u / 2) % 2 ? p1 : p0) + (int64_t)kt * 128;
+                if (left < KE) {
+                    const int over = (piece(u, lane) + 1) * CE - left;
+                    if (over > 0) o -= (uint32_t)(over * sizeof(E));
+                }
+            }
+            load_to_lds(lds + u * 1024, base, o);
+        }
+    }
+    // Zero for the k past the end in the pieces that this lane loaded.
+    __device__ __forceinline__ void clear_tail(char* lds, int left, int wave, int lane) const {
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int u = wave + NW * i;
+            const bool past = TRANS ? row_in(u, lane) >= left : piece(u, lane) * CE >= left;
+            if (past) *(f32x4*)(lds + u * 1024 + lane * 16) = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+    // Fragment s of the 16 rows from w0 + 16 i on.
+    __device__ __forceinline__ static typename Type<E>::frag frag(const char* lds, int w0, int i, int s, int lane) {
+        const int r = lane & 15, g = lane >> 4;
+        using F = typename Type<E>::frag;
+        if constexpr (!TRANS) {
+            return *(const F*)(lds + (w0 + 16 * i + r) * 128 + ((4 * s + g) ^ (r & 7)) * 16);
+        } else if constexpr (sizeof(E) == 2) {
+            const int x = swz<E, NC>(8 * g + (r >> 2));
+            const char* p = lds + (32 * s + 8 * g + (r >> 2)) * (ROWS * 2) +
+                            (((w0 + 16 * i) / 8 + ((r >> 1) & 1)) ^ x) * 16 + (r & 1) * 8;
+            const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, p));
+            const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, p + 4 * ROWS * 2));
+            const i16x8 c = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            return __builtin_bit_cast(F, c);
+        } else {
+            const char* p = lds + (16 * s + 4 * g) * (ROWS * 4) +
+                            (((w0 + 16 * i) / 4 + (r >> 2)) ^ swz<E, NC>(4 * g)) * 16 + (r & 3) * 4;
+            F f;
+#pragma unroll
+            for (int j = 0; j < 4; j++) f[j] = *(const float*)(p + j * ROWS * 4);
+            return f;
+        }
+    }
+};
+
+// ----------------------------------------------------------------- epilogues
+// sigmoid_f: layer_rows.hpp.  gelu: x Phi(x), Phi by the complementary error
+// function, which keeps its digits where x is far below zero.
+__device__ __forceinline__ float act_f(float x, int act) {
+    if (act == GDN_FFN_GELU) return 0.5f * x * erfcf(-x * 0.70710678f);
+    const float s = layer::sigmoid_f(x);
+    return act == GDN_FFN_SILU ? x * s : s;
+}
+// act(x) and its slope; 1 - sigmoid(x) is sigmoid(-x), which keeps its digits.
+__device__ __forceinline__ void act_slope(float x, int act, float& a, float& d) {
+    if (act == GDN_FFN_GELU) {
+        const float phi = 0.5f * erfcf(-x * 0.70710678f);
+        a = x * phi;
+        d = phi + x * 0.39894228f * expf(-0.5f * x * x);
+        return;
+    }
+    const float s = layer::sigmoid_f(x), t = layer::sigmoid_f(-x);
+    a = act == GDN_FFN_SILU ? x * s : s;
+    d = act == GDN_FFN_SILU ? s * (1.f + x * t) : s * t;
+}
+
+// Four consecutive elements of a row, those of them before `end`.
+template <class E> __device__ __forceinline__ void store4(E* row, int64_t n, int64_t end, f32x4 v) {
+    typedef typename layer::VecU<E, 4>::t V;
+    if (n + 4 <= end) {
+        V t;
+#pragma unroll
+        for (int e = 0; e < 4; e++) t[e] = (E)v[e];
+        *(V*)(row + n) = t;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (n + e < end) row[n + e] = (E)v[e];
+    }
+}
+__device__ __forceinline__ f32x4 load4(const float* row, int n, int end) {
+    typedef typename layer::VecU<float, 4>::t V;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (n + 4 <= end) {
+        const V t = *(const V*)(row + n);
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = t[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (n + e < end) v[e] = row[n + e];
+    }
+    return v;
+}
+
+// What becomes of four sums (n .. n+3 of row m): v of the product, w of the pair's second matrix.
+template <class E, int KIND> __device__ __forceinline__ void finish(const GemmArgs& a, int m, int n, f32x4 v, f32x4 w) {
+    if constexpr (KIND == GATE_UP) {
+        if (a.gu) {   // kept in fp32: rounded to the type they would add as much error to the gradients as the operands do
+            float* row = a.gu + (int64_t)m * 2 * a.F;
+            store4<float>(row, n, a.F, v);
+            store4<float>(row + a.F, n, a.F, w);
+        }
+        f32x4 h;
+#pragma unroll
+        for (int e = 0; e < 4; e++) h[e] = act_f(v[e], a.act) * w[e];
+        store4<E>((E*)a.h + (int64_t)m * a.N, n, a.N, h);
+    } else if constexpr (KIND == DH) {
+        const float* row = a.gu + (int64_t)m * 2 * a.F;
+        const f32x4 g = load4(row, n, a.F), u = load4(row + a.F, n, a.F);
+        f32x4 dg, du, h;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            float act, slope;
+            act_slope(g[e], a.act, act, slope);
+            dg[e] = v[e] * u[e] * slope;
+            du[e] = v[e] * act;
+            h[e] = act * u[e];
+        }
+        E* d = (E*)a.dgu + (int64_t)m * 2 * a.N;
+        store4<E>(d, n, a.N, dg);
+        store4<E>(d + a.N, n, a.N, du);
+        store4<E>((E*)a.h + (int64_t)m * a.N, n, a.N, h);
+    } else {
+        const bool second = m >= a.osplit;
+        if (second) m -= a.osplit;
+        if (m < a.rows_out) store4<E>((E*)(second ? a.out1 : a.out0) + m * a.ldo, n, a.cols_out, v);
+    }
+}
+
+template <class E, int KIND, int BM, int BN, int WM, int WN, int NST>
+__global__ __launch_bounds__(64 * WM * WN) void ffn_gemm_kernel(GemmArgs a) {
+    constexpr bool PAIR = KIND == GATE_UP, QT = KIND == DW, PT = KIND == DH || KIND == DX || KIND == DW;
+    constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16, KE = Type<E>::KE;
+    constexpr int BT = PAIR ? BN / 2 : BN;      // columns of a tile
+    using Q = Operand<E, BM, NW, QT, false>;
+    using P = Operand<E, BN, NW, PT, PAIR>;
+    constexpr int STAGE = Q::BYTES + P::BYTES, LOADS = Q::PER + P::PER;
+    __shared__ __attribute__((aligned(1024))) char smem[NST * STAGE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+
+    // Workgroups go to the chip's 8 parts in turn; each part takes a run of tiles, and within
+    // it 8 rows of tiles at a time, so that its L2 serves an operand's tile to several.
+    const int tiles = a.tilesM * a.tilesN, total = tiles * a.splits;
+    const int xcd = blockIdx.x & 7, per = total >> 3, rem = total & 7;
+    int id = xcd * per + (xcd < rem ? xcd : rem) + (int)(blockIdx.x >> 3);
+    const int split = id / tiles;
+    id -= split * tiles;
+    const int group = id / (8 * a.tilesN), in = id - group * 8 * a.tilesN;
+    const int high = a.tilesM - group * 8 < 8 ? a.tilesM - group * 8 : 8;
+    const int m0 = (group * 8 + in % high) * BM, n0 = in / high * BT;
+
+    const int all = (a.K + KE - 1) / KE, k0 = split * a.steps, k1 = k0 + a.steps < all ? k0 + a.steps : all;
+    Q q;
+    P p;
+    q.init(QT ? m0 : m0, a.M, a.ldq, wave, lane);
+    p.init(n0, a.N, a.ldp, wave, lane);
+    const char* qb = (const char*)a.q + (QT ? 0 : (int64_t)m0 * a.ldq * (int64_t)sizeof(E));
+    const char* pb0 = (const char*)a.p0 + (PT ? 0 : (int64_t)n0 * a.ldp * (int64_t)sizeof(E));
+    const char* pb1 = a.p1 ? (const char*)a.p1 + (PT ? 0 : (int64_t)n0 * a.ldp * (int64_t)sizeof(E)) : nullptr;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)LDS_PTR(char, smem);
+    auto load = [&](int kt, int stage) {
+        q.load(lds0 + stage * STAGE, qb, nullptr, 0, a.ldq, kt, a.K, wave, lane);
+        p.load(lds0 + stage * STAGE + Q::BYTES, pb0, pb1, a.psplit, a.ldp, kt, a.K, wave, lane);
+    };
+
+    f32x4 acc[TN][TM];
+#pragma unroll
+    for (int j = 0; j < TN; j++)
+#pragma unroll
+        for (int i = 0; i < TM; i++) acc[j][i] = gdr::zero4();
+
+#pragma unroll
+    for (int t = 0; t < NST - 1; t++)
+        if (k0 + t < k1) load(k0 + t, t);
+    int stage = 0, ahead = NST - 1;
+    for (int kt = k0; kt < k1; kt++) {
+        // this wave's part of the step has landed; the steps after it may be on their way
+        if (kt + NST - 2 < k1) wait_loads<(NST - 2) * LOADS>();
+        else wait_loads<0>();
+        char* cur = smem + stage * STAGE;
+        if (a.K - kt * KE < KE) {
+            q.clear_tail(cur, a.K - kt * KE, wave, lane);
+            p.clear_tail(cur + Q::BYTES, a.K - kt * KE, wave, lane);
+        }
+        gdr::lds_barrier();   // everyone's part has landed, and nobody reads the stage that is loaded next
+        if (kt + NST - 1 < k1) load(kt + NST - 1, ahead);
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            typename Type<E>::frag fp[TN], fq[TM];
+#pragma unroll
+            for (int i = 0; i < TM; i++) fq[i] = Q::frag(cur, wm * TM * 16, i, s, lane);
+#pragma unroll
+            for (int j = 0; j < TN; j++) fp[j] = P::frag(cur + Q::BYTES, wn * TN * 16, j, s, lane);
+#pragma unroll
+            for (int j = 0; j < TN; j++)
+#pragma unroll
+                for (int i = 0; i < TM; i++) acc[j][i] = mma<E>(fp[j], fq[i], acc[j][i]);
+        }
+        stage = stage + 1 == NST ? 0 : stage + 1;
+        ahead = ahead + 1 == NST ? 0 : ahead + 1;
+    }
+
+    const int r = lane & 15, g = lane >> 4;
+    constexpr int STEP = PAIR ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < TM; i++) {
+        const int m = m0 + wm * TM * 16 + 16 * i + r;
+        if (m >= a.M) continue;
+#pragma unroll
+        for (int j = 0; j < TN; j += STEP) {
+            const int n = n0 + wn * (TN / STEP) * 16 + 16 * (j / STEP) + 4 * g;
+            if (n >= a.N) continue;
+            if (a.splits > 1) {
+                float* row = a.part + ((int64_t)split * a.M + m) * STEP * a.N;
+                *(f32x4*)(row + n) = acc[j][i];
+                if constexpr (PAIR) *(f32x4*)(row + a.N + n) = acc[j + 1][i];
+            } else {
+                finish<E, KIND>(a, m, n, acc[j][i], acc[j + STEP - 1][i]);
+            }
+        }
+    }
+}
+
+// The splits' sums in their order, and what becomes of them: four columns a lane.
+template <class E, int KIND> __global__ __launch_bounds__(256) void ffn_join_kernel(GemmArgs a) {
+    constexpr int STEP = KIND == GATE_UP ? 2 : 1;
+    const int quads = a.N / 4;
+    const int64_t total = (int64_t)a.M * quads, plane = (int64_t)a.M * STEP * a.N;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+        const int m = (int)(id / quads), n = 4 * (int)(id % quads);
+        const float* p = a.part + (int64_t)m * STEP * a.N + n;
+        f32x4 v = *(const f32x4*)p, w = *(const f32x4*)(p + (STEP - 1) * a.N);
+        for (int s = 1; s < a.splits; s++) {
+            v += *(const f32x4*)(p + s * plane);
+            if constexpr (STEP == 2) w += *(const f32x4*)(p + s * plane + a.N);
+        }
+        finish<E, KIND>(a, m, n, v, w);
+    }
+}
+
+template <class E, int KIND, int BM, int BN, int WM, int WN, int NST>
+hipError_t run_shape(const GemmArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((ffn_gemm_kernel<E, KIND, BM, BN, WM, WN, NST>), dim3((unsigned)(a.tilesM * a.tilesN * a.splits)),
+                       dim3(64 * WM * WN), 0, s, a);
+    if (a.splits > 1) {
+        const int64_t n = ((int64_t)a.M * (a.N / 4) + 255) / 256;
+        hipLaunchKernelGGL((ffn_join_kernel<E, KIND>), dim3((unsigned)(n < 4096 ? n : 4096)), dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+template <class E, int KIND> hipError_t run_kind(const GemmArgs& a, int cfg, hipStream_t s) {
+    switch (cfg) {
+        case 0: return run_shape<E, KIND, 256, 256, 2, 4, 2>(a, s);
+        case 1: return run_shape<E, KIND, 128, 128, 2, 2, 2>(a, s);
+        case 2: return run_shape<E, KIND, 64, 64, 2, 2, 4>(a, s);
+        default: return run_shape<E, KIND, 32, 64, 2, 2, 6>(a, s);
+    }
+}
+template <class E> hipError_t run_gemm(Kind kind, const GemmArgs& a, int cfg, hipStream_t s) {
+    switch (kind) {
+        case GATE_UP: return run_kind<E, GATE_UP>(a, cfg, s);
+        case DOWN: return run_kind<E, DOWN>(a, cfg, s);
+        case DH: return run_kind<E, DH>(a, cfg, s);
+        case DX: return run_kind<E, DX>(a, cfg, s);
+        default: return run_kind<E, DW>(a, cfg, s);
+    }
+}
+
+}  // namespace ffn

@@ -1,0 +1,54 @@
+// ffn_launch.hpp -- host-side plan and launchers of the gated feed-forward block
+// (include/gdn_ffn.h; internal).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ffn {
+
+// One product out[m][n] = sum_k Q[m][k] P[n][k].  Leading dimensions are in
+// elements; every row that is read begins on 16 bytes.
+struct GemmArgs {
+    const void* q; int64_t ldq;                     // Q stored [m][k], or [k][m]
+    const void* p0; const void* p1; int64_t ldp;    // P stored [n][k], or [k][n]; the second matrix of a pair
+    int psplit;                                     // P stored [k][n]: rows from psplit on are p1's
+    int M, N, K;                                    // N of one matrix of a pair
+    int tilesM, tilesN, splits, steps;              // steps: k-steps of a split
+    float* part;                                    // splits > 1: sums of each split, [split][M][width of a row]
+    // epilogue
+    void* out0; void* out1; int64_t ldo;            // plain: rows from osplit on are out1's
+    int osplit, rows_out, cols_out;                 // rows of each that exist, columns that exist
+    float* gu; int F;                               // gate and up before the activation, [M][2 F], F columns exist
+    void* h; void* dgu;                             // [M][N], [M][2 N]
+    int act;
+};
+
+enum Kind { GATE_UP, DOWN, DH, DX, DW };            // which product: orientations and epilogue
+
+// A tensor to copy into rows of another length: dst[r][c] = src[r][c] where that exists, else zero.
+struct PadItem {
+    const void* src; void* dst;
+    int64_t rows, rows_dst;
+    int cols, cols_dst;
+};
+struct PadArgs {
+    PadItem item[5];
+    int n;
+};
+
+// Tile shape and number of splits along k of a product.
+struct Shape {
+    int cfg, bm, bn, splits, steps, tilesM, tilesN;
+};
+Shape shape_of(Kind kind, int M, int N, int K, int esize);
+size_t part_floats(Kind kind, int M, int N, int K, int esize);
+
+hipError_t launch_gemm(int dtype, Kind kind, GemmArgs a, hipStream_t s);
+hipError_t launch_pad(int esize, const PadArgs& a, hipStream_t s);
+
+hipError_t gemm_bf16(Kind kind, const GemmArgs& a, const Shape& sh, hipStream_t s);
+hipError_t gemm_f16(Kind kind, const GemmArgs& a, const Shape& sh, hipStream_t s);
+hipError_t gemm_f32(Kind kind, const GemmArgs& a, const Shape& sh, hipStream_t s);
+
+}  // namespace ffn
