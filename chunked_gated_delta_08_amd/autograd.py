@@ -1,6 +1,6 @@
 """torch.autograd wrappers around the library's chunked forward and backward, and
 around the operators that stand beside it in a layer (gated RMSNorm, residual add
-with RMSNorm, gated linear recurrence).
+with RMSNorm, dropout, gated feed-forward block, gated linear recurrence).
 
 FlashQLA backward explainer §一: the chunked gated delta rule is exposed to
 training code as one autograd function; its forward saves the gate as the
@@ -168,3 +168,93 @@ def gated_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, cu_seqlen
     chunk_gated_delta_rule; cu_seqlens_host, its CPU copy, avoids a copy in each pass.
     The final state is fp32."""
     return GatedLinearRecurrence.apply(*_contiguous(x, g, initial_state), cu_seqlens, cu_seqlens_host, B)
+
+
+def _rng(rng):
+    """(the tensor to save or None, the numbers or None)"""
+    return (rng, None) if isinstance(rng, torch.Tensor) else (None, (int(rng[0]), int(rng[1])))
+
+
+class Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, rng):
+        x = x.contiguous()
+        t, ctx.numbers = _rng(rng)
+        ctx.save_for_backward(t)
+        ctx.p = p
+        return binding.dropout(x, p, rng)
+
+    @staticmethod
+    def backward(ctx, dy):
+        # linear in dy: differentiating it again is the same call
+        return Dropout.apply(dy.contiguous(), ctx.p, ctx.numbers or ctx.saved_tensors[0]), None, None
+
+
+def dropout(x, p, rng):
+    """x / (1 - p) where the generator keeps the element, else 0 (p to the nearest 2^-16).
+
+    rng: (seed, offset), or an int64 tensor [2] on the GPU that holds them and must not
+    change before the backward.  The mask is a function of rng and of the element's row
+    and column in x [..., D]; it is not stored.  Calls that shall differ take another offset.
+    Differentiable in x, any number of times."""
+    return Dropout.apply(x.contiguous(), p, rng)
+
+
+class DropoutAddRMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, res, w, scale, p, rng, eps):
+        x, res, w = x.contiguous(), res.contiguous(), w.contiguous()
+        scale = None if scale is None else scale.contiguous()
+        out = binding.dropout_add_norm_fwd(x, res, w, p, rng, scale=scale, eps=eps)
+        t, ctx.numbers = _rng(rng)
+        ctx.save_for_backward(None if scale is None else x, out["res"], w, scale, t)
+        ctx.cfg = (p, eps, x.dtype)
+        ctx.set_materialize_grads(False)   # an unused residual stream has no gradient to read
+        return out["y"], out["res"]
+
+    @staticmethod
+    def backward(ctx, dy, dres):
+        x, res, w, scale, t = ctx.saved_tensors
+        p, eps, dtype = ctx.cfg
+        incoming = (dy, dres)
+        dy = torch.zeros_like(res, dtype=dtype) if dy is None else dy.contiguous()
+        dres = None if dres is None else dres.contiguous()
+        r = binding.dropout_add_norm_bwd(dy, dres, res, w, p, ctx.numbers or t, x=x, scale=scale, eps=eps)
+        return _first_order("dropout_add_rms_norm", ctx, incoming,
+                            (r["dx"], r["dres"], r["dw"], r["dscale"], None, None, None))
+
+
+def dropout_add_rms_norm(x, res, weight, p, rng, scale=None, eps=1e-5):
+    """y, res' = the residual stream res' = res + scale dropout(x, p, rng) and y = RMSNorm(res') weight,
+    in one pass.  As add_rms_norm; p and rng as for dropout."""
+    return DropoutAddRMSNorm.apply(*_contiguous(x, res, weight, scale), p, rng, eps)
+
+
+class GatedFFN(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, w_down, act, keep):
+        x, w_gate, w_up, w_down = (t.contiguous() for t in (x, w_gate, w_up, w_down))
+        out = binding.gated_ffn_fwd(x, w_gate, w_up, w_down, act=act, want_saved=keep)
+        if keep:
+            ctx.save_for_backward(x, w_gate, w_up, w_down, out["saved"])
+            ctx.act = act
+        return out["y"]
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w_gate, w_up, w_down, saved = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        r = binding.gated_ffn_bwd(x, w_gate, w_up, w_down, saved, dy.contiguous(), act=ctx.act, want_dx=need[0],
+                                  want_dw=any(need[1:4]))
+        return _first_order("gated_ffn", ctx, (dy,), tuple(
+            r[k] if n else None for k, n in zip(("dx", "dw_gate", "dw_up", "dw_down"), need)) + (None, None))
+
+
+def gated_ffn(x, w_gate, w_up, w_down, act="silu"):
+    """(act(x w_gate^T) * (x w_up^T)) w_down^T over x [..., D]; w_gate, w_up [F, D], w_down [D, F], all of
+    x's dtype.  act is "silu", "gelu" (exact) or "sigmoid".
+
+    Differentiable in x and the weights; the gradients are in x's dtype.  Between the passes it keeps
+    [T, 2F] fp32, the gate and the up row of each token."""
+    t = _contiguous(x, w_gate, w_up, w_down)
+    return GatedFFN.apply(*t, act, torch.is_grad_enabled() and any(v.requires_grad for v in t))

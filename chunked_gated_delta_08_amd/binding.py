@@ -492,7 +492,7 @@ def bigdn_bwd(qkv, beta, decay, qw, kw, cos, sin, dout, F, S, k_scale=1.0, norm_
 
 # --------------------------------------------------------------------------
 # Layer operators (include/gdn_layer.h): gated RMSNorm, residual add with
-# RMSNorm, gated linear recurrence, single-token steps.  Every tensor of a call
+# RMSNorm, dropout, gated linear recurrence, single-token steps.  Every tensor of a call
 # is on one device, which need not be the current one; `stream` (default: that
 # device's current stream) belongs to it; where a call allocates its outputs or
 # workspace, that stream first waits for the current one, whose memory they may
@@ -511,10 +511,15 @@ class GlrProblem(ctypes.Structure):
                 ("polls", ctypes.c_int)]
 
 
+class Dropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("rng", ctypes.c_void_p)]
+
+
 GLR_TILE = 16
 ACTS = {"silu": 0, "sigmoid": 1}
 EXPORTED_LAYER = ["norm_workspace_size", "gated_norm_fwd", "gated_norm_bwd", "add_norm_fwd", "add_norm_bwd",
-                  "glr_num_states", "glr_workspace_size", "glr_fwd", "glr_bwd", "glr_step", "gdr_step"]
+                  "gdn_dropout_fwd", "dropout_add_norm_fwd", "dropout_add_norm_bwd", "glr_num_states",
+                  "glr_workspace_size", "glr_fwd", "glr_bwd", "glr_step", "gdr_step"]
 _i, _i64, _f = ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _np, _gp = ctypes.POINTER(NormProblem), ctypes.POINTER(GlrProblem)
 lib.norm_workspace_size.restype = _sz
@@ -523,6 +528,10 @@ lib.gated_norm_fwd.argtypes = [_np] + [_vp] * 5
 lib.gated_norm_bwd.argtypes = [_np] + [_vp] * 8 + [_sz, _vp]
 lib.add_norm_fwd.argtypes = [_np] + [_vp] * 7
 lib.add_norm_bwd.argtypes = [_np] + [_vp] * 11 + [_sz, _vp]
+_dp = ctypes.POINTER(Dropout)
+lib.gdn_dropout_fwd.argtypes = [_i64, _i64, _i, _dp] + [_vp] * 3
+lib.dropout_add_norm_fwd.argtypes = [_np, _dp] + [_vp] * 7
+lib.dropout_add_norm_bwd.argtypes = [_np, _dp] + [_vp] * 11 + [_sz, _vp]
 lib.glr_num_states.restype = _i64
 lib.glr_num_states.argtypes = [_gp]
 lib.glr_workspace_size.restype = _sz
@@ -671,9 +680,60 @@ def check_add_norm_args(x, res, w, scale=None, cuda=True):
     _same_device(x, res, w, scale)
 
 
+def check_dropout_args(x, p, rng, cuda=True):
+    """0 <= p <= 1; rng: (seed, offset), whole numbers taken modulo 2^64, or an int64 tensor [2] on x's device."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p is {p}; expected a probability")
+    if isinstance(rng, torch.Tensor):
+        _need(rng, "rng", torch.int64, (2,), cuda=cuda)
+        _same_device(x, rng)
+    elif len(rng) != 2:
+        raise ValueError("rng must be (seed, offset) or an int64 tensor [2]")
+
+
+def _dropout(p, rng):
+    if isinstance(rng, torch.Tensor):
+        return Dropout(p, 0, 0, rng.data_ptr())
+    return Dropout(p, int(rng[0]) & 0xFFFFFFFFFFFFFFFF, int(rng[1]) & 0xFFFFFFFFFFFFFFFF, None)
+
+
+def dropout(x, p, rng, out=None, stream=None):
+    """y = x / (1 - p) where the generator keeps the element, else 0; p to the nearest 2^-16.
+    The mask is a function of rng = (seed, offset) and of the element's row and column in
+    x [..., D]: the gradient is dropout(dy, p, rng).  An rng that is a tensor on the GPU is
+    read when the kernel runs, so each replay of a graph may have its own.  out may be x."""
+    _need(x, "x")
+    if x.dtype not in _DT:
+        raise TypeError(f"x has dtype {x.dtype}; expected one of {_FLOATS}")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    check_dropout_args(x, p, rng)
+    if out is None:
+        y = torch.empty_like(x)
+    else:
+        y = out
+        _need(y, "out", x.dtype, x.shape)
+        _same_device(x, y)
+    D = x.shape[-1]
+    if D:
+        _launch(x.device, stream, (y,) if out is None else (), lib.gdn_dropout_fwd, x.numel() // D, D, _DT[x.dtype],
+                _dropout(p, rng), _p(x), _p(y))
+    return y
+
+
 def add_norm_fwd(x, res, w, scale=None, eps=1e-5, out=None, stream=None):
     """res' = res + scale x and y = RMSNorm(res') w.  Returns dict y (x's dtype), res
     (res's dtype).  out={"y": ..., "res": res} updates the residual stream in place."""
+    return _add_norm_fwd(lib.add_norm_fwd, (), x, res, w, scale, eps, out, stream)
+
+
+def dropout_add_norm_fwd(x, res, w, p, rng, scale=None, eps=1e-5, out=None, stream=None):
+    """add_norm_fwd of dropout(x, p, rng), in one pass."""
+    check_dropout_args(x, p, rng)
+    return _add_norm_fwd(lib.dropout_add_norm_fwd, (_dropout(p, rng),), x, res, w, scale, eps, out, stream)
+
+
+def _add_norm_fwd(call, drop, x, res, w, scale, eps, out, stream):
     check_add_norm_args(x, res, w, scale)
     own = ()
     if out is None:
@@ -684,7 +744,7 @@ def add_norm_fwd(x, res, w, scale=None, eps=1e-5, out=None, stream=None):
         _need(out.get("res"), "res", res.dtype, x.shape)
         _same_device(x, *out.values())
     p, _ = _norm_problem(x, eps, res.dtype)
-    _launch(x.device, stream, own, lib.add_norm_fwd, p, _p(x), _p(res), _p(w), _p(scale), _p(out["y"]), _p(out["res"]))
+    _launch(x.device, stream, own, call, p, *drop, _p(x), _p(res), _p(w), _p(scale), _p(out["y"]), _p(out["res"]))
     return out
 
 
@@ -702,27 +762,39 @@ def add_norm_bwd(dy, dres, res, w, x=None, scale=None, eps=1e-5, out=None, works
     """Gradients of add_norm_fwd: dy of y, dres (None: zero) of res', at res = the
     forward's res'.  Returns dict dx (dy's dtype), dres, dw, dscale (None without
     scale).  Without scale and in one dtype, dx is dres, the same tensor."""
+    return _add_norm_bwd(lib.add_norm_bwd, (), dy, dres, res, w, x, scale, eps, out, workspace, stream)
+
+
+def dropout_add_norm_bwd(dy, dres, res, w, p, rng, x=None, scale=None, eps=1e-5, out=None, workspace=None,
+                         stream=None):
+    """Gradients of dropout_add_norm_fwd, as add_norm_bwd's; dx is always a tensor of its own."""
+    check_dropout_args(dy, p, rng)
+    return _add_norm_bwd(lib.dropout_add_norm_bwd, (_dropout(p, rng),), dy, dres, res, w, x, scale, eps, out, workspace,
+                         stream)
+
+
+def _add_norm_bwd(call, drop, dy, dres, res, w, x, scale, eps, out, workspace, stream):
     check_add_norm_bwd_args(dy, dres, res, w, x, scale)
     own = []
     if out is None:
         d = torch.empty_like(res)
-        out = {"dx": d if scale is None and dy.dtype == res.dtype else torch.empty_like(dy), "dres": d,
+        out = {"dx": d if scale is None and not drop and dy.dtype == res.dtype else torch.empty_like(dy), "dres": d,
                "dw": torch.empty_like(w), "dscale": None if scale is None else torch.empty_like(scale)}
         own += out.values()
     else:
         _need(out.get("dres"), "dres", res.dtype, res.shape)
-        _need(out.get("dx"), "dx", dy.dtype, dy.shape, optional=scale is None)
+        _need(out.get("dx"), "dx", dy.dtype, dy.shape, optional=scale is None and not drop)
         _need(out.get("dw"), "dw", torch.float32, w.shape)
         _need(out.get("dscale"), "dscale", torch.float32, w.shape, optional=scale is None)
         _same_device(dy, *out.values())
     dx = out.get("dx")
-    if scale is None and dx is out["dres"]:
+    if scale is None and not drop and dx is out["dres"]:
         dx = None
     ds = None if scale is None else out["dscale"]
     p, size = _norm_problem(dy, eps, res.dtype)
     ws, size, mine = _workspace(workspace, size, w)
     own.append(mine)
-    _launch(dy.device, stream, own, lib.add_norm_bwd, p, _p(dy), _p(dres), _p(res), _p(w), _p(x), _p(scale), _p(dx),
+    _launch(dy.device, stream, own, call, p, *drop, _p(dy), _p(dres), _p(res), _p(w), _p(x), _p(scale), _p(dx),
             _p(out["dres"]), _p(out["dw"]), _p(ds), _p(ws), size)
     return out
 

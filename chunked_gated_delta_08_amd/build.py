@@ -19,7 +19,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 HIP_SOURCES = ["gdr_prep.hip", "gdr_scan.hip", "gdr_grad.hip", "kda_bwd.hip", "gdr_fwd.hip", "kda_full.hip",
-               "bigdn.hip", "gdr_noalloc.hip", "layer_gated_norm.hip", "layer_add_norm.hip", "layer_step.hip", "glr.hip",
+               "bigdn.hip", "gdr_noalloc.hip", "layer_gated_norm.hip", "layer_add_norm.hip", "layer_step.hip", "glr.hip", "layer_dropout.hip",
                "ffn.hip", "ffn_bf16.hip", "ffn_f16.hip", "ffn_f32.hip"]
 # per-source device flags: the WY-factor, scan and KDA kernels keep MFMA
 # accumulators in VGPRs; the gradient and forward-output kernels are left to

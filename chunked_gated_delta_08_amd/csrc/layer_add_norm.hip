@@ -5,12 +5,15 @@
 //   h = res + s x,  r = (sum h^2 / D + eps)^(-1/2),  n = h r,  y = n w,  res' = h
 //   dn = dy w,  dh = dres + r (dn - n mean(dn n)),
 //   dx = s dh,  ds = sum_rows dh x,  dw = sum_rows dy n
+// With dropout (DROP) x stands for m x, m = 1 / (1 - p) or 0 from the generator of
+// layer_dropout.hpp, in the backward again: dx = m s dh, ds = sum_rows dh m x.
 // y is formed from the unrounded h; the backward takes the stored res' for h.
 // Bound by HBM, built like the gated norm (layer_gated_norm.hip).  Measured:
 // forward 32768 x 2048 bf16 92 us (5.8 TB/s of 537 MB), backward 16384 x 4096 fp16
 // 142 us and 7 for the join (5.4 TB/s of 805 MB), 5 x 2048 3 to 4 us, which is the
 // launch.  No value is spilled but in the fp32 backward with a scale beyond D = 4096
 // (three).
+#include "layer_dropout.hpp"
 #include "layer_rows.hpp"
 
 namespace layer {
@@ -25,7 +28,7 @@ __device__ __forceinline__ void load_row(Raw<T, VEC> (&r)[NV], const void* p, lo
 #pragma unroll
     for (int i = 0; i < NV; i++) load_raw<TPR>(r[i], (const T*)p + off, i, lane, D);
 }
-template <class E, class R, int VEC, int TPR, int NV, bool SCALE>
+template <class E, class R, int VEC, int TPR, int NV, bool SCALE, bool DROP>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void add_norm_fwd_kernel(NormArgs a) {
     constexpr int NT = TPR > 256 ? TPR : 256, GR = NT / TPR;
     __shared__ float lds[TPR > 64 ? 2 * NT / 64 : 1];
@@ -34,22 +37,27 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void add_norm_fwd_kernel(Nor
     float w[NV][VEC], sc[SCALE ? NV : 1][VEC];
     load_weights<VEC, TPR, NV>(w, a.w, lane, D);
     if constexpr (SCALE) load_weights<VEC, TPR, NV>(sc, a.scale, lane, D);
+    const Keep keep(a.drop);
     int phase = 0;
     for (long r0 = (long)blockIdx.x * GR; r0 < a.rows; r0 += (long)gridDim.x * GR, phase ^= 1) {
         const bool live = r0 + grp < a.rows;
-        const long off = (live ? r0 + grp : a.rows - 1) * D;
+        const long row = live ? r0 + grp : a.rows - 1, off = row * D;
         Rows<E, R, VEC, NV> in;
         load_row<E, VEC, TPR, NV>(in.e, a.x, off, lane, D);
         load_row<R, VEC, TPR, NV>(in.res, a.res, off, lane, D);
         float h[NV][VEC], s[1] = {0.f};
 #pragma unroll
-        for (int i = 0; i < NV; i++)
+        for (int i = 0; i < NV; i++) {
+            uint32_t m = 0;
+            if constexpr (DROP) m = keep.mask<VEC>(row, (D + 7) / 8, (i * TPR + lane) * VEC);
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                const float v = (float)in.e[i].v[e];
+                float v = (float)in.e[i].v[e];
+                if constexpr (DROP) v = m >> e & 1 ? v * keep.mul : 0.f;
                 h[i][e] = (float)in.res[i].v[e] + (SCALE ? sc[i][e] * v : v);
                 s[0] += h[i][e] * h[i][e];
             }
+        }
         row_sum<TPR, 1, NT>(s, lds, phase);
         const float r = rsqrtf(s[0] * inv + a.eps);
         if (!live) continue;
@@ -73,7 +81,7 @@ __device__ __forceinline__ void load_rows(Rows<E, R, VEC, NV>& r, const NormArgs
     if constexpr (SCALE) load_row<E, VEC, TPR, NV>(r.x, a.x, off, lane, a.D);
 }
 
-template <class E, class R, int VEC, int TPR, int NV, bool SCALE, int BT>
+template <class E, class R, int VEC, int TPR, int NV, bool SCALE, bool DROP, int BT>
 __global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
     constexpr int GR = BT / TPR;
     __shared__ float lds[BT * VEC];
@@ -90,6 +98,7 @@ __global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
             dw[i][e] = 0.f;
             if (SCALE) ds[i][e] = 0.f;
         }
+    const Keep keep(a.drop);
     int phase = 0;
     Rows<E, R, VEC, NV> in, next;
     load_rows<E, R, VEC, TPR, NV, SCALE>(in, a, (long)blockIdx.x * GR + grp, lane);
@@ -112,16 +121,18 @@ __global__ __launch_bounds__(BT) void add_norm_bwd_kernel(NormArgs a) {
             for (int i = 0; i < NV; i++) {
                 const int c = (i * TPR + lane) * VEC;
                 float dh[VEC], dx[VEC];
+                uint32_t m01 = 0;
+                if constexpr (DROP) m01 = keep.mask<VEC>(r0 + grp, (D + 7) / 8, c);
 #pragma unroll
                 for (int e = 0; e < VEC; e++) {
                     const float n = (float)in.res[i].v[e] * r, g = (float)in.e[i].v[e];
                     dh[e] = r * (g * w[i][e] - n * m) + (a.dres ? (float)in.dres[i].v[e] : 0.f);
                     dw[i][e] += g * n;
+                    dx[e] = dh[e];
+                    if constexpr (DROP) dx[e] = m01 >> e & 1 ? dh[e] * keep.mul : 0.f;
                     if constexpr (SCALE) {
-                        ds[i][e] += dh[e] * (float)in.x[i].v[e];
-                        dx[e] = dh[e] * sc[i][e];
-                    } else {
-                        dx[e] = dh[e];
+                        ds[i][e] += DROP && !(m01 >> e & 1) ? 0.f : dx[e] * (float)in.x[i].v[e];
+                        dx[e] *= sc[i][e];
                     }
                 }
                 store_vec<R, VEC>((R*)a.dres_out + off, c, D, dh);
@@ -171,13 +182,21 @@ __global__ void zero_kernel(float* a, float* b, int n) {
     if (b) b[i] = 0.f;
 }
 
+// f(has a scale, is dropped out)
+template <class F> void by_branch(const NormArgs& a, F&& f) {
+    if (a.dropped) a.scale ? f(std::true_type{}, std::true_type{}) : f(std::false_type{}, std::true_type{});
+    else a.scale ? f(std::true_type{}, std::false_type{}) : f(std::false_type{}, std::false_type{});
+}
+
 template <class E, class R> hipError_t add_fwd(const NormArgs& a, hipStream_t s) {
     constexpr int VEC = sizeof(R) == 4 ? 4 : 8;
     return split_rows<false, false, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, NT = TPR > 256 ? TPR : 256;
         const dim3 grid(grid_rows(a.rows, NT / TPR, MAX_FWD_BLOCKS));
-        if (a.scale) hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV, true>), grid, dim3(NT), 0, s, a);
-        else hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV, false>), grid, dim3(NT), 0, s, a);
+        by_branch(a, [&](auto S, auto K) {
+            hipLaunchKernelGGL((add_norm_fwd_kernel<E, R, VEC, TPR, NV, decltype(S)::value, decltype(K)::value>), grid,
+                               dim3(NT), 0, s, a);
+        });
         return hipGetLastError();
     });
 }
@@ -189,10 +208,10 @@ template <class E, class R> hipError_t add_bwd(const NormArgs& a0, hipStream_t s
     const hipError_t e = split_rows<false, true, VEC>((a.D + VEC - 1) / VEC, [&](auto T, auto N) {
         constexpr int TPR = decltype(T)::value, NV = decltype(N)::value, BT = TPR > BWD_THREADS ? TPR : BWD_THREADS;
         blocks = bwd_blocks(a, BT / TPR, TPR * NV > 512);
-        if (a.scale)
-            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, true, BT>), dim3(blocks), dim3(BT), 0, s, a);
-        else
-            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, false, BT>), dim3(blocks), dim3(BT), 0, s, a);
+        by_branch(a, [&](auto S, auto K) {
+            hipLaunchKernelGGL((add_norm_bwd_kernel<E, R, VEC, TPR, NV, decltype(S)::value, decltype(K)::value, BT>),
+                               dim3(blocks), dim3(BT), 0, s, a);
+        });
         return hipGetLastError();
     });
     return e != hipSuccess ? e : norm_wsum(a, blocks, s);

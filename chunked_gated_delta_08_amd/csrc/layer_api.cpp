@@ -32,6 +32,51 @@ layer::NormArgs norm_args(const norm_problem* p) {
 
 size_t norm_ws(const norm_problem* p) { return 4 * layer::norm_part_floats((long)p->rows, p->D); }
 
+int check_dropout(const gdn_dropout* d, layer::Drop* out) {
+    if (!d || !(d->p >= 0.0 && d->p <= 1.0) || ((uintptr_t)d->rng & 7)) return GDR_ERR_INVALID;
+    const uint32_t t = (uint32_t)floor(d->p * 65536.0 + 0.5);
+    *out = {d->seed, d->offset, d->rng, t, t < 65536 ? (float)(65536.0 / (65536.0 - t)) : 0.f};
+    return GDR_OK;
+}
+
+// Both forms of the add norm; d NULL: no dropout.
+int add_fwd(const norm_problem* p, const gdn_dropout* d, const layer::Drop& drop, const void* x, const void* res,
+            const float* w, const float* scale, void* y, void* res_out, hipStream_t stream) {
+    int st = check_norm(p);
+    if (st != GDR_OK || (st = check_res(p)) != GDR_OK) return st;
+    if (p->rows == 0) return GDR_OK;
+    if (!x || !res || !w || !y || !res_out) return GDR_ERR_INVALID;
+    const size_t es = size_of(p->dtype), rs = size_of(p->res_dtype), c = 4 * (size_t)p->D;
+    const size_t n = (size_t)p->rows * p->D * es, m = (size_t)p->rows * p->D * rs;
+    if (!buffers_ok({{x, n, es}, {res, m, rs}, {w, c, 4}, {scale, c, 4}, {drop.rng, 16, 8}},
+                    {{{y, n, es}, 1}, {{res_out, m, rs}, 2}}))
+        return GDR_ERR_INVALID;
+    layer::NormArgs a = norm_args(p);
+    a.x = x; a.res = res; a.w = w; a.scale = scale; a.y = y; a.res_out = res_out;
+    a.dropped = d != nullptr; a.drop = drop;
+    return status(layer::launch_add_norm_fwd(a, stream));
+}
+int add_bwd(const norm_problem* p, const gdn_dropout* d, const layer::Drop& drop, const void* dy, const void* dres,
+            const void* res, const float* w, const void* x, const float* scale, void* dx, void* dres_out, float* dw,
+            float* dscale, void* ws, size_t ws_bytes, hipStream_t stream) {
+    int st = check_norm(p);
+    if (st != GDR_OK || (st = check_res(p)) != GDR_OK) return st;
+    if (!dw || !scale != !dscale) return GDR_ERR_INVALID;
+    if (p->rows > 0 && (!dy || !res || !w || !dres_out || (scale && !x) || ((scale || d) && !dx))) return GDR_ERR_INVALID;
+    const size_t es = size_of(p->dtype), rs = size_of(p->res_dtype), c = 4 * (size_t)p->D, need = norm_ws(p);
+    const size_t n = (size_t)p->rows * p->D * es, m = (size_t)p->rows * p->D * rs;
+    if ((st = check_ws(ws, ws_bytes, need)) != GDR_OK) return st;
+    if (!buffers_ok({{dy, n, es}, {x, n, es}, {dres, m, rs}, {res, m, rs}, {w, c, 4}, {scale, c, 4}, {drop.rng, 16, 8}},
+                    {{{dx, n, es}, 3}, {{dres_out, m, rs}, 12}, {{dw, c, 4}, 0}, {{dscale, c, 4}, 0},
+                     {{ws, need, 16}, 0}}))
+        return GDR_ERR_INVALID;
+    layer::NormArgs a = norm_args(p);
+    a.dy = dy; a.dres = dres; a.res = res; a.w = w; a.x = x; a.scale = scale; a.dx = dx; a.dres_out = dres_out;
+    a.dw = dw; a.dscale = dscale; a.part = (float*)ws;
+    a.dropped = d != nullptr; a.drop = drop;
+    return status(layer::launch_add_norm_bwd(a, stream));
+}
+
 int check_glr(const glr_problem* p, layer::GlrArgs* a) {
     if (!p || p->B < 1 || p->T < 0 || p->D < 1 || !known(p->dtype)) return GDR_ERR_INVALID;
     int64_t n = (int64_t)p->B * p->T, nseq = p->B;
@@ -95,37 +140,43 @@ int gated_norm_bwd(const norm_problem* p, const void* x, const void* z, const fl
 
 int add_norm_fwd(const norm_problem* p, const void* x, const void* res, const float* w, const float* scale, void* y,
                  void* res_out, hipStream_t stream) {
-    int st = check_norm(p);
-    if (st != GDR_OK || (st = check_res(p)) != GDR_OK) return st;
-    if (p->rows == 0) return GDR_OK;
-    if (!x || !res || !w || !y || !res_out) return GDR_ERR_INVALID;
-    const size_t es = size_of(p->dtype), rs = size_of(p->res_dtype), c = 4 * (size_t)p->D;
-    const size_t n = (size_t)p->rows * p->D * es, m = (size_t)p->rows * p->D * rs;
-    if (!buffers_ok({{x, n, es}, {res, m, rs}, {w, c, 4}, {scale, c, 4}}, {{{y, n, es}, 1}, {{res_out, m, rs}, 2}}))
-        return GDR_ERR_INVALID;
-    layer::NormArgs a = norm_args(p);
-    a.x = x; a.res = res; a.w = w; a.scale = scale; a.y = y; a.res_out = res_out;
-    return status(layer::launch_add_norm_fwd(a, stream));
+    return add_fwd(p, nullptr, {}, x, res, w, scale, y, res_out, stream);
 }
 
 int add_norm_bwd(const norm_problem* p, const void* dy, const void* dres, const void* res, const float* w,
                  const void* x, const float* scale, void* dx, void* dres_out, float* dw, float* dscale, void* ws,
                  size_t ws_bytes, hipStream_t stream) {
-    int st = check_norm(p);
-    if (st != GDR_OK || (st = check_res(p)) != GDR_OK) return st;
-    if (!dw || !scale != !dscale) return GDR_ERR_INVALID;
-    if (p->rows > 0 && (!dy || !res || !w || !dres_out || (scale && (!x || !dx)))) return GDR_ERR_INVALID;
-    const size_t es = size_of(p->dtype), rs = size_of(p->res_dtype), c = 4 * (size_t)p->D, need = norm_ws(p);
-    const size_t n = (size_t)p->rows * p->D * es, m = (size_t)p->rows * p->D * rs;
-    if ((st = check_ws(ws, ws_bytes, need)) != GDR_OK) return st;
-    if (!buffers_ok({{dy, n, es}, {x, n, es}, {dres, m, rs}, {res, m, rs}, {w, c, 4}, {scale, c, 4}},
-                    {{{dx, n, es}, 3}, {{dres_out, m, rs}, 12}, {{dw, c, 4}, 0}, {{dscale, c, 4}, 0},
-                     {{ws, need, 16}, 0}}))
-        return GDR_ERR_INVALID;
-    layer::NormArgs a = norm_args(p);
-    a.dy = dy; a.dres = dres; a.res = res; a.w = w; a.x = x; a.scale = scale; a.dx = dx; a.dres_out = dres_out;
-    a.dw = dw; a.dscale = dscale; a.part = (float*)ws;
-    return status(layer::launch_add_norm_bwd(a, stream));
+    return add_bwd(p, nullptr, {}, dy, dres, res, w, x, scale, dx, dres_out, dw, dscale, ws, ws_bytes, stream);
+}
+
+int gdn_dropout_fwd(int64_t rows, int64_t D, gdr_dtype dtype, const gdn_dropout* d, const void* x, void* y,
+                    hipStream_t stream) {
+    layer::Drop drop;
+    const int st = check_dropout(d, &drop);
+    if (st != GDR_OK) return st;
+    if (rows < 0 || D < 1 || !known(dtype)) return GDR_ERR_INVALID;
+    if (D > (int64_t)1 << 40 || rows > ((int64_t)1 << 40) / D) return GDR_ERR_UNSUPPORTED;
+    if (rows == 0) return GDR_OK;
+    if (!x || !y) return GDR_ERR_INVALID;
+    const size_t es = size_of(dtype), n = (size_t)rows * D * es;
+    if (!buffers_ok({{x, n, es}, {drop.rng, 16, 8}}, {{{y, n, es}, 1}})) return GDR_ERR_INVALID;
+    return status(layer::launch_dropout(dtype, x, y, rows, D, drop, stream));
+}
+
+int dropout_add_norm_fwd(const norm_problem* p, const gdn_dropout* d, const void* x, const void* res, const float* w,
+                         const float* scale, void* y, void* res_out, hipStream_t stream) {
+    layer::Drop drop;
+    const int st = check_dropout(d, &drop);
+    return st != GDR_OK ? st : add_fwd(p, d, drop, x, res, w, scale, y, res_out, stream);
+}
+
+int dropout_add_norm_bwd(const norm_problem* p, const gdn_dropout* d, const void* dy, const void* dres,
+                         const void* res, const float* w, const void* x, const float* scale, void* dx, void* dres_out,
+                         float* dw, float* dscale, void* ws, size_t ws_bytes, hipStream_t stream) {
+    layer::Drop drop;
+    const int st = check_dropout(d, &drop);
+    return st != GDR_OK ? st
+                        : add_bwd(p, d, drop, dy, dres, res, w, x, scale, dx, dres_out, dw, dscale, ws, ws_bytes, stream);
 }
 
 int64_t glr_num_states(const glr_problem* p) {

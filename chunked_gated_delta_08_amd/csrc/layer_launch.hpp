@@ -6,6 +6,15 @@
 
 namespace layer {
 
+// Dropout (gdn_dropout): the host's part of the mask.
+struct Drop {
+    uint64_t seed, offset;
+    const uint64_t* rng;   // device seed and offset, or NULL
+    uint32_t drop;         // of 65536, how many values drop an element
+    float mul;             // 65536 / (65536 - drop)
+};
+hipError_t launch_dropout(int dtype, const void* x, void* y, int64_t rows, int64_t D, const Drop& d, hipStream_t s);
+
 // Both norms.  E: dtype (gdr_dtype), R: type of the residual stream.
 struct NormArgs {
     long rows;
@@ -21,6 +30,7 @@ struct NormArgs {
     float* dw; float* dscale;
     float* part; float* part_s;   // backward: the workgroups' column sums for dw and dscale, `pitch` floats apart
     int pitch;
+    bool dropped; Drop drop;      // add norm: whether the branch x is dropped out, and how
 };
 
 // Floats of `part` that either backward may use.

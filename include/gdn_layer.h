@@ -8,6 +8,8 @@
  *   gated norm   y = x r w act(z),  r = (sum_D x^2 / D + eps)^(-1/2) per row,
  *                act(z) = z sigmoid(z), sigmoid(z), or 1 where z is absent
  *   add norm     res' = res + s x,  y = res' r w,  r of the unrounded res'
+ *   dropout      y = m x,  m = 1/(1-p) or 0 per element, from a counter-based generator;
+ *                in the add norm m x stands for x
  *   recurrence   h_t = exp(g_t) h_{t-1} + x_t   per channel, h_{-1} = h0
  *   rule's step  S <- exp(g) S;  S <- S + beta k (v - S^T k)^T;  o = scale S^T q
  *                (one token of the recurrence in gdr.h)
@@ -93,6 +95,47 @@ int add_norm_fwd(const norm_problem *p, const void *x, const void *res, const fl
 int add_norm_bwd(const norm_problem *p, const void *dy, const void *dres, const void *res, const float *w,
                  const void *x, const float *scale, void *dx, void *dres_out, float *dw, float *dscale, void *ws,
                  size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Dropout.  The mask is a function of (seed, offset, row, column) alone and is computed
+ * wherever it is needed, never stored: a forward and its backward give the same
+ * gdn_dropout, calls that shall differ another offset (or seed).
+ * Element `column` of row `row` has 16 bits b: with G = ceil(D / 8), group
+ * n = row G + column / 8 and e = column % 8, Philox 4x32-10 (Salmon et al. 2011) with
+ * key (seed low, seed high) and counter (n low, n high, offset low, offset high) gives
+ * four words, and b is half e % 2 (low half first) of word e / 2.  The element is
+ * dropped where b < t, t = floor(65536 p + 1/2), and multiplied by 65536 / (65536 - t)
+ * otherwise: the probability is p to the nearest 2^-16, and the factor is its own.
+ * A dropped element is 0 whatever x is.  t = 65536 drops all of them.
+ */
+typedef struct gdn_dropout {
+    double p;                /* 0 <= p <= 1 */
+    uint64_t seed, offset;
+    const uint64_t *rng;     /* device {seed, offset}, 8-byte aligned, read by the kernels instead of the
+                                two above (a captured graph then takes what it holds at each replay), or NULL */
+} gdn_dropout;
+
+/*
+ * gdn_dropout_fwd -- y = m x; the gradient is the same call on dy.
+ *   x, y [rows, D] dtype   y may be x
+ * rows >= 0, D >= 1, rows * D <= 2^40.
+ */
+int gdn_dropout_fwd(int64_t rows, int64_t D, gdr_dtype dtype, const gdn_dropout *d, const void *x, void *y,
+                    hipStream_t stream);
+
+/*
+ * dropout_add_norm_fwd -- res' = res + s m x and y = RMSNorm(res') w: add_norm_fwd of m x.
+ */
+int dropout_add_norm_fwd(const norm_problem *p, const gdn_dropout *d, const void *x, const void *res, const float *w,
+                         const float *scale, void *y, void *res_out, hipStream_t stream);
+
+/*
+ * dropout_add_norm_bwd -- its gradients, as add_norm_bwd's: dx = s m dres_out, dscale = sum over the rows
+ * of dres_out m x.  dx [rows, D] dtype is always written, and is dres_out's buffer in no case.
+ */
+int dropout_add_norm_bwd(const norm_problem *p, const gdn_dropout *d, const void *dy, const void *dres,
+                         const void *res, const float *w, const void *x, const float *scale, void *dx, void *dres_out,
+                         float *dw, float *dscale, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* Sizes of the gated linear recurrence.  The token axis is flattened over the
  * batch, as in gdr.h: dense B sequences of T tokens, or (cu_seqlens != NULL,
