@@ -56,10 +56,11 @@ template <class E, int NC> __device__ __forceinline__ int swz(int k) {
     return x & (NC - 1);
 }
 
-// 16 bytes of each lane from base + off to LDS at lds + 16 lane.
+// 16 bytes of each lane from base + off to LDS at lds + 16 lane.  (m0 holds nothing else here: the
+// compiler sets it anew wherever it uses it, and keeps no value in it.)
 __device__ __forceinline__ void load_to_lds(uint32_t lds, const char* base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory", "m0");
+                 :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
 template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
 
@@ -158,22 +159,23 @@ template <class E, int ROWS, int NW, bool TRANS, bool PAIR> struct Operand {
 // ----------------------------------------------------------------- epilogues
 // sigmoid_f: layer_rows.hpp.  gelu: x Phi(x), Phi by the complementary error
 // function, which keeps its digits where x is far below zero.
-__device__ __forceinline__ float act_f(float x, int act) {
-    if (act == GDN_FFN_GELU) return 0.5f * x * erfcf(-x * 0.70710678f);
+template <int ACT> __device__ __forceinline__ float act_f(float x) {
+    if constexpr (ACT == GDN_FFN_GELU) return 0.5f * x * erfcf(-x * 0.70710678f);
     const float s = layer::sigmoid_f(x);
-    return act == GDN_FFN_SILU ? x * s : s;
+    return ACT == GDN_FFN_SILU ? x * s : s;
 }
-// act(x) and its slope; 1 - sigmoid(x) is sigmoid(-x), which keeps its digits.
-__device__ __forceinline__ void act_slope(float x, int act, float& a, float& d) {
-    if (act == GDN_FFN_GELU) {
+// act(x) and its slope.  With e = exp(-x), s = sigmoid(x) = 1 / (1 + e) and 1 - s = e s,
+// which keeps its digits where s is close to 1; e stays finite.
+template <int ACT> __device__ __forceinline__ void act_slope(float x, float& a, float& d) {
+    if constexpr (ACT == GDN_FFN_GELU) {
         const float phi = 0.5f * erfcf(-x * 0.70710678f);
         a = x * phi;
         d = phi + x * 0.39894228f * expf(-0.5f * x * x);
-        return;
+    } else {
+        const float e = fminf(layer::exp_neg(x), 0x1p126f), s = __builtin_amdgcn_rcpf(1.f + e), t = e * s;
+        a = ACT == GDN_FFN_SILU ? x * s : s;
+        d = ACT == GDN_FFN_SILU ? s * (1.f + x * t) : s * t;
     }
-    const float s = layer::sigmoid_f(x), t = layer::sigmoid_f(-x);
-    a = act == GDN_FFN_SILU ? x * s : s;
-    d = act == GDN_FFN_SILU ? s * (1.f + x * t) : s * t;
 }
 
 // Four consecutive elements of a row, those of them before `end`.
@@ -190,23 +192,41 @@ template <class E> __device__ __forceinline__ void store4(E* row, int64_t n, int
             if (n + e < end) row[n + e] = (E)v[e];
     }
 }
-__device__ __forceinline__ f32x4 load4(const float* row, int n, int end) {
-    typedef typename layer::VecU<float, 4>::t V;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (n + 4 <= end) {
-        const V t = *(const V*)(row + n);
+// Gate and up of four columns as kept by the forward, zero past the last column.  VEC: F is a multiple of 4,
+// so are the columns.  Without branches, so that several stay on their way.
+struct Kept {
+    f32x4 g, u;
+    template <bool VEC> __device__ __forceinline__ void load(const GemmArgs& a, int m, int n) {
+        const float* row = a.gu + (int64_t)m * 2 * a.F;
+        if constexpr (VEC) {
+            row += n < a.F ? n : a.F - 4;
+            typedef typename layer::VecU<float, 4>::t V;
+            g = __builtin_bit_cast(f32x4, *(const V*)row), u = __builtin_bit_cast(f32x4, *(const V*)(row + a.F));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = t[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (n + e < end) v[e] = row[n + e];
+            for (int e = 0; e < 4; e++) {
+                const int c = n + e < a.F ? n + e : a.F - 1;
+                g[e] = row[c], u[e] = row[a.F + c];
+            }
+        }
     }
-    return v;
+    template <bool VEC> __device__ __forceinline__ void mask(const GemmArgs& a, int n) {
+        if constexpr (!VEC)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (n + e >= a.F) g[e] = u[e] = 0.f;
+    }
+};
+
+// Orders a wave's own accesses to LDS (they are carried out in their order).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // What becomes of four sums (n .. n+3 of row m): v of the product, w of the pair's second matrix.
-template <class E, int KIND> __device__ __forceinline__ void finish(const GemmArgs& a, int m, int n, f32x4 v, f32x4 w) {
+template <class E, int KIND, int ACT>
+__device__ __forceinline__ void finish(const GemmArgs& a, int m, int n, f32x4 v, f32x4 w, const Kept& kept) {
     if constexpr (KIND == GATE_UP) {
         if (a.gu) {   // kept in fp32: rounded to the type they would add as much error to the gradients as the operands do
             float* row = a.gu + (int64_t)m * 2 * a.F;
@@ -215,19 +235,17 @@ template <class E, int KIND> __device__ __forceinline__ void finish(const GemmAr
         }
         f32x4 h;
 #pragma unroll
-        for (int e = 0; e < 4; e++) h[e] = act_f(v[e], a.act) * w[e];
+        for (int e = 0; e < 4; e++) h[e] = act_f<ACT>(v[e]) * w[e];
         store4<E>((E*)a.h + (int64_t)m * a.N, n, a.N, h);
     } else if constexpr (KIND == DH) {
-        const float* row = a.gu + (int64_t)m * 2 * a.F;
-        const f32x4 g = load4(row, n, a.F), u = load4(row + a.F, n, a.F);
         f32x4 dg, du, h;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             float act, slope;
-            act_slope(g[e], a.act, act, slope);
-            dg[e] = v[e] * u[e] * slope;
+            act_slope<ACT>(kept.g[e], act, slope);
+            dg[e] = v[e] * kept.u[e] * slope;
             du[e] = v[e] * act;
-            h[e] = act * u[e];
+            h[e] = act * kept.u[e];
         }
         E* d = (E*)a.dgu + (int64_t)m * 2 * a.N;
         store4<E>(d, n, a.N, dg);
@@ -237,6 +255,25 @@ template <class E, int KIND> __device__ __forceinline__ void finish(const GemmAr
         const bool second = m >= a.osplit;
         if (second) m -= a.osplit;
         if (m < a.rows_out) store4<E>((E*)(second ? a.out1 : a.out0) + m * a.ldo, n, a.cols_out, v);
+    }
+}
+
+// f(act, whether F is a multiple of 4): what the epilogue's code goes by, uniform
+template <int KIND, class F> __device__ __forceinline__ void by_act(const GemmArgs& a, F&& f) {
+    using std::integral_constant;
+    if constexpr (KIND != GATE_UP && KIND != DH) {
+        f(integral_constant<int, 0>{}, std::true_type{});
+    } else {
+        const bool vec = KIND != DH || a.F % 4 == 0;
+        auto g = [&](auto act) {
+            if constexpr (KIND == DH) {
+                if (!vec) return f(act, std::false_type{});
+            }
+            f(act, std::true_type{});
+        };
+        if (a.act == GDN_FFN_SILU) g(integral_constant<int, GDN_FFN_SILU>{});
+        else if (a.act == GDN_FFN_GELU) g(integral_constant<int, GDN_FFN_GELU>{});
+        else g(integral_constant<int, GDN_FFN_SIGMOID>{});
     }
 }
 
@@ -266,7 +303,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm_kernel(GemmArgs a) {
     const int all = (a.K + KE - 1) / KE, k0 = split * a.steps, k1 = k0 + a.steps < all ? k0 + a.steps : all;
     Q q;
     P p;
-    q.init(QT ? m0 : m0, a.M, a.ldq, wave, lane);
+    q.init(m0, a.M, a.ldq, wave, lane);
     p.init(n0, a.N, a.ldp, wave, lane);
     const char* qb = (const char*)a.q + (QT ? 0 : (int64_t)m0 * a.ldq * (int64_t)sizeof(E));
     const char* pb0 = (const char*)a.p0 + (PT ? 0 : (int64_t)n0 * a.ldp * (int64_t)sizeof(E));
@@ -314,25 +351,75 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm_kernel(GemmArgs a) {
         ahead = ahead + 1 == NST ? 0 : ahead + 1;
     }
 
+    // The sums go out through LDS, up to 64 rows of a wave at a time, so that lanes side by side hold
+    // columns side by side: whole lines are written, and what the epilogue reads comes in whole lines,
+    // DEPTH passes ahead.  Quad q of a row lies at q ^ row.
+    constexpr int STEP = PAIR ? 2 : 1, COLS = 16 * TN / STEP, QUADS = 4 * TN;
+    constexpr int LPR = COLS / 4, RPP = 64 / LPR;                      // lanes of a row, rows of a pass
+    constexpr int CH = TM < 4 ? TM : 4, PC = 16 * CH / RPP, DEPTH = PC < 4 ? PC : 4;
+    static_assert(NW * 16 * CH * QUADS * 16 <= NST * STAGE && TM % CH == 0 && PC % DEPTH == 0, "fits the stages");
     const int r = lane & 15, g = lane >> 4;
-    constexpr int STEP = PAIR ? 2 : 1;
+    char* mine = smem + wave * 16 * CH * QUADS * 16;
+    const int row0 = lane / LPR, col = lane % LPR * 4, n = n0 + wn * COLS + col, m1 = m0 + wm * TM * 16 + row0;
+    auto quad = [&](int row, int q) { return (f32x4*)(mine + row * QUADS * 16 + (q ^ (row & (QUADS - 1))) * 16); };
+    auto spread = [&](auto I) {
+        constexpr int c = decltype(I)::value * CH;
 #pragma unroll
-    for (int i = 0; i < TM; i++) {
-        const int m = m0 + wm * TM * 16 + 16 * i + r;
-        if (m >= a.M) continue;
+        for (int i = 0; i < CH; i++)
 #pragma unroll
-        for (int j = 0; j < TN; j += STEP) {
-            const int n = n0 + wn * (TN / STEP) * 16 + 16 * (j / STEP) + 4 * g;
-            if (n >= a.N) continue;
-            if (a.splits > 1) {
-                float* row = a.part + ((int64_t)split * a.M + m) * STEP * a.N;
-                *(f32x4*)(row + n) = acc[j][i];
-                if constexpr (PAIR) *(f32x4*)(row + a.N + n) = acc[j + 1][i];
-            } else {
-                finish<E, KIND>(a, m, n, acc[j][i], acc[j + STEP - 1][i]);
+            for (int j = 0; j < TN; j++)
+                *quad(16 * i + r, PAIR ? j % 2 * (QUADS / 2) + j / 2 * 4 + g : j * 4 + g) = acc[j][c + i];
+        wave_sync();
+    };
+    auto chunks = [&](auto&& f) {
+        f(std::integral_constant<int, 0>{});
+        if constexpr (TM > CH) f(std::integral_constant<int, 1>{});
+        static_assert(TM <= 2 * CH, "two chunks at most");
+    };
+    if (a.splits > 1) {
+        gdr::lds_barrier();   // the stages are no longer read
+        chunks([&](auto I) {
+            spread(I);
+            for (int p = 0; p < PC; p++) {
+                const int row = p * RPP + row0, m = m1 + decltype(I)::value * CH * 16 + p * RPP;
+                const f32x4 v = *quad(row, col / 4), w = *quad(row, col / 4 + (PAIR ? QUADS / 2 : 0));
+                if (m >= a.M || n >= a.N) continue;
+                float* part = a.part + ((int64_t)split * a.M + m) * STEP * a.N + n;
+                *(f32x4*)part = v;
+                if constexpr (PAIR) *(f32x4*)(part + a.N) = w;
             }
-        }
+            wave_sync();
+        });
+        return;
     }
+    by_act<KIND>(a, [&](auto A, auto V) {
+        constexpr int ACT = decltype(A)::value;
+        constexpr bool VEC = decltype(V)::value;
+        Kept kept[DEPTH];
+        auto fetch = [&](Kept& k, int p) {
+            if constexpr (KIND == DH) {
+                const int m = m1 + p * RPP;
+                k.template load<VEC>(a, m < a.M ? m : a.M - 1, n);
+            }
+        };
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) fetch(kept[d], d);
+        gdr::lds_barrier();   // the stages are no longer read
+        chunks([&](auto I) {
+            spread(I);
+#pragma unroll 1
+            for (int p = 0; p < PC; p += DEPTH)
+#pragma unroll
+                for (int d = 0; d < DEPTH; d++) {
+                    const int at = decltype(I)::value * PC + p + d, row = (p + d) * RPP + row0, m = m1 + at * RPP;
+                    const f32x4 v = *quad(row, col / 4), w = *quad(row, col / 4 + (PAIR ? QUADS / 2 : 0));
+                    if constexpr (KIND == DH) kept[d].template mask<VEC>(a, n);
+                    if (m < a.M && n < a.N) finish<E, KIND, ACT>(a, m, n, v, w, kept[d]);
+                    fetch(kept[d], at + DEPTH);
+                }
+            wave_sync();
+        });
+    });
 }
 
 // The splits' sums in their order, and what becomes of them: four columns a lane.
@@ -348,7 +435,14 @@ template <class E, int KIND> __global__ __launch_bounds__(256) void ffn_join_ker
             v += *(const f32x4*)(p + s * plane);
             if constexpr (STEP == 2) w += *(const f32x4*)(p + s * plane + a.N);
         }
-        finish<E, KIND>(a, m, n, v, w);
+        by_act<KIND>(a, [&](auto A, auto V) {
+            Kept kept;
+            if constexpr (KIND == DH) {
+                kept.template load<decltype(V)::value>(a, m, n);
+                kept.template mask<decltype(V)::value>(a, n);
+            }
+            finish<E, KIND, decltype(A)::value>(a, m, n, v, w, kept);
+        });
     }
 }
 

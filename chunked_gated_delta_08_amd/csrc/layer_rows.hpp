@@ -122,13 +122,16 @@ __device__ __forceinline__ void store_vec(E* row, int c, int D, const float (&x)
     }
 }
 
+// exp(-z) with its one rounding of the exponent (see sigmoid_f).
+__device__ __forceinline__ float exp_neg(float z) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(-z, 0x1.715476p+0f, -z * 0x1.4ae0cp-26f));
+}
 // sigmoid in fp32, off by at most (|z| + 5) 2^-24 of itself: the exponent's one
 // rounding, |z| 2^-24 (log2(e) in two parts: its one-part rounding adds 0.22 |z|),
 // one unit in the last place, 2 2^-24, each for exp2 and rcp, and the sum's
 // rounding; zero below 2^-126.
 __device__ __forceinline__ float sigmoid_f(float z) {
-    const float t = __builtin_fmaf(-z, 0x1.715476p+0f, -z * 0x1.4ae0cp-26f);
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t));
+    return __builtin_amdgcn_rcpf(1.f + exp_neg(z));
 }
 
 // Sum over the TPR lanes of a row; for TPR above 64 over the group's waves
