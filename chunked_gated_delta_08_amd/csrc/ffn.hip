@@ -5,26 +5,59 @@
 
 namespace ffn {
 
+namespace {
+// Of each tile: its sizes, how many workgroups a CU holds, and the time of a step where one of them has
+// the CU, where as many as it holds share it (all of them), and of the rest of a tile; us, for 16-bit types and fp32,
+// from runs of all five products at 128 to 16384 tokens.
+struct Tile {
+    int bm, bn, held;
+    float one[2], all[2], rest;
+};
+constexpr Tile TILE[] = {
+    {256, 256, 1, {1.65f, 7.6f}, {1.65f, 7.6f}, 6.f},
+    {128, 128, 2, {0.55f, 2.2f}, {0.98f, 3.8f}, 3.f},
+    {128, 128, 1, {0.47f, 2.1f}, {0.47f, 2.1f}, 3.f},
+    {64, 128, 2, {0.35f, 1.1f}, {0.59f, 1.95f}, 2.f},
+    {64, 64, 2, {0.22f, 0.65f}, {0.37f, 1.0f}, 1.5f},
+};
+constexpr int CUS = 256;
+}  // namespace
+
+// The tile and the splits of least estimated time: each CU takes its share of the workgroups, as
+// many at once as it holds; splits add the sums' way through memory.  Up to 64 rows of a product with
+// weights stored [n][k] (GATE_UP, DOWN) the weights' bytes are what counts: one workgroup a CU reads them
+// fastest (17 x 2048 x 8192 bf16, us: gate and up 256 workgroups 12.8, 512 15.1; 61 x 4096 x 12288 gate and up 192
+// tiles of 64 x 128 42.5, 384 of 64 x 64 47.2; down 64 tiles in 4 splits 25.2, in 8 27.3, whole 61.2).
 Shape shape_of(Kind kind, int M, int N, int K, int esize) {
-    static const int bm[] = {256, 128, 64, 32}, bn[] = {256, 128, 64, 64};
-    const int ke = 128 / esize, all = (K + ke - 1) / ke;
-    auto tiles = [&](int c) {
-        const int bt = kind == GATE_UP ? bn[c] / 2 : bn[c];
-        return (int64_t)((M + bm[c] - 1) / bm[c]) * ((N + bt - 1) / bt);
+    const int ke = 128 / esize, all = (K + ke - 1) / ke, wide = esize == 4;
+    auto shape = [&](int c, int bm, int bn, int want) {
+        const int bt = kind == GATE_UP ? bn / 2 : bn;
+        Shape s{c, 1, 0, (M + bm - 1) / bm, (N + bt - 1) / bt};
+        s.steps = (all + want - 1) / want;
+        if (s.steps) s.splits = (all + s.steps - 1) / s.steps;
+        return s;
     };
-    int c = M <= 32 ? 3 : M <= 64 ? 2 : tiles(0) >= 192 ? 0 : 1;
-    if (c == 1 && tiles(1) < 128) c = 2;
-    Shape s{};
-    s.cfg = c, s.bm = bm[c], s.bn = bn[c];
-    const int bt = kind == GATE_UP ? s.bn / 2 : s.bn;
-    s.tilesM = (M + s.bm - 1) / s.bm, s.tilesN = (N + bt - 1) / bt;
-    int64_t want = c == 0 ? 1 : 512 / tiles(c);
-    if (want > all / 4) want = all / 4;
-    if (want > 16) want = 16;
-    if (want < 1) want = 1;
-    s.steps = (int)((all + want - 1) / want);
-    s.splits = s.steps ? (all + s.steps - 1) / s.steps : 1;
-    return s;
+    if (M <= 64 && (kind == GATE_UP || kind == DOWN)) {
+        const int small = (N + 63) / 64 * (kind == GATE_UP ? 2 : 1), c = M <= 32 ? THIN : small <= CUS ? SMALL : LOW;
+        int want = CUS / small;
+        if (want > all / 4) want = all / 4;
+        return shape(c, c == THIN ? 32 : 64, c == LOW ? 128 : 64, want < 1 ? 1 : want);
+    }
+    Shape best{};
+    float least = 0.f;
+    for (int c = 0; c < THIN; c++)
+        for (int want = 1; want <= 16; want++) {
+            const Tile& t = TILE[c];
+            const Shape s = shape(c, t.bm, t.bn, want);
+            const int64_t tiles = (int64_t)s.tilesM * s.tilesN;
+            if (want > 1 && (all < 4 * want || tiles * (want - 1) >= 2 * CUS)) break;
+            if (want > 1 && s.splits != want) continue;
+            const int64_t each = (tiles * s.splits + CUS - 1) / CUS, full = each / t.held, odd = each % t.held;
+            float us = full * (s.steps * t.all[wide] + t.rest) + odd * (s.steps * t.one[wide] + t.rest);
+            if (s.splits > 1) us += 4.f + 2e-6f * s.splits * M * N * (kind == GATE_UP ? 2 : 1);   // 8 bytes each at 4 TB/s
+            if (best.tilesM == 0 || us < least) least = us, best = s;
+        }
+    return best;
 }
 
 size_t part_floats(Kind kind, int M, int N, int K, int esize) {
@@ -44,13 +77,28 @@ hipError_t launch_gemm(int dtype, Kind kind, GemmArgs a, hipStream_t s) {
 }
 
 namespace {
+// A lane writes 16 bytes of a padded row.
 template <class U> __global__ __launch_bounds__(256) void ffn_pad_kernel(PadArgs a) {
+    constexpr int V = 16 / sizeof(U);
+    typedef U Vec __attribute__((ext_vector_type(V)));
+    typedef U Loose __attribute__((ext_vector_type(V), aligned(sizeof(U))));
     const PadItem& it = a.item[blockIdx.y];
-    const int64_t total = it.rows_dst * it.cols_dst;
+    const int per = it.cols_dst / V;
+    const int64_t total = it.rows_dst * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / it.cols_dst;
-        const int c = (int)(i - r * it.cols_dst);
-        ((U*)it.dst)[i] = r < it.rows && c < it.cols ? ((const U*)it.src)[r * it.cols + c] : (U)0;
+        const int64_t r = total >> 32 ? i / per : (int64_t)((uint32_t)i / (uint32_t)per);
+        const int c = (int)(i - r * per) * V;
+        const U* src = (const U*)it.src + r * it.cols + c;
+        Vec v;
+        if (r < it.rows && c + V <= it.cols) {
+            const Loose t = *(const Loose*)src;
+#pragma unroll
+            for (int e = 0; e < V; e++) v[e] = t[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e++) v[e] = r < it.rows && c + e < it.cols ? src[e] : (U)0;
+        }
+        ((Vec*)it.dst)[i] = v;
     }
 }
 }  // namespace
@@ -58,7 +106,7 @@ template <class U> __global__ __launch_bounds__(256) void ffn_pad_kernel(PadArgs
 hipError_t launch_pad(int esize, const PadArgs& a, hipStream_t s) {
     int64_t most = 1;
     for (int i = 0; i < a.n; i++) {
-        const int64_t n = (a.item[i].rows_dst * a.item[i].cols_dst + 1023) / 1024;
+        const int64_t n = (a.item[i].rows_dst * a.item[i].cols_dst * esize / 16 + 255) / 256;
         if (n > most) most = n;
     }
     const dim3 grid((unsigned)(most < 4096 ? most : 4096), a.n);

@@ -478,9 +478,20 @@ template <class E, int KIND> __global__ __launch_bounds__(256) void ffn_join_ker
         const int m = (int)(id / quads), n = 4 * (int)(id % quads);
         const float* p = a.part + (int64_t)m * STEP * a.N + n;
         f32x4 v = *(const f32x4*)p, w = *(const f32x4*)(p + (STEP - 1) * a.N);
-        for (int s = 1; s < a.splits; s++) {
-            v += *(const f32x4*)(p + s * plane);
-            if constexpr (STEP == 2) w += *(const f32x4*)(p + s * plane + a.N);
+        for (int s = 1; s < a.splits; s += 4) {   // four on their way at a time
+            f32x4 x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float* at = p + (s + i < a.splits ? s + i : 0) * plane;
+                x[i] = *(const f32x4*)at;
+                if constexpr (STEP == 2) y[i] = *(const f32x4*)(at + a.N);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (s + i >= a.splits) break;
+                v += x[i];
+                if constexpr (STEP == 2) w += y[i];
+            }
         }
         by_act<KIND>(a, [&](auto A, auto V) {
             Kept kept;
@@ -506,9 +517,11 @@ hipError_t run_shape(const GemmArgs& a, hipStream_t s) {
 
 template <class E, int KIND> hipError_t run_kind(const GemmArgs& a, int cfg, hipStream_t s) {
     switch (cfg) {
-        case 0: return run_shape<E, KIND, 256, 256, 2, 4, 2>(a, s);
-        case 1: return run_shape<E, KIND, 128, 128, 2, 2, 2>(a, s);
-        case 2: return run_shape<E, KIND, 64, 64, 2, 2, 4>(a, s);
+        case BIG: return run_shape<E, KIND, 256, 256, 2, 4, 2>(a, s);
+        case MIDDLE: return run_shape<E, KIND, 128, 128, 2, 4, 2>(a, s);
+        case DEEP: return run_shape<E, KIND, 128, 128, 2, 4, 4>(a, s);
+        case LOW: return run_shape<E, KIND, 64, 128, 2, 4, 3>(a, s);
+        case SMALL: return run_shape<E, KIND, 64, 64, 2, 2, 4>(a, s);
         default: return run_shape<E, KIND, 32, 64, 2, 2, 6>(a, s);
     }
 }

@@ -38,8 +38,9 @@ struct PadArgs {
 };
 
 // Tile shape and number of splits along k of a product.
+enum Config { BIG, MIDDLE, DEEP, LOW, SMALL, THIN, TILES };
 struct Shape {
-    int cfg, bm, bn, splits, steps, tilesM, tilesN;
+    int cfg, splits, steps, tilesM, tilesN;
 };
 Shape shape_of(Kind kind, int M, int N, int K, int esize);
 size_t part_floats(Kind kind, int M, int N, int K, int esize);
