@@ -1005,10 +1005,12 @@ class FfnProblem(ctypes.Structure):
 
 
 FFN_ACTS = {"silu": 0, "sigmoid": 1, "gelu": 2}
-EXPORTED_FFN = ["ffn_workspace_size", "gated_ffn_fwd", "gated_ffn_bwd"]
+EXPORTED_FFN = ["ffn_workspace_size", "ffn_saved_width", "gated_ffn_fwd", "gated_ffn_bwd"]
 _fp = ctypes.POINTER(FfnProblem)
 lib.ffn_workspace_size.restype = _sz
 lib.ffn_workspace_size.argtypes = [_fp, _i]
+lib.ffn_saved_width.restype = _i64
+lib.ffn_saved_width.argtypes = [_fp]
 lib.gated_ffn_fwd.argtypes = [_fp] + [_vp] * 7 + [_sz, _vp]
 lib.gated_ffn_bwd.argtypes = [_fp] + [_vp] * 11 + [_sz, _vp]
 
@@ -1025,9 +1027,15 @@ def ffn_workspace_size(T, D, F, dtype, bwd=False):
     return _ffn_sizes(T, D, F, dtype, "silu")[1][bool(bwd)]
 
 
+def ffn_saved_width(F, dtype):
+    """Floats that gated_ffn_fwd saves for a token: 2F, F rounded up to 16 bytes of the type."""
+    piece = 8 if dtype != torch.float32 else 4
+    return 2 * (-(-F // piece) * piece)
+
+
 def check_gated_ffn_args(x, w_gate, w_up, w_down, act="silu", saved=None, dy=None, bwd=False, cuda=True):
-    """x, dy [..., D]; w_gate, w_up [F, D]; w_down [D, F], all of one dtype; saved [T, 2F] fp32,
-    T the rows of x.  Returns T, D, F."""
+    """x, dy [..., D]; w_gate, w_up [F, D]; w_down [D, F], all of one dtype; saved
+    [T, ffn_saved_width(F, dtype)] fp32, T the rows of x.  Returns T, D, F."""
     _need(x, "x", cuda=cuda)
     if x.dtype not in _DT:
         raise TypeError(f"x has dtype {x.dtype}; expected one of {_FLOATS}")
@@ -1044,7 +1052,7 @@ def check_gated_ffn_args(x, w_gate, w_up, w_down, act="silu", saved=None, dy=Non
     _need(w_up, "w_up", x.dtype, (F, D), cuda=cuda)
     _need(w_down, "w_down", x.dtype, (D, F), cuda=cuda)
     if bwd:
-        _need(saved, "saved", torch.float32, (T, 2 * F), cuda=cuda)
+        _need(saved, "saved", torch.float32, (T, ffn_saved_width(F, x.dtype)), cuda=cuda)
         _need(dy, "dy", x.dtype, x.shape, cuda=cuda)
     _same_device(x, w_gate, w_up, w_down, saved, dy)
     piece = 16 // x.element_size()
@@ -1057,17 +1065,17 @@ def check_gated_ffn_args(x, w_gate, w_up, w_down, act="silu", saved=None, dy=Non
 
 def gated_ffn_fwd(x, w_gate, w_up, w_down, act="silu", want_saved=False, out=None, workspace=None, stream=None):
     """y = (act(x w_gate^T) * (x w_up^T)) w_down^T over the last axis; act is "silu", "gelu"
-    (exact) or "sigmoid".  Returns dict y, saved (fp32 [T, 2F], what gated_ffn_bwd
-    needs, when wanted)."""
+    (exact) or "sigmoid".  Returns dict y, saved (fp32 [T, ffn_saved_width], what
+    gated_ffn_bwd needs, when wanted)."""
     T, D, F = check_gated_ffn_args(x, w_gate, w_up, w_down, act)
     own = []
     if out is None:
         out = {"y": torch.empty_like(x),
-               "saved": x.new_empty((T, 2 * F), dtype=torch.float32) if want_saved else None}
+               "saved": x.new_empty((T, ffn_saved_width(F, x.dtype)), dtype=torch.float32) if want_saved else None}
         own += out.values()
     else:
         _need(out.get("y"), "y", x.dtype, x.shape)
-        _need(out.get("saved"), "saved", torch.float32, (T, 2 * F), optional=True)
+        _need(out.get("saved"), "saved", torch.float32, (T, ffn_saved_width(F, x.dtype)), optional=True)
         _same_device(x, *out.values())
     p, sizes = _ffn_sizes(T, D, F, x.dtype, act)
     ws, size, mine = _workspace(workspace, sizes[0], x)

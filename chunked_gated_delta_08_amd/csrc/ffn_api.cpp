@@ -73,6 +73,8 @@ extern "C" {
 
 size_t ffn_workspace_size(const ffn_problem* p, int bwd) { return check(p) != GDR_OK ? 0 : plan_of(p, bwd != 0).bytes; }
 
+int64_t ffn_saved_width(const ffn_problem* p) { return check(p) != GDR_OK ? -1 : 2 * (int64_t)plan_of(p, false).F; }
+
 int gated_ffn_fwd(const ffn_problem* p, const void* x, const void* w_gate, const void* w_up, const void* w_down,
                   void* y, float* saved, void* ws, size_t ws_bytes, hipStream_t stream) {
     int st = check(p);
@@ -83,7 +85,7 @@ int gated_ffn_fwd(const ffn_problem* p, const void* x, const void* w_gate, const
     if ((st = check_ws(ws, ws_bytes, l.bytes)) != GDR_OK) return st;
     const size_t es = l.e, in = l.pad ? es : 16, n = (size_t)l.T * p->D * es, w = (size_t)p->D * p->F * es;
     if (!buffers_ok({{x, n, in}, {w_gate, w, in}, {w_up, w, in}, {w_down, w, in}},
-                    {{{y, n, es}, 0}, {{saved, (size_t)l.T * p->F * 8, 4}, 0}, {{ws, l.bytes, 16}, 0}}))
+                    {{{y, n, es}, 0}, {{saved, (size_t)l.T * l.F * 8, 16}, 0}, {{ws, l.bytes, 16}, 0}}))
         return GDR_ERR_INVALID;
     char* b = (char*)ws;
     hipError_t e = hipSuccess;
@@ -100,7 +102,7 @@ int gated_ffn_fwd(const ffn_problem* p, const void* x, const void* w_gate, const
     a.act = p->act, a.part = (float*)(b + l.part);
     a.q = x, a.ldq = l.D, a.p0 = w_gate, a.p1 = w_up, a.ldp = l.D;
     a.M = l.T, a.N = l.F, a.K = l.D;
-    a.gu = saved, a.F = p->F, a.h = b + l.h;
+    a.gu = saved, a.h = b + l.h;
     if ((e = launch_gemm(p->dtype, GATE_UP, a, stream)) != hipSuccess) return status(e);
     a.q = b + l.h, a.ldq = l.F, a.p0 = w_down, a.p1 = nullptr, a.ldp = l.F;
     a.N = l.D, a.K = l.F;
@@ -119,7 +121,7 @@ int gated_ffn_bwd(const ffn_problem* p, const void* x, const void* w_gate, const
     if ((st = check_ws(ws, ws_bytes, l.bytes)) != GDR_OK) return st;
     const size_t es = l.e, in = l.pad ? es : 16, n = (size_t)l.T * p->D * es, w = (size_t)p->D * p->F * es;
     if (!buffers_ok({{x, n, in}, {w_gate, w, in}, {w_up, w, in}, {w_down, w, in},
-                     {saved, (size_t)l.T * p->F * 8, 4}, {dy, n, in}},
+                     {saved, (size_t)l.T * l.F * 8, 16}, {dy, n, in}},
                     {{{dx, n, es}, 0}, {{dw_gate, w, es}, 0}, {{dw_up, w, es}, 0}, {{dw_down, w, es}, 0},
                      {{ws, l.bytes, 16}, 0}}))
         return GDR_ERR_INVALID;
@@ -137,7 +139,7 @@ int gated_ffn_bwd(const ffn_problem* p, const void* x, const void* w_gate, const
         x = b + l.x, dy = b + l.dy, w_gate = b + l.wg, w_up = b + l.wu, w_down = b + l.wd;
     }
     GemmArgs a{};
-    a.act = p->act, a.part = (float*)(b + l.part), a.F = p->F, a.h = b + l.h, a.dgu = b + l.dgu, a.gu = (float*)saved;
+    a.act = p->act, a.part = (float*)(b + l.part), a.h = b + l.h, a.dgu = b + l.dgu, a.gu = (float*)saved;
     a.q = dy, a.ldq = l.D, a.p0 = w_down, a.ldp = l.F;
     a.M = l.T, a.N = l.F, a.K = l.D;
     if ((e = launch_gemm(p->dtype, DH, a, stream)) != hipSuccess) return status(e);

@@ -194,29 +194,12 @@ template <class E> __device__ __forceinline__ void store4(E* row, int64_t n, int
             if (n + e < end) row[n + e] = (E)v[e];
     }
 }
-// Gate and up of four columns as kept by the forward, zero past the last column.  VEC: F is a multiple of 4,
-// so are the columns.  Without branches, so that several stay on their way.
+// Gate and up of four columns as kept by the forward.  Without branches, so that several stay on their way.
 struct Kept {
     f32x4 g, u;
-    template <bool VEC> __device__ __forceinline__ void load(const GemmArgs& a, int m, int n) {
-        const float* row = a.gu + (int64_t)m * 2 * a.F;
-        if constexpr (VEC) {
-            row += n < a.F ? n : a.F - 4;
-            typedef typename layer::VecU<float, 4>::t V;
-            g = __builtin_bit_cast(f32x4, *(const V*)row), u = __builtin_bit_cast(f32x4, *(const V*)(row + a.F));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int c = n + e < a.F ? n + e : a.F - 1;
-                g[e] = row[c], u[e] = row[a.F + c];
-            }
-        }
-    }
-    template <bool VEC> __device__ __forceinline__ void mask(const GemmArgs& a, int n) {
-        if constexpr (!VEC)
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (n + e >= a.F) g[e] = u[e] = 0.f;
+    __device__ __forceinline__ void load(const GemmArgs& a, int m, int n) {
+        const float* row = a.gu + (int64_t)m * 2 * a.N + (n < a.N ? n : 0);
+        g = *(const f32x4*)row, u = *(const f32x4*)(row + a.N);
     }
 };
 
@@ -231,9 +214,8 @@ template <class E, int KIND, int ACT>
 __device__ __forceinline__ void finish(const GemmArgs& a, int m, int n, f32x4 v, f32x4 w, const Kept& kept) {
     if constexpr (KIND == GATE_UP) {
         if (a.gu) {   // kept in fp32: rounded to the type they would add as much error to the gradients as the operands do
-            float* row = a.gu + (int64_t)m * 2 * a.F;
-            store4<float>(row, n, a.F, v);
-            store4<float>(row + a.F, n, a.F, w);
+            float* row = a.gu + (int64_t)m * 2 * a.N + n;
+            *(f32x4*)row = v, *(f32x4*)(row + a.N) = w;
         }
         f32x4 h;
 #pragma unroll
@@ -260,23 +242,13 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int m, int n, f32x4 v,
     }
 }
 
-// f(act, whether F is a multiple of 4): what the epilogue's code goes by, uniform
+// f(act): what the epilogue's code goes by, uniform
 template <int KIND, class F> __device__ __forceinline__ void by_act(const GemmArgs& a, F&& f) {
     using std::integral_constant;
-    if constexpr (KIND != GATE_UP && KIND != DH) {
-        f(integral_constant<int, 0>{}, std::true_type{});
-    } else {
-        const bool vec = KIND != DH || a.F % 4 == 0;
-        auto g = [&](auto act) {
-            if constexpr (KIND == DH) {
-                if (!vec) return f(act, std::false_type{});
-            }
-            f(act, std::true_type{});
-        };
-        if (a.act == GDN_FFN_SILU) g(integral_constant<int, GDN_FFN_SILU>{});
-        else if (a.act == GDN_FFN_GELU) g(integral_constant<int, GDN_FFN_GELU>{});
-        else g(integral_constant<int, GDN_FFN_SIGMOID>{});
-    }
+    if constexpr (KIND != GATE_UP && KIND != DH) f(integral_constant<int, 0>{});
+    else if (a.act == GDN_FFN_SILU) f(integral_constant<int, GDN_FFN_SILU>{});
+    else if (a.act == GDN_FFN_GELU) f(integral_constant<int, GDN_FFN_GELU>{});
+    else f(integral_constant<int, GDN_FFN_SIGMOID>{});
 }
 
 template <class E, int KIND, int BM, int BN, int WM, int WN, int NST>
@@ -439,14 +411,13 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm_kernel(GemmArgs a) {
         });
         return;
     }
-    by_act<KIND>(a, [&](auto A, auto V) {
+    by_act<KIND>(a, [&](auto A) {
         constexpr int ACT = decltype(A)::value;
-        constexpr bool VEC = decltype(V)::value;
         Kept kept[DEPTH];
         auto fetch = [&](Kept& k, int p) {
             if constexpr (KIND == DH) {
                 const int m = m1 + p * RPP;
-                k.template load<VEC>(a, m < a.M ? m : a.M - 1, n);
+                k.load(a, m < a.M ? m : a.M - 1, n);
             }
         };
 #pragma unroll
@@ -460,7 +431,6 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm_kernel(GemmArgs a) {
                 for (int d = 0; d < DEPTH; d++) {
                     const int at = decltype(I)::value * PC + p + d, row = (p + d) * RPP + row0, m = m1 + at * RPP;
                     const f32x4 v = *quad(row, col / 4), w = *quad(row, col / 4 + (PAIR ? QUADS / 2 : 0));
-                    if constexpr (KIND == DH) kept[d].template mask<VEC>(a, n);
                     if (m < a.M && n < a.N) finish<E, KIND, ACT>(a, m, n, v, w, kept[d]);
                     fetch(kept[d], at + DEPTH);
                 }
@@ -493,12 +463,9 @@ template <class E, int KIND> __global__ __launch_bounds__(256) void ffn_join_ker
                 if constexpr (STEP == 2) w += y[i];
             }
         }
-        by_act<KIND>(a, [&](auto A, auto V) {
+        by_act<KIND>(a, [&](auto A) {
             Kept kept;
-            if constexpr (KIND == DH) {
-                kept.template load<decltype(V)::value>(a, m, n);
-                kept.template mask<decltype(V)::value>(a, n);
-            }
+            if constexpr (KIND == DH) kept.load(a, m, n);
             finish<E, KIND, decltype(A)::value>(a, m, n, v, w, kept);
         });
     }

@@ -19,7 +19,7 @@ struct GemmArgs {
     // epilogue
     void* out0; void* out1; int64_t ldo;            // plain: rows from osplit on are out1's
     int osplit, rows_out, cols_out;                 // rows of each that exist, columns that exist
-    float* gu; int F;                               // gate and up before the activation, [M][2 F], F columns exist
+    float* gu;                                      // gate and up before the activation, [M][2 N]
     void* h; void* dgu;                             // [M][N], [M][2 N]
     int act;
 };
