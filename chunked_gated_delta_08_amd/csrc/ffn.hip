@@ -18,7 +18,7 @@ constexpr Tile TILE[] = {
     {128, 128, 2, {0.55f, 2.2f}, {0.98f, 3.8f}, 3.f},
     {128, 128, 1, {0.47f, 2.1f}, {0.47f, 2.1f}, 3.f},
     {64, 128, 2, {0.35f, 1.1f}, {0.59f, 1.95f}, 2.f},
-    {64, 64, 2, {0.22f, 0.65f}, {0.37f, 1.0f}, 1.5f},
+    {64, 64, 2, {0.22f, 0.65f}, {0.37f, 1.08f}, 1.5f},
 };
 constexpr int CUS = 256;
 }  // namespace
