@@ -255,6 +255,6 @@ def gated_ffn(x, w_gate, w_up, w_down, act="silu"):
     x's dtype.  act is "silu", "gelu" (exact) or "sigmoid".
 
     Differentiable in x and the weights; the gradients are in x's dtype.  Between the passes it keeps
-    2F floats a token, its gate and up rows."""
+    2F floats and F of the type a token, its gate and up rows and their product."""
     t = _contiguous(x, w_gate, w_up, w_down)
     return GatedFFN.apply(*t, act, torch.is_grad_enabled() and any(v.requires_grad for v in t))

@@ -1028,9 +1028,11 @@ def ffn_workspace_size(T, D, F, dtype, bwd=False):
 
 
 def ffn_saved_width(F, dtype):
-    """Floats that gated_ffn_fwd saves for a token: 2F, F rounded up to 16 bytes of the type."""
+    """Floats that gated_ffn_fwd saves for a token: gate and up in fp32 and their product in the
+    type, F rounded up to 16 bytes of the type."""
     piece = 8 if dtype != torch.float32 else 4
-    return 2 * (-(-F // piece) * piece)
+    F = -(-F // piece) * piece
+    return 2 * F + (F if piece == 4 else F // 2)
 
 
 def check_gated_ffn_args(x, w_gate, w_up, w_down, act="silu", saved=None, dy=None, bwd=False, cuda=True):

@@ -15,6 +15,7 @@ struct Tile {
 };
 constexpr Tile TILE[] = {
     {256, 256, 1, {1.65f, 7.6f}, {1.65f, 7.6f}, 6.f},
+    {256, 128, 1, {0.93f, 4.0f}, {0.93f, 4.0f}, 4.5f},
     {128, 128, 2, {0.55f, 2.2f}, {0.98f, 3.8f}, 3.f},
     {128, 128, 1, {0.47f, 2.1f}, {0.47f, 2.1f}, 3.f},
     {64, 128, 2, {0.35f, 1.1f}, {0.59f, 1.95f}, 2.f},

@@ -38,7 +38,6 @@ Plan plan_of(const ffn_problem* p, bool bwd) {
         return o;
     };
     const size_t row = (size_t)l.T * l.F * l.e, xs = (size_t)l.T * l.D * l.e, ws = (size_t)l.D * l.F * l.e;
-    l.h = take(row);
     size_t f = 0;
     auto most = [&](Kind k, int M, int N, int K) {
         const size_t n = part_floats(k, M, N, K, l.e);
@@ -51,6 +50,7 @@ Plan plan_of(const ffn_problem* p, bool bwd) {
         most(DW, l.D, l.F, l.T);
         most(DW, 2 * l.F, l.D, l.T);
     } else {
+        l.h = take(row);   // not used by a call that keeps it
         most(GATE_UP, l.T, l.F, l.D);
         most(DOWN, l.T, l.D, l.F);
     }
@@ -63,6 +63,11 @@ Plan plan_of(const ffn_problem* p, bool bwd) {
     return l;
 }
 
+// Kept for the backward: gate and up [T][2 F] fp32, behind them h [T][F].
+int64_t saved_width(const Plan& l) { return 2 * (int64_t)l.F + (int64_t)l.F * l.e / 4; }
+size_t saved_bytes(const Plan& l) { return 4 * (size_t)l.T * saved_width(l); }
+char* saved_h(const Plan& l, const float* saved) { return (char*)saved + 8 * (size_t)l.T * l.F; }
+
 void add(PadArgs& a, const void* src, void* dst, int64_t rows, int64_t rows_dst, int cols, int cols_dst) {
     a.item[a.n++] = {src, dst, rows, rows_dst, cols, cols_dst};
 }
@@ -73,7 +78,7 @@ extern "C" {
 
 size_t ffn_workspace_size(const ffn_problem* p, int bwd) { return check(p) != GDR_OK ? 0 : plan_of(p, bwd != 0).bytes; }
 
-int64_t ffn_saved_width(const ffn_problem* p) { return check(p) != GDR_OK ? -1 : 2 * (int64_t)plan_of(p, false).F; }
+int64_t ffn_saved_width(const ffn_problem* p) { return check(p) != GDR_OK ? -1 : saved_width(plan_of(p, false)); }
 
 int gated_ffn_fwd(const ffn_problem* p, const void* x, const void* w_gate, const void* w_up, const void* w_down,
                   void* y, float* saved, void* ws, size_t ws_bytes, hipStream_t stream) {
@@ -85,7 +90,7 @@ int gated_ffn_fwd(const ffn_problem* p, const void* x, const void* w_gate, const
     if ((st = check_ws(ws, ws_bytes, l.bytes)) != GDR_OK) return st;
     const size_t es = l.e, in = l.pad ? es : 16, n = (size_t)l.T * p->D * es, w = (size_t)p->D * p->F * es;
     if (!buffers_ok({{x, n, in}, {w_gate, w, in}, {w_up, w, in}, {w_down, w, in}},
-                    {{{y, n, es}, 0}, {{saved, (size_t)l.T * l.F * 8, 16}, 0}, {{ws, l.bytes, 16}, 0}}))
+                    {{{y, n, es}, 0}, {{saved, saved_bytes(l), 16}, 0}, {{ws, l.bytes, 16}, 0}}))
         return GDR_ERR_INVALID;
     char* b = (char*)ws;
     hipError_t e = hipSuccess;
@@ -102,9 +107,9 @@ int gated_ffn_fwd(const ffn_problem* p, const void* x, const void* w_gate, const
     a.act = p->act, a.part = (float*)(b + l.part);
     a.q = x, a.ldq = l.D, a.p0 = w_gate, a.p1 = w_up, a.ldp = l.D;
     a.M = l.T, a.N = l.F, a.K = l.D;
-    a.gu = saved, a.h = b + l.h;
+    a.gu = saved, a.h = saved ? saved_h(l, saved) : b + l.h;
     if ((e = launch_gemm(p->dtype, GATE_UP, a, stream)) != hipSuccess) return status(e);
-    a.q = b + l.h, a.ldq = l.F, a.p0 = w_down, a.p1 = nullptr, a.ldp = l.F;
+    a.q = a.h, a.ldq = l.F, a.p0 = w_down, a.p1 = nullptr, a.ldp = l.F;
     a.N = l.D, a.K = l.F;
     a.out0 = y, a.ldo = p->D, a.osplit = INT_MAX, a.rows_out = l.T, a.cols_out = p->D;
     return status(launch_gemm(p->dtype, DOWN, a, stream));
@@ -121,7 +126,7 @@ int gated_ffn_bwd(const ffn_problem* p, const void* x, const void* w_gate, const
     if ((st = check_ws(ws, ws_bytes, l.bytes)) != GDR_OK) return st;
     const size_t es = l.e, in = l.pad ? es : 16, n = (size_t)l.T * p->D * es, w = (size_t)p->D * p->F * es;
     if (!buffers_ok({{x, n, in}, {w_gate, w, in}, {w_up, w, in}, {w_down, w, in},
-                     {saved, (size_t)l.T * l.F * 8, 16}, {dy, n, in}},
+                     {saved, saved_bytes(l), 16}, {dy, n, in}},
                     {{{dx, n, es}, 0}, {{dw_gate, w, es}, 0}, {{dw_up, w, es}, 0}, {{dw_down, w, es}, 0},
                      {{ws, l.bytes, 16}, 0}}))
         return GDR_ERR_INVALID;
@@ -139,7 +144,7 @@ int gated_ffn_bwd(const ffn_problem* p, const void* x, const void* w_gate, const
         x = b + l.x, dy = b + l.dy, w_gate = b + l.wg, w_up = b + l.wu, w_down = b + l.wd;
     }
     GemmArgs a{};
-    a.act = p->act, a.part = (float*)(b + l.part), a.h = b + l.h, a.dgu = b + l.dgu, a.gu = (float*)saved;
+    a.act = p->act, a.part = (float*)(b + l.part), a.dgu = b + l.dgu, a.gu = (float*)saved;
     a.q = dy, a.ldq = l.D, a.p0 = w_down, a.ldp = l.F;
     a.M = l.T, a.N = l.F, a.K = l.D;
     if ((e = launch_gemm(p->dtype, DH, a, stream)) != hipSuccess) return status(e);
@@ -158,7 +163,7 @@ int gated_ffn_bwd(const ffn_problem* p, const void* x, const void* w_gate, const
         if ((e = launch_gemm(p->dtype, DW, a, stream)) != hipSuccess) return status(e);
     }
     if (dw_down) {
-        a.q = dy, a.ldq = l.D, a.p0 = b + l.h, a.ldp = l.F;
+        a.q = dy, a.ldq = l.D, a.p0 = saved ? saved_h(l, saved) : nullptr, a.ldp = l.F;
         a.M = l.D, a.N = l.F, a.K = l.T;
         a.out0 = dw_down, a.osplit = INT_MAX, a.ldo = p->F, a.rows_out = p->D, a.cols_out = p->F;
         e = launch_gemm(p->dtype, DW, a, stream);

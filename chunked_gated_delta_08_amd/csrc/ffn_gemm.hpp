@@ -222,19 +222,17 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int m, int n, f32x4 v,
         for (int e = 0; e < 4; e++) h[e] = act_f<ACT>(v[e]) * w[e];
         store4<E>((E*)a.h + (int64_t)m * a.N, n, a.N, h);
     } else if constexpr (KIND == DH) {
-        f32x4 dg, du, h;
+        f32x4 dg, du;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             float act, slope;
             act_slope<ACT>(kept.g[e], act, slope);
             dg[e] = v[e] * kept.u[e] * slope;
             du[e] = v[e] * act;
-            h[e] = act * kept.u[e];
         }
         E* d = (E*)a.dgu + (int64_t)m * 2 * a.N;
         store4<E>(d, n, a.N, dg);
         store4<E>(d + a.N, n, a.N, du);
-        store4<E>((E*)a.h + (int64_t)m * a.N, n, a.N, h);
     } else {
         const bool second = m >= a.osplit;
         if (second) m -= a.osplit;
@@ -251,8 +249,9 @@ template <int KIND, class F> __device__ __forceinline__ void by_act(const GemmAr
     else f(integral_constant<int, GDN_FFN_SIGMOID>{});
 }
 
+// The second bound: registers for as many workgroups as a CU's 160 KB of LDS hold.
 template <class E, int KIND, int BM, int BN, int WM, int WN, int NST>
-__global__ __launch_bounds__(64 * WM * WN) void ffn_gemm_kernel(GemmArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, 163840 / ((BM + BN) * 128 * NST) * WM * WN / 4) void ffn_gemm_kernel(GemmArgs a) {
     constexpr bool PAIR = KIND == GATE_UP, QT = KIND == DW, PT = KIND == DH || KIND == DX || KIND == DW;
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16, KE = Type<E>::KE;
     constexpr int BT = PAIR ? BN / 2 : BN;      // columns of a tile
@@ -375,7 +374,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm_kernel(GemmArgs a) {
     // DEPTH passes ahead.  Quad q of a row lies at q ^ row.
     constexpr int STEP = PAIR ? 2 : 1, COLS = 16 * TN / STEP, QUADS = 4 * TN;
     constexpr int LPR = COLS / 4, RPP = 64 / LPR;                      // lanes of a row, rows of a pass
-    constexpr int CH = TM < 4 ? TM : 4, PC = 16 * CH / RPP, DEPTH = PC < 4 ? PC : 4;
+    constexpr int CH = TM < 4 ? TM : 4, PC = 16 * CH / RPP, DEPTH = PC < 4 ? PC : BM * BN == 128 * 128 && NST == 2 ? 2 : 4;   // 2: registers for two workgroups
     static_assert(NW * 16 * CH * QUADS * 16 <= NST * STAGE && TM % CH == 0 && PC % DEPTH == 0, "fits the stages");
     const int r = lane & 15, g = lane >> 4;
     char* mine = smem + wave * 16 * CH * QUADS * 16;
@@ -485,6 +484,7 @@ hipError_t run_shape(const GemmArgs& a, hipStream_t s) {
 template <class E, int KIND> hipError_t run_kind(const GemmArgs& a, int cfg, hipStream_t s) {
     switch (cfg) {
         case BIG: return run_shape<E, KIND, 256, 256, 2, 4, 2>(a, s);
+        case WIDE: return run_shape<E, KIND, 256, 128, 4, 2, 3>(a, s);
         case MIDDLE: return run_shape<E, KIND, 128, 128, 2, 4, 2>(a, s);
         case DEEP: return run_shape<E, KIND, 128, 128, 2, 4, 4>(a, s);
         case LOW: return run_shape<E, KIND, 64, 128, 2, 4, 3>(a, s);

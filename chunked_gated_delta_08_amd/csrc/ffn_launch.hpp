@@ -20,7 +20,7 @@ struct GemmArgs {
     void* out0; void* out1; int64_t ldo;            // plain: rows from osplit on are out1's
     int osplit, rows_out, cols_out;                 // rows of each that exist, columns that exist
     float* gu;                                      // gate and up before the activation, [M][2 N]
-    void* h; void* dgu;                             // [M][N], [M][2 N]
+    void* h; void* dgu;                             // act(gate) up [M][N], and the gradients of gate and up [M][2 N]
     int act;
 };
 
@@ -38,7 +38,7 @@ struct PadArgs {
 };
 
 // Tile shape and number of splits along k of a product.
-enum Config { BIG, MIDDLE, DEEP, LOW, SMALL, THIN, TILES };
+enum Config { BIG, WIDE, MIDDLE, DEEP, LOW, SMALL, THIN, TILES };
 struct Shape {
     int cfg, splits, steps, tilesM, tilesN;
 };

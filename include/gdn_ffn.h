@@ -41,14 +41,16 @@ typedef struct ffn_problem {
 /* Bytes of workspace gated_ffn_fwd (bwd = 0) or gated_ffn_bwd (bwd != 0) needs; 0 if the problem is invalid. */
 size_t ffn_workspace_size(const ffn_problem *p, int bwd);
 
-/* Floats that a token's g and u take in `saved`: 2F, F rounded up to a multiple of 8 (of 4 for fp32); -1 if invalid. */
+/* Floats that a token takes in `saved`: g and u in fp32 and h in the type, F rounded up to a multiple of 8 (of 4
+ * for fp32); -1 if invalid. */
 int64_t ffn_saved_width(const ffn_problem *p);
 
 /*
  * gated_ffn_fwd -- y = (act(x Wg^T) (x Wu^T)) Wd^T.
  *   x [T, D]   w_gate, w_up [F, D] (two halves of one [2F, D] tensor, say)   w_down [D, F]
  *   y [T, D]
- *   saved [T, ffn_saved_width(p)] fp32, 16-byte aligned, or NULL   g and u of each token, for gated_ffn_bwd
+ *   saved [T, ffn_saved_width(p)] fp32, 16-byte aligned, or NULL   what gated_ffn_bwd needs:
+ *       g and u of every token, behind them h
  */
 int gated_ffn_fwd(const ffn_problem *p, const void *x, const void *w_gate, const void *w_up, const void *w_down,
                   void *y, float *saved, void *ws, size_t ws_bytes, hipStream_t stream);

@@ -190,7 +190,7 @@ def test_ffn_no_tokens(B):
     d = {n: t.cuda() for n, t in inputs(3, 40, 72, "bf16").items()}
     e = {**d, "x": d["x"][:0], "dy": d["dy"][:0]}
     f = B.gated_ffn_fwd(e["x"], e["wg"], e["wu"], e["wd"], want_saved=True)
-    assert f["y"].shape == (0, 40) and f["saved"].shape == (0, 144)
+    assert f["y"].shape == (0, 40) and f["saved"].shape == (0, 180)
     out = {k: torch.ones_like(v) for k, v in zip(NAMES, (e["x"], e["wg"], e["wu"], e["wd"]))}
     B.gated_ffn_bwd(e["x"], e["wg"], e["wu"], e["wd"], f["saved"], e["dy"], out=out)
     assert all((out[k] == 0).all() for k in NAMES[1:])
@@ -244,7 +244,7 @@ def test_ffn_halves_of_one_weight(B):
 
 
 def test_ffn_far_offsets(B):
-    """Rows beyond 2^32 bytes of the saved gate and up rows (4.6 GB) and of dgu."""
+    """Rows beyond 2^32 bytes of the saved gate and up rows (4.6 GB, h behind them) and of dgu."""
     T, D, F = 70000, 64, 8192
     G = torch.Generator(device="cuda").manual_seed(3)
 
