@@ -6,21 +6,25 @@
 namespace ffn {
 
 namespace {
-// Of each tile: its sizes, how many workgroups a CU holds, and the time of a step where one of them has
-// the CU, where as many as it holds share it (all of them), and of the rest of a tile; us, for 16-bit types and fp32,
-// from runs of all five products at 128 to 16384 tokens.
+// Of each tile: its sizes, how many workgroups a CU holds, and in us the time of a step where one of them has
+// the CU, where as many as it holds share it (all of them), and of the rest of a tile, for 16-bit types and fp32
+// (0: not used, the smaller tiles are as fast; an fp32 step is bound by the matrix unit whatever the tile).
+// Fitted to 9036 (16-bit) and 8696 (fp32) timings of the five products, 62 and 47 sizes from 100 to 16384 tokens,
+// every tile and number of splits: what the estimate picks takes 1.1 % (fp32 0.3 %) longer than the fastest, on average,
+// and at worst 30 % (9 %).
 struct Tile {
     int bm, bn, held;
-    float one[2], all[2], rest;
+    float one[2], all[2], rest[2];
 };
 constexpr Tile TILE[] = {
-    {256, 256, 1, {1.65f, 7.6f}, {1.65f, 7.6f}, 6.f},
-    {256, 128, 1, {0.93f, 4.0f}, {0.93f, 4.0f}, 4.5f},
-    {128, 128, 2, {0.55f, 2.2f}, {0.98f, 3.8f}, 3.f},
-    {128, 128, 1, {0.47f, 2.1f}, {0.47f, 2.1f}, 3.f},
-    {64, 128, 2, {0.35f, 1.1f}, {0.59f, 1.95f}, 2.f},
-    {64, 64, 2, {0.22f, 0.65f}, {0.37f, 1.08f}, 1.5f},
+    {256, 256, 1, {1.38f, 0.f}, {1.38f, 0.f}, {2.0f, 0.f}},
+    {256, 128, 1, {0.78f, 0.f}, {0.78f, 0.f}, {1.8f, 0.f}},
+    {128, 128, 2, {0.585f, 1.88f}, {0.836f, 3.56f}, {0.1f, 1.4f}},
+    {128, 128, 1, {0.47f, 0.f}, {0.47f, 0.f}, {1.1f, 0.f}},
+    {64, 128, 2, {0.327f, 1.01f}, {0.57f, 1.9f}, {0.65f, 1.0f}},
+    {64, 64, 2, {0.194f, 0.534f}, {0.369f, 1.0f}, {0.41f, 1.2f}},
 };
+constexpr float JOIN = 3.f, JOIN_SUM = 1.1e-6f;   // the launch that joins splits, and for each sum of a split
 constexpr int CUS = 256;
 }  // namespace
 
@@ -46,7 +50,8 @@ Shape shape_of(Kind kind, int M, int N, int K, int esize) {
     }
     Shape best{};
     float least = 0.f;
-    for (int c = 0; c < THIN; c++)
+    for (int c = 0; c < THIN; c++) {
+        if (TILE[c].one[wide] == 0.f) continue;
         for (int want = 1; want <= 16; want++) {
             const Tile& t = TILE[c];
             const Shape s = shape(c, t.bm, t.bn, want);
@@ -54,10 +59,11 @@ Shape shape_of(Kind kind, int M, int N, int K, int esize) {
             if (want > 1 && (all < 4 * want || tiles * (want - 1) >= 2 * CUS)) break;
             if (want > 1 && s.splits != want) continue;
             const int64_t each = (tiles * s.splits + CUS - 1) / CUS, full = each / t.held, odd = each % t.held;
-            float us = full * (s.steps * t.all[wide] + t.rest) + odd * (s.steps * t.one[wide] + t.rest);
-            if (s.splits > 1) us += 4.f + 2e-6f * s.splits * M * N * (kind == GATE_UP ? 2 : 1);   // 8 bytes each at 4 TB/s
+            float us = full * (s.steps * t.all[wide] + t.rest[wide]) + odd * (s.steps * t.one[wide] + t.rest[wide]);
+            if (s.splits > 1) us += JOIN + JOIN_SUM * s.splits * M * N * (kind == GATE_UP ? 2 : 1);
             if (best.tilesM == 0 || us < least) least = us, best = s;
         }
+    }
     return best;
 }
 

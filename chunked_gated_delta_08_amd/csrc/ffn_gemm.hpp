@@ -482,14 +482,18 @@ hipError_t run_shape(const GemmArgs& a, hipStream_t s) {
 }
 
 template <class E, int KIND> hipError_t run_kind(const GemmArgs& a, int cfg, hipStream_t s) {
+    if constexpr (sizeof(E) == 2) {
+        if (cfg == BIG) return run_shape<E, KIND, 256, 256, 2, 4, 2>(a, s);
+        if (cfg == WIDE) return run_shape<E, KIND, 256, 128, 4, 2, 3>(a, s);
+        if (cfg == DEEP) return run_shape<E, KIND, 128, 128, 2, 4, 4>(a, s);
+    }
+    if constexpr (KIND == GATE_UP || KIND == DOWN) {
+        if (cfg == THIN) return run_shape<E, KIND, 32, 64, 2, 2, 6>(a, s);
+    }
     switch (cfg) {
-        case BIG: return run_shape<E, KIND, 256, 256, 2, 4, 2>(a, s);
-        case WIDE: return run_shape<E, KIND, 256, 128, 4, 2, 3>(a, s);
         case MIDDLE: return run_shape<E, KIND, 128, 128, 2, 4, 2>(a, s);
-        case DEEP: return run_shape<E, KIND, 128, 128, 2, 4, 4>(a, s);
         case LOW: return run_shape<E, KIND, 64, 128, 2, 4, 3>(a, s);
-        case SMALL: return run_shape<E, KIND, 64, 64, 2, 2, 4>(a, s);
-        default: return run_shape<E, KIND, 32, 64, 2, 2, 6>(a, s);
+        default: return run_shape<E, KIND, 64, 64, 2, 2, 4>(a, s);
     }
 }
 template <class E> hipError_t run_gemm(Kind kind, const GemmArgs& a, int cfg, hipStream_t s) {
