@@ -1,5 +1,7 @@
 // ffn.hip -- which tile and how many splits a product of the feed-forward block takes, and the
 // copy into padded rows.
+#include <algorithm>
+
 #include "ffn_launch.hpp"
 #include "../../include/gdr.h"
 
@@ -9,7 +11,7 @@ namespace {
 // Of each tile: its sizes, how many workgroups a CU holds, and in us the time of a step where one of them has
 // the CU, where as many as it holds share it (all of them), and of the rest of a tile, for 16-bit types and fp32
 // (0: not used, the smaller tiles are as fast; an fp32 step is bound by the matrix unit whatever the tile).
-// Fitted to 9036 (16-bit) and 8696 (fp32) timings of the five products, 62 and 47 sizes from 100 to 16384 tokens,
+// Fitted to 9036 (16-bit) and 8696 (fp32) timings of the products, 62 and 47 sizes from 100 to 16384 tokens,
 // every tile and number of splits: what the estimate picks takes 1.1 % (fp32 0.3 %) longer than the fastest, on average,
 // and at worst 30 % (9 %).
 struct Tile {
@@ -26,6 +28,14 @@ constexpr Tile TILE[] = {
 };
 constexpr float JOIN = 3.f, JOIN_SUM = 1.1e-6f;   // the launch that joins splits, and for each sum of a split
 constexpr int CUS = 256;
+
+Shape shape(Kind kind, int c, int bm, int bn, int M, int N, int all, int want) {
+    const int bt = kind == GATE_UP ? bn / 2 : bn;
+    Shape s{c, 1, 0, (M + bm - 1) / bm, (N + bt - 1) / bt};
+    s.steps = (all + want - 1) / want;
+    if (s.steps) s.splits = (all + s.steps - 1) / s.steps;
+    return s;
+}
 }  // namespace
 
 // The tile and the splits of least estimated time: each CU takes its share of the workgroups, as
@@ -35,18 +45,11 @@ constexpr int CUS = 256;
 // tiles of 64 x 128 42.5, 384 of 64 x 64 47.2; down 64 tiles in 4 splits 25.2, in 8 27.3, whole 61.2).
 Shape shape_of(Kind kind, int M, int N, int K, int esize) {
     const int ke = 128 / esize, all = (K + ke - 1) / ke, wide = esize == 4;
-    auto shape = [&](int c, int bm, int bn, int want) {
-        const int bt = kind == GATE_UP ? bn / 2 : bn;
-        Shape s{c, 1, 0, (M + bm - 1) / bm, (N + bt - 1) / bt};
-        s.steps = (all + want - 1) / want;
-        if (s.steps) s.splits = (all + s.steps - 1) / s.steps;
-        return s;
-    };
     if (M <= 64 && (kind == GATE_UP || kind == DOWN)) {
         const int small = (N + 63) / 64 * (kind == GATE_UP ? 2 : 1), c = M <= 32 ? THIN : small <= CUS ? SMALL : LOW;
         int want = CUS / small;
         if (want > all / 4) want = all / 4;
-        return shape(c, c == THIN ? 32 : 64, c == LOW ? 128 : 64, want < 1 ? 1 : want);
+        return shape(kind, c, c == THIN ? 32 : 64, c == LOW ? 128 : 64, M, N, all, want < 1 ? 1 : want);
     }
     Shape best{};
     float least = 0.f;
@@ -54,7 +57,7 @@ Shape shape_of(Kind kind, int M, int N, int K, int esize) {
         if (TILE[c].one[wide] == 0.f) continue;
         for (int want = 1; want <= 16; want++) {
             const Tile& t = TILE[c];
-            const Shape s = shape(c, t.bm, t.bn, want);
+            const Shape s = shape(kind, c, t.bm, t.bn, M, N, all, want);
             const int64_t tiles = (int64_t)s.tilesM * s.tilesN;
             if (want > 1 && (all < 4 * want || tiles * (want - 1) >= 2 * CUS)) break;
             if (want > 1 && s.splits != want) continue;
@@ -77,9 +80,113 @@ hipError_t launch_gemm(int dtype, Kind kind, GemmArgs a, hipStream_t s) {
     const Shape sh = shape_of(kind, a.M, a.N, a.K, dtype == GDR_F32 ? 4 : 2);
     a.tilesM = sh.tilesM, a.tilesN = sh.tilesN, a.splits = sh.splits, a.steps = sh.steps;
     switch (dtype) {
-        case GDR_F32: return gemm_f32(kind, a, sh, s);
-        case GDR_F16: return gemm_f16(kind, a, sh, s);
-        default: return gemm_bf16(kind, a, sh, s);
+        case GDR_F32: return gemm_f32(kind, a, sh.cfg, s);
+        case GDR_F16: return gemm_f16(kind, a, sh.cfg, s);
+        default: return gemm_bf16(kind, a, sh.cfg, s);
+    }
+}
+
+namespace {
+// When the workgroups of the gradients' products are through, in us: they start in their order wherever a place is free,
+// those of a product take the same time.  The constants, as TILE's, from 17 sizes with each tile and number of splits.
+float makespan(const Shape (&s)[3], const Tile& t, int wide) {
+    struct { float at; int64_t places; } level[8];
+    int64_t total = 0;
+    for (const Shape& x : s) total += (int64_t)x.tilesM * x.tilesN * x.splits;
+    const bool alone = total <= CUS;
+    const int64_t places = alone ? CUS : (int64_t)CUS * t.held;
+    int n = 1;
+    level[0] = {0.f, places};
+    float end = 0.f;
+    for (const Shape& x : s) {
+        int64_t left = (int64_t)x.tilesM * x.tilesN * x.splits;
+        const float d = x.steps * (alone ? t.one : t.all)[wide] + t.rest[wide];
+        const int64_t rounds = left / places;   // every place gets as many
+        for (int i = 0; i < n; i++) level[i].at += rounds * d, end = std::max(end, level[i].at);
+        left -= rounds * places;
+        while (left > 0) {   // the earliest places
+            int e = 0;
+            for (int i = 1; i < n; i++)
+                if (level[i].at < level[e].at) e = i;
+            const int64_t m = std::min(left, level[e].places);
+            const float at = level[e].at + d;
+            end = std::max(end, at);
+            left -= m;
+            if (m == level[e].places || n == 8) level[e].at = at;
+            else level[e].places -= m, level[n++] = {at, m};
+        }
+    }
+    return end;
+}
+constexpr Tile GRAD_TILE[] = {
+    {256, 256, 1, {1.55f, 0.f}, {1.55f, 0.f}, {6.4f, 0.f}},
+    {256, 128, 1, {0.89f, 0.f}, {0.89f, 0.f}, {4.2f, 0.f}},
+    {128, 128, 2, {0.71f, 1.88f}, {0.96f, 3.56f}, {1.3f, 1.4f}},
+    {64, 64, 2, {0.f, 0.534f}, {0.f, 1.0f}, {0.f, 1.2f}},
+};
+constexpr int GRAD_CONFIG[] = {BIG, WIDE, MIDDLE, SMALL};
+}  // namespace
+
+GradPlan grad_plan(int T, int D, int F, int esize) {
+    const int ke = 128 / esize, wide = esize == 4;
+    const int M[3] = {T, 2 * F, D}, N[3] = {D, D, F}, K[3] = {2 * F, T, T};
+    static const int by_dx[3] = {0, 1, 2}, by_dw[3] = {1, 2, 0}, dx_splits[] = {1, 2, 3, 4, 6, 8}, dw_splits[] = {1, 2, 4};
+    const int* order = 2 * F >= T ? by_dx : by_dw;   // the longest sums first
+    GradPlan best{};
+    float least = -1.f;
+    for (int c = 0; c < 4; c++) {
+        const Tile& t = GRAD_TILE[c];
+        if (t.one[wide] == 0.f) continue;
+        for (int sx : dx_splits)
+            for (int sw : dw_splits) {
+                GradPlan p{GRAD_CONFIG[c], {}, {order[0], order[1], order[2]}};
+                float us = 0.f;
+                bool ok = true, joined = false;
+                for (int i = 0; i < 3 && ok; i++) {
+                    const int j = order[i], all = (K[j] + ke - 1) / ke, want = j == 0 ? sx : sw;
+                    const Shape x = shape(DX, c, t.bm, t.bn, M[j], N[j], all, want);
+                    ok = want == 1 || (all >= 4 * want && (int64_t)x.tilesM * x.tilesN * (want - 1) < 2 * CUS);
+                    if (x.splits > 1) joined = true, us += JOIN_SUM * x.splits * M[j] * N[j];
+                    p.s[i] = x;
+                }
+                if (!ok) continue;
+                us += makespan(p.s, t, wide) + (joined ? JOIN : 0.f);
+                if (least < 0.f || us < least) least = us, best = p;
+            }
+    }
+    return best;
+}
+
+size_t grad_floats(const GradPlan& p, int T, int D, int F) {
+    const size_t size[3] = {(size_t)T * D, 2 * (size_t)F * D, (size_t)D * F};
+    size_t n = 0;
+    for (int i = 0; i < 3; i++)
+        if (p.s[i].splits > 1) n += p.s[i].splits * size[p.order[i]];
+    return n;
+}
+
+hipError_t launch_grads(int dtype, const GradPlan& plan, const GemmArgs (&g)[3], const bool (&want)[3], float* part,
+                        hipStream_t s) {
+    GradArgs p{};
+    int at = 0;
+    for (int i = 0; i < 3; i++) {
+        const int j = plan.order[i];
+        const Shape& x = plan.s[i];
+        GemmArgs& a = p.g[i];
+        a = g[j];
+        p.dx[i] = j == 0;
+        p.start[i] = at;
+        if (!want[j] || a.M == 0) continue;
+        a.tilesM = x.tilesM, a.tilesN = x.tilesN, a.splits = x.splits, a.steps = x.steps;
+        if (a.splits > 1) a.part = part, part += (size_t)a.splits * a.M * a.N;
+        at += (a.tilesM * a.tilesN * a.splits + 7) / 8 * 8;
+    }
+    p.start[3] = at;
+    if (at == 0) return hipSuccess;
+    switch (dtype) {
+        case GDR_F32: return grads_f32(p, plan.cfg, s);
+        case GDR_F16: return grads_f16(p, plan.cfg, s);
+        default: return grads_bf16(p, plan.cfg, s);
     }
 }
 

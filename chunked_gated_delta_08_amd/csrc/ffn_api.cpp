@@ -3,6 +3,8 @@
 // allocates device memory.
 #include <limits.h>
 
+#include <algorithm>
+
 #include "ffn_launch.hpp"
 #include "gdn_ffn.h"
 #include "layer_check.hpp"
@@ -14,7 +16,7 @@ using namespace ffn;
 int check(const ffn_problem* p) {
     if (!p || p->T < 0 || p->D < 1 || p->F < 1 || !known(p->dtype)) return GDR_ERR_INVALID;
     if (p->act != GDN_FFN_SILU && p->act != GDN_FFN_SIGMOID && p->act != GDN_FFN_GELU) return GDR_ERR_INVALID;
-    if (p->T > (1 << 24) || p->D > 65536 || p->F > 65536 || p->T * (p->D + 2LL * p->F) >= 1LL << 38)
+    if (p->T > (1 << 24) || p->D > 65536 || p->F > 65536 || p->T * (p->D + 2LL * p->F) >= 1LL << 36)
         return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
@@ -25,6 +27,7 @@ struct Plan {
     int T, D, F, e, piece;
     bool pad;
     size_t h, dgu, part, x, wg, wu, wd, dy, bytes;
+    GradPlan grads;
 };
 Plan plan_of(const ffn_problem* p, bool bwd) {
     Plan l{};
@@ -46,9 +49,8 @@ Plan plan_of(const ffn_problem* p, bool bwd) {
     if (bwd) {
         l.dgu = take(2 * row);
         most(DH, l.T, l.F, l.D);
-        most(DX, l.T, l.D, 2 * l.F);
-        most(DW, l.D, l.F, l.T);
-        most(DW, 2 * l.F, l.D, l.T);
+        l.grads = grad_plan(l.T, l.D, l.F, l.e);
+        f = std::max(f, grad_floats(l.grads, l.T, l.D, l.F));
     } else {
         l.h = take(row);   // not used by a call that keeps it
         most(GATE_UP, l.T, l.F, l.D);
@@ -148,26 +150,18 @@ int gated_ffn_bwd(const ffn_problem* p, const void* x, const void* w_gate, const
     a.q = dy, a.ldq = l.D, a.p0 = w_down, a.ldp = l.F;
     a.M = l.T, a.N = l.F, a.K = l.D;
     if ((e = launch_gemm(p->dtype, DH, a, stream)) != hipSuccess) return status(e);
-    a.osplit = INT_MAX;
-    if (dx) {
-        a.q = b + l.dgu, a.ldq = 2 * l.F, a.p0 = w_gate, a.p1 = w_up, a.psplit = l.F, a.ldp = l.D;
-        a.M = l.T, a.N = l.D, a.K = 2 * l.F;
-        a.out0 = dx, a.ldo = p->D, a.rows_out = l.T, a.cols_out = p->D;
-        if ((e = launch_gemm(p->dtype, DX, a, stream)) != hipSuccess) return status(e);
-    }
-    a.p1 = nullptr;
-    if (dw_gate) {
-        a.q = b + l.dgu, a.ldq = 2 * l.F, a.p0 = x, a.ldp = l.D;
-        a.M = 2 * l.F, a.N = l.D, a.K = l.T;
-        a.out0 = dw_gate, a.out1 = dw_up, a.osplit = l.F, a.ldo = p->D, a.rows_out = p->F, a.cols_out = p->D;
-        if ((e = launch_gemm(p->dtype, DW, a, stream)) != hipSuccess) return status(e);
-    }
-    if (dw_down) {
-        a.q = dy, a.ldq = l.D, a.p0 = saved ? saved_h(l, saved) : nullptr, a.ldp = l.F;
-        a.M = l.D, a.N = l.F, a.K = l.T;
-        a.out0 = dw_down, a.osplit = INT_MAX, a.ldo = p->F, a.rows_out = p->D, a.cols_out = p->F;
-        e = launch_gemm(p->dtype, DW, a, stream);
-    }
+    GemmArgs g[3];   // dx, dw of gate and up, dw of down
+    for (GemmArgs& x : g) x = a, x.osplit = INT_MAX, x.p1 = nullptr;
+    g[0].q = b + l.dgu, g[0].ldq = 2 * l.F, g[0].p0 = w_gate, g[0].p1 = w_up, g[0].psplit = l.F, g[0].ldp = l.D;
+    g[0].M = l.T, g[0].N = l.D, g[0].K = 2 * l.F;
+    g[0].out0 = dx, g[0].ldo = p->D, g[0].rows_out = l.T, g[0].cols_out = p->D;
+    g[1].q = b + l.dgu, g[1].ldq = 2 * l.F, g[1].p0 = x, g[1].ldp = l.D;
+    g[1].M = 2 * l.F, g[1].N = l.D, g[1].K = l.T;
+    g[1].out0 = dw_gate, g[1].out1 = dw_up, g[1].osplit = l.F, g[1].ldo = p->D, g[1].rows_out = p->F, g[1].cols_out = p->D;
+    g[2].q = dy, g[2].ldq = l.D, g[2].p0 = saved ? saved_h(l, saved) : nullptr, g[2].ldp = l.F;
+    g[2].M = l.D, g[2].N = l.F, g[2].K = l.T;
+    g[2].out0 = dw_down, g[2].ldo = p->F, g[2].rows_out = p->D, g[2].cols_out = p->F;
+    e = launch_grads(p->dtype, l.grads, g, {dx != nullptr, dw_gate != nullptr, dw_down != nullptr}, a.part, stream);
     return status(e);
 }
 

@@ -266,24 +266,23 @@ template <int KIND, class F> __device__ __forceinline__ void by_act(const GemmAr
     else f(integral_constant<int, GDN_FFN_SIGMOID>{});
 }
 
-// The second bound: registers for as many workgroups as a CU's 160 KB of LDS hold.
+// Workgroup `block` of a product.
 template <class E, int KIND, int BM, int BN, int WM, int WN, int NST>
-__global__ __launch_bounds__(64 * WM * WN, 163840 / ((BM + BN) * 128 * NST) * WM * WN / 4) void ffn_gemm_kernel(GemmArgs a) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs& a, int block, char* smem) {
     constexpr bool PAIR = KIND == GATE_UP, QT = KIND == DW, PT = KIND == DH || KIND == DX || KIND == DW;
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16, KE = Type<E>::KE;
     constexpr int BT = PAIR ? BN / 2 : BN;      // columns of a tile
     using Q = Operand<E, BM, NW, QT, false>;
     using P = Operand<E, BN, NW, PT, PAIR>;
     constexpr int STAGE = Q::BYTES + P::BYTES, LOADS = Q::PER + P::PER;
-    __shared__ __attribute__((aligned(1024))) char smem[NST * STAGE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
 
     // Workgroups go to the chip's 8 parts in turn; each part takes a run of tiles, and within
     // it 8 rows of tiles at a time, so that its L2 serves an operand's tile to several.
     const int tiles = a.tilesM * a.tilesN, total = tiles * a.splits;
-    const int xcd = blockIdx.x & 7, per = total >> 3, rem = total & 7;
-    int id = xcd * per + (xcd < rem ? xcd : rem) + (int)(blockIdx.x >> 3);
+    const int xcd = block & 7, per = total >> 3, rem = total & 7;
+    int id = xcd * per + (xcd < rem ? xcd : rem) + (block >> 3);
     const int split = id / tiles;
     id -= split * tiles;
     const int group = id / (8 * a.tilesN), in = id - group * 8 * a.tilesN;
@@ -455,8 +454,29 @@ __global__ __launch_bounds__(64 * WM * WN, 163840 / ((BM + BN) * 128 * NST) * WM
     });
 }
 
+// Registers for as many workgroups as a CU's 160 KB of LDS hold.
+#define FFN_BOUNDS __launch_bounds__(64 * WM * WN, 163840 / ((BM + BN) * 128 * NST) * WM * WN / 4)
+template <class E, int KIND, int BM, int BN, int WM, int WN, int NST> __global__ FFN_BOUNDS void ffn_gemm_kernel(GemmArgs a) {
+    __shared__ __attribute__((aligned(1024))) char smem[NST * (BM + BN) * 128];
+    gemm_tile<E, KIND, BM, BN, WM, WN, NST>(a, blockIdx.x, smem);
+}
+// The gradients' products in one launch, one after another in the grid: alone each of them fills the chip badly where
+// there are few tokens.  Each begins at a multiple of 8, so that its tiles keep to their parts of the chip.
+template <class E, int BM, int BN, int WM, int WN, int NST> __global__ FFN_BOUNDS void ffn_grads_kernel(GradArgs p) {
+    __shared__ __attribute__((aligned(1024))) char smem[NST * (BM + BN) * 128];
+    int block = blockIdx.x;
+    GemmArgs a = p.g[0];
+    bool dx = p.dx[0];
+    if (block >= p.start[1]) a = p.g[1], dx = p.dx[1];
+    if (block >= p.start[2]) a = p.g[2], dx = p.dx[2];
+    block -= block >= p.start[2] ? p.start[2] : block >= p.start[1] ? p.start[1] : 0;
+    if (block >= a.tilesM * a.tilesN * a.splits) return;
+    if (dx) gemm_tile<E, DX, BM, BN, WM, WN, NST>(a, block, smem);
+    else gemm_tile<E, DW, BM, BN, WM, WN, NST>(a, block, smem);
+}
+
 // The splits' sums in their order, and what becomes of them: four columns a lane.
-template <class E, int KIND> __global__ __launch_bounds__(256) void ffn_join_kernel(GemmArgs a) {
+template <class E, int KIND> __device__ __forceinline__ void join_splits(const GemmArgs& a) {
     constexpr int STEP = KIND == GATE_UP ? 2 : 1;
     const int quads = a.N / 4;
     const int64_t total = (int64_t)a.M * quads, plane = (int64_t)a.M * STEP * a.N;
@@ -487,14 +507,31 @@ template <class E, int KIND> __global__ __launch_bounds__(256) void ffn_join_ker
     }
 }
 
+template <class E, int KIND> __global__ __launch_bounds__(256) void ffn_join_kernel(GemmArgs a) { join_splits<E, KIND>(a); }
+template <class E> __global__ __launch_bounds__(256) void ffn_join_grads_kernel(GradArgs p) {   // dx and dw end alike
+    GemmArgs a = p.g[0];
+    if (blockIdx.y == 1) a = p.g[1];
+    if (blockIdx.y == 2) a = p.g[2];
+    if (a.splits > 1) join_splits<E, DX>(a);
+}
+
+inline unsigned join_blocks(const GemmArgs& a) {
+    const int64_t n = ((int64_t)a.M * (a.N / 4) + 255) / 256;
+    return (unsigned)(n < 4096 ? n : 4096);
+}
+template <class E, int BM, int BN, int WM, int WN, int NST> hipError_t run_grads_shape(const GradArgs& p, hipStream_t s) {
+    hipLaunchKernelGGL((ffn_grads_kernel<E, BM, BN, WM, WN, NST>), dim3((unsigned)p.start[3]), dim3(64 * WM * WN), 0, s, p);
+    unsigned most = 0;
+    for (const GemmArgs& a : p.g)
+        if (a.splits > 1 && join_blocks(a) > most) most = join_blocks(a);
+    if (most) hipLaunchKernelGGL(ffn_join_grads_kernel<E>, dim3(most, 3), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
 template <class E, int KIND, int BM, int BN, int WM, int WN, int NST>
 hipError_t run_shape(const GemmArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((ffn_gemm_kernel<E, KIND, BM, BN, WM, WN, NST>), dim3((unsigned)(a.tilesM * a.tilesN * a.splits)),
                        dim3(64 * WM * WN), 0, s, a);
-    if (a.splits > 1) {
-        const int64_t n = ((int64_t)a.M * (a.N / 4) + 255) / 256;
-        hipLaunchKernelGGL((ffn_join_kernel<E, KIND>), dim3((unsigned)(n < 4096 ? n : 4096)), dim3(256), 0, s, a);
-    }
+    if (a.splits > 1) hipLaunchKernelGGL((ffn_join_kernel<E, KIND>), dim3(join_blocks(a)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -517,9 +554,16 @@ template <class E> hipError_t run_gemm(Kind kind, const GemmArgs& a, int cfg, hi
     switch (kind) {
         case GATE_UP: return run_kind<E, GATE_UP>(a, cfg, s);
         case DOWN: return run_kind<E, DOWN>(a, cfg, s);
-        case DH: return run_kind<E, DH>(a, cfg, s);
-        case DX: return run_kind<E, DX>(a, cfg, s);
-        default: return run_kind<E, DW>(a, cfg, s);
+        default: return run_kind<E, DH>(a, cfg, s);
+    }
+}
+template <class E> hipError_t run_grads(const GradArgs& p, int cfg, hipStream_t s) {
+    if constexpr (sizeof(E) == 2) {
+        if (cfg == BIG) return run_grads_shape<E, 256, 256, 2, 4, 2>(p, s);
+        if (cfg == WIDE) return run_grads_shape<E, 256, 128, 4, 2, 3>(p, s);
+        return run_grads_shape<E, 128, 128, 2, 4, 2>(p, s);
+    } else {
+        return cfg == MIDDLE ? run_grads_shape<E, 128, 128, 2, 4, 2>(p, s) : run_grads_shape<E, 64, 64, 2, 2, 4>(p, s);
     }
 }
 

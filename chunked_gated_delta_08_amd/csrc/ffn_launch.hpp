@@ -24,6 +24,13 @@ struct GemmArgs {
     int act;
 };
 
+// The products dx, dw of gate and up, dw of down, in any order: where each begins in the grid, and its end.
+struct GradArgs {
+    GemmArgs g[3];
+    bool dx[3];
+    int start[4];
+};
+
 enum Kind { GATE_UP, DOWN, DH, DX, DW };            // which product: orientations and epilogue
 
 // A tensor to copy into rows of another length: dst[r][c] = src[r][c] where that exists, else zero.
@@ -46,10 +53,25 @@ Shape shape_of(Kind kind, int M, int N, int K, int esize);
 size_t part_floats(Kind kind, int M, int N, int K, int esize);
 
 hipError_t launch_gemm(int dtype, Kind kind, GemmArgs a, hipStream_t s);
+
+// The gradients' products: 0 dx, 1 dw of gate and up, 2 dw of down, in one launch and in this order.
+struct GradPlan {
+    int cfg;
+    Shape s[3];
+    int order[3];
+};
+GradPlan grad_plan(int T, int D, int F, int esize);
+size_t grad_floats(const GradPlan& p, int T, int D, int F);
+hipError_t launch_grads(int dtype, const GradPlan& p, const GemmArgs (&g)[3], const bool (&want)[3], float* part,
+                        hipStream_t s);
 hipError_t launch_pad(int esize, const PadArgs& a, hipStream_t s);
 
-hipError_t gemm_bf16(Kind kind, const GemmArgs& a, const Shape& sh, hipStream_t s);
-hipError_t gemm_f16(Kind kind, const GemmArgs& a, const Shape& sh, hipStream_t s);
-hipError_t gemm_f32(Kind kind, const GemmArgs& a, const Shape& sh, hipStream_t s);
+#define FFN_TYPE(T)                                                                      \
+    hipError_t gemm_##T(Kind kind, const GemmArgs& a, int cfg, hipStream_t s);           \
+    hipError_t grads_##T(const GradArgs& p, int cfg, hipStream_t s);
+FFN_TYPE(bf16)
+FFN_TYPE(f16)
+FFN_TYPE(f32)
+#undef FFN_TYPE
 
 }  // namespace ffn

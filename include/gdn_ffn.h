@@ -33,7 +33,7 @@ typedef enum { GDN_FFN_SILU = 0, GDN_FFN_SIGMOID = 1, GDN_FFN_GELU = 2 } gdn_ffn
 
 typedef struct ffn_problem {
     int64_t T;       /* tokens, 0 <= T <= 2^24 */
-    int D, F;        /* width of x and y, of the hidden row; 1 <= D, F <= 65536, T * (D + 2 F) < 2^38 */
+    int D, F;        /* width of x and y, of the hidden row; 1 <= D, F <= 65536, T * (D + 2 F) < 2^36 */
     gdr_dtype dtype; /* type of x, the weights, y, dy and of every gradient */
     gdn_ffn_act act;
 } ffn_problem;

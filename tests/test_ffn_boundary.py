@@ -59,7 +59,7 @@ def bwd(B, p, ws_bytes=BIG, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), -1), (dict(D=0), -1), (dict(F=0), -1), (dict(dtype=3), -1), (dict(act=3), -1), (dict(act=-1), -1),
-    (dict(T=(1 << 24) + 1), -2), (dict(D=65537), -2), (dict(F=65537), -2), (dict(T=1 << 24, D=8192, F=4096), -2)])
+    (dict(T=(1 << 24) + 1), -2), (dict(D=65537), -2), (dict(F=65537), -2), (dict(T=1 << 24, D=2048, F=1024), -2)])
 def test_ffn_problem_refused(B, kw, code):
     p = ffn(B, **kw)
     assert fwd(B, p) == code and bwd(B, p) == code
