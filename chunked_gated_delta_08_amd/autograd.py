@@ -230,10 +230,15 @@ def dropout_add_rms_norm(x, res, weight, p, rng, scale=None, eps=1e-5):
     return DropoutAddRMSNorm.apply(*_contiguous(x, res, weight, scale), p, rng, eps)
 
 
+def _on_16_bytes(t):
+    """Contiguous, and where the feed-forward block's operands have to begin."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class GatedFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, act, keep):
-        x, w_gate, w_up, w_down = (t.contiguous() for t in (x, w_gate, w_up, w_down))
         out = binding.gated_ffn_fwd(x, w_gate, w_up, w_down, act=act, want_saved=keep)
         if keep:
             ctx.save_for_backward(x, w_gate, w_up, w_down, out["saved"])
@@ -244,7 +249,7 @@ class GatedFFN(torch.autograd.Function):
     def backward(ctx, dy):
         x, w_gate, w_up, w_down, saved = ctx.saved_tensors
         need = ctx.needs_input_grad
-        r = binding.gated_ffn_bwd(x, w_gate, w_up, w_down, saved, dy.contiguous(), act=ctx.act, want_dx=need[0],
+        r = binding.gated_ffn_bwd(x, w_gate, w_up, w_down, saved, _on_16_bytes(dy), act=ctx.act, want_dx=need[0],
                                   want_dw=any(need[1:4]))
         return _first_order("gated_ffn", ctx, (dy,), tuple(
             r[k] if n else None for k, n in zip(("dx", "dw_gate", "dw_up", "dw_down"), need)) + (None, None))
@@ -256,5 +261,5 @@ def gated_ffn(x, w_gate, w_up, w_down, act="silu"):
 
     Differentiable in x and the weights; the gradients are in x's dtype.  Between the passes it keeps
     2F floats and F of the type a token, its gate and up rows and their product."""
-    t = _contiguous(x, w_gate, w_up, w_down)
+    t = [_on_16_bytes(v) for v in (x, w_gate, w_up, w_down)]
     return GatedFFN.apply(*t, act, torch.is_grad_enabled() and any(v.requires_grad for v in t))

@@ -7,8 +7,8 @@ Subcommands (run with ``python -m chunked_gated_delta_08_amd.profiling``):
       MiB, fp32, ``torch.mul(src, 1, out=dst)``) a few times: the calibration
       kernel for the FETCH_SIZE / WRITE_SIZE counters.
   layer --case NAME [--reps R]
-      Runs one listed case of perf/operators.py (an operator of the layer around
-      the gated delta rule) R times over three sets of inputs.
+      Runs one listed case of perf/operators.py or perf/more_operators.py (an operator
+      of the layer around the gated delta rule) R times over three sets of inputs.
   stats --csv <prefix>_kernel_stats.csv --out <txt> --cmd "<command>"
       Writes a short text table of per-kernel dispatch counts and durations.  With
       rocprofv3's --mangled-kernels the names are demangled here (its own demangling
@@ -67,6 +67,11 @@ for _k, _f in (("glr_fwd_kernel", "glr"), ("glr_bwd_kernel", "glr"), ("glr_clear
     KERNEL_SOURCES[_k] = [_CS + _f + ".hip", _CS + "layer_launch.hpp"] + _COMMON
     if _f == "glr":
         KERNEL_SOURCES[_k].insert(1, _CS + "glr_chain.hpp")
+for _k in ("add_norm_fwd_kernel", "add_norm_bwd_kernel"):
+    KERNEL_SOURCES[_k].insert(1, _CS + "layer_dropout.hpp")
+KERNEL_SOURCES["dropout_kernel"] = [_CS + "layer_dropout.hip", _CS + "layer_dropout.hpp"] + _ROWS
+for _k in ("ffn_gemm_kernel", "ffn_grads_kernel", "ffn_join_kernel", "ffn_join_grads_kernel", "ffn_pad_kernel"):
+    KERNEL_SOURCES[_k] = [_CS + "ffn_gemm.hpp", _CS + "ffn.hip", _CS + "ffn_launch.hpp"] + _ROWS
 
 
 def _code_of(text):
@@ -126,11 +131,16 @@ def _layer(args):
     import importlib.util
     import torch
     sys.path.insert(0, ROOT)
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
-    cases = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(cases)
+    for name in ("operators", "more_operators"):
+        spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
+        cases = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(cases)
+        case = {c["name"]: c for c in cases.listed()}.get(args.case)
+        if case:
+            break
+    else:
+        sys.exit(f"no case {args.case}")
     cases.own = True
-    case = {c["name"]: c for c in cases.listed()}[args.case]
     states = [cases.prepare(case, seed) for seed in range(3)]
     for i in range(args.reps):
         cases.run(states[i % 3])

@@ -401,6 +401,10 @@ def test_ffn_autograd(B):
     with torch.no_grad():
         assert not A.gated_ffn(x, wg, wu, wd).requires_grad
     assert torch.equal(A.gated_ffn(x.t().contiguous().t(), wg, wu, wd).detach(), want["y"])   # any strides
+    off = torch.empty(x.numel() + 1, device="cuda")[1:].view(x.shape).copy_(x)   # or place
+    with pytest.raises(ValueError, match="x must be aligned"):
+        B.gated_ffn_fwd(off, wg, wu, d["wd"])
+    assert torch.equal(A.gated_ffn(off, wg, wu, wd).detach(), want["y"])
     x.requires_grad_()
     g, = torch.autograd.grad(A.gated_ffn(x, wg, wu, wd).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="second derivative"):
