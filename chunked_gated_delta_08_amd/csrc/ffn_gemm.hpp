@@ -279,15 +279,19 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int block, char* sm
     const int wm = wave / WN, wn = wave % WN;
 
     // Workgroups go to the chip's 8 parts in turn; each part takes a run of tiles, and within
-    // it 8 rows of tiles at a time, so that its L2 serves an operand's tile to several.
+    // it `rows` rows of tiles at a time, so that its L2 serves an operand's tile to several.  Rows of 256: three where
+    // their Q stays in the part's 4 MB (and an odd number, which spreads rows whose pitch is a power of two over
+    // the memory's channels), else four (16384 x 2048 x 8192 bf16, us: gate and up with 8, 4 and 3 rows 1128, 1094
+    // and 973, dh 717, 696 and 676; 8192 x 4096 x 12288: 1293, 1284, 1350 and 793, 796, 816).
     const int tiles = a.tilesM * a.tilesN, total = tiles * a.splits;
     const int xcd = block & 7, per = total >> 3, rem = total & 7;
     int id = xcd * per + (xcd < rem ? xcd : rem) + (block >> 3);
     const int split = id / tiles;
     id -= split * tiles;
-    const int group = id / (8 * a.tilesN), in = id - group * 8 * a.tilesN;
-    const int high = a.tilesM - group * 8 < 8 ? a.tilesM - group * 8 : 8;
-    const int m0 = (group * 8 + in % high) * BM, n0 = in / high * BT;
+    const int rows = BM < 256 ? 8 : a.K * (int)sizeof(E) <= 4096 ? 3 : 4;
+    const int group = id / (rows * a.tilesN), in = id - group * rows * a.tilesN;
+    const int high = a.tilesM - group * rows < rows ? a.tilesM - group * rows : rows;
+    const int m0 = (group * rows + in % high) * BM, n0 = in / high * BT;
 
     const int all = (a.K + KE - 1) / KE, k0 = split * a.steps, k1 = k0 + a.steps < all ? k0 + a.steps : all;
     Q q;
