@@ -3,7 +3,7 @@
 Every HIP source is compiled with packed-fp32 instructions disabled
 (-Xclang -target-feature -Xclang -packed-fp32-ops); objects are built in
 parallel and linked into one shared library exporting the C ABI of
-include/gdr.h.
+include/*.h.
 """
 import os
 import subprocess
