@@ -27,6 +27,17 @@ constexpr Tile TILE[] = {
     {64, 64, 2, {0.194f, 0.534f}, {0.369f, 1.0f}, {0.41f, 1.2f}},
 };
 constexpr float JOIN = 3.f, JOIN_SUM = 1.1e-6f;   // the launch that joins splits, and for each sum of a split
+// The same for up to 64 rows of a product with weights stored [n][k] (GATE_UP, DOWN), with the time that the join takes
+// for each split. From 2600 and 2700 timings of the products, 192 sizes each with 1 to 64 tokens: what is picked takes 0.3 %
+// longer than the fastest on average, at worst 11 % (splits wherever CUs were free took 6 %: whole forwards in a graph, us,
+// 25 x 512 x 1408 bf16 11.6 and now 9.7, 64 x 1024 x 2816 17.3 and 14.1, 64 x 4096 x 5632 fp32 112 and 94).
+constexpr Tile FEW[] = {
+    {32, 64, 2, {0.135f, 0.327f}, {0.241f, 0.62f}, {1.7f, 1.1f}},
+    {64, 128, 2, {0.305f, 1.04f}, {0.744f, 1.99f}, {2.0f, 2.4f}},
+    {64, 64, 2, {0.186f, 0.578f}, {0.459f, 1.05f}, {1.9f, 1.0f}},
+};
+constexpr int FEW_CONFIG[] = {THIN, LOW, SMALL};
+constexpr float FEW_JOIN[] = {1.2f, 1.3f}, FEW_SPLIT[] = {0.25f, 0.3f}, FEW_SUM[] = {1.9e-6f, 1.1e-6f};
 constexpr int CUS = 256;
 
 Shape shape(Kind kind, int c, int bm, int bn, int M, int N, int all, int want) {
@@ -39,33 +50,33 @@ Shape shape(Kind kind, int c, int bm, int bn, int M, int N, int all, int want) {
 }  // namespace
 
 // The tile and the splits of least estimated time: each CU takes its share of the workgroups, as
-// many at once as it holds; splits add the sums' way through memory.  Up to 64 rows of a product with
-// weights stored [n][k] (GATE_UP, DOWN) the weights' bytes are what counts: one workgroup a CU reads them
-// fastest (17 x 2048 x 8192 bf16, us: gate and up 256 workgroups 12.8, 512 15.1; 61 x 4096 x 12288 gate and up 192
-// tiles of 64 x 128 42.5, 384 of 64 x 64 47.2; down 64 tiles in 4 splits 25.2, in 8 27.3, whole 61.2).
+// many at once as it holds; splits add the sums' way through memory.
 Shape shape_of(Kind kind, int M, int N, int K, int esize) {
-    const int ke = 128 / esize, all = (K + ke - 1) / ke, wide = esize == 4;
-    if (M <= 64 && (kind == GATE_UP || kind == DOWN)) {
-        const int small = (N + 63) / 64 * (kind == GATE_UP ? 2 : 1), c = M <= 32 ? THIN : small <= CUS ? SMALL : LOW;
-        int want = CUS / small;
-        if (want > all / 4) want = all / 4;
-        return shape(kind, c, c == THIN ? 32 : 64, c == LOW ? 128 : 64, M, N, all, want < 1 ? 1 : want);
-    }
+    const int ke = 128 / esize, all = (K + ke - 1) / ke, wide = esize == 4, pair = kind == GATE_UP ? 2 : 1;
+    const bool few = M <= 64 && (kind == GATE_UP || kind == DOWN);
     Shape best{};
     float least = 0.f;
-    for (int c = 0; c < THIN; c++) {
-        if (TILE[c].one[wide] == 0.f) continue;
-        for (int want = 1; want <= 16; want++) {
-            const Tile& t = TILE[c];
+    auto consider = [&](const Tile& t, int c) {
+        for (int want = 1; want <= (few ? 32 : 16); want++) {
             const Shape s = shape(kind, c, t.bm, t.bn, M, N, all, want);
             const int64_t tiles = (int64_t)s.tilesM * s.tilesN;
-            if (want > 1 && (all < 4 * want || tiles * (want - 1) >= 2 * CUS)) break;
+            if (want > 1 && (all < (few ? 2 : 4) * want || tiles * (want - 1) >= (few ? 4 : 2) * CUS)) break;
             if (want > 1 && s.splits != want) continue;
             const int64_t each = (tiles * s.splits + CUS - 1) / CUS, full = each / t.held, odd = each % t.held;
             float us = full * (s.steps * t.all[wide] + t.rest[wide]) + odd * (s.steps * t.one[wide] + t.rest[wide]);
-            if (s.splits > 1) us += JOIN + JOIN_SUM * s.splits * M * N * (kind == GATE_UP ? 2 : 1);
+            if (s.splits > 1) {
+                us += few ? FEW_JOIN[wide] + FEW_SPLIT[wide] * s.splits : JOIN;
+                us += (few ? FEW_SUM[wide] : JOIN_SUM) * s.splits * M * N * pair;
+            }
             if (best.tilesM == 0 || us < least) least = us, best = s;
         }
+    };
+    if (few) {
+        for (int i = 0; i < 3; i++)
+            if ((M <= 32) == (FEW_CONFIG[i] == THIN)) consider(FEW[i], FEW_CONFIG[i]);
+    } else {
+        for (int c = 0; c < THIN; c++)
+            if (TILE[c].one[wide] != 0.f) consider(TILE[c], c);
     }
     return best;
 }

@@ -146,6 +146,18 @@ def test_ffn_large(B, T, D, F, dtype, act):
     assert all(torch.equal(got[k], again[k]) for k in got)
 
 
+@pytest.mark.parametrize("T,D,F,dtype", [
+    (1, 64, 12288, "bf16"), (17, 8192, 64, "bf16"), (40, 8192, 96, "f16"), (64, 136, 12296, "bf16"), (60, 8200, 1000, "f32"),
+    (3, 4096, 5632, "f32"), (50, 4096, 5632, "f32"), (64, 1024, 2816, "bf16"), (32, 512, 1408, "f16")])
+def test_ffn_few_tokens(B, T, D, F, dtype):
+    """Many splits of either product, few, and none."""
+    d = {n: t.cuda() for n, t in inputs(T, D, F, dtype).items()}
+    ref, tol, norm = reference(**d, act="silu", dtype=dtype)
+    y = B.gated_ffn_fwd(d["x"], d["wg"], d["wu"], d["wd"])["y"]
+    close("y", y, ref["y"], tol["y"], norm)
+    assert torch.equal(run(B, d, "silu")["y"], y)
+
+
 def test_ffn_misaligned_odd_rows(B):
     """Odd widths may begin at any element."""
     for dtype in DT:
