@@ -70,8 +70,11 @@ int64_t saved_width(const Plan& l) { return 2 * (int64_t)l.F + (int64_t)l.F * l.
 size_t saved_bytes(const Plan& l) { return 4 * (size_t)l.T * saved_width(l); }
 char* saved_h(const Plan& l, const float* saved) { return (char*)saved + 8 * (size_t)l.T * l.F; }
 
-void add(PadArgs& a, const void* src, void* dst, int64_t rows, int64_t rows_dst, int cols, int cols_dst) {
+// Copies src into padded rows (and `rows_dst` of them) at dst, where it then is; not if its rows are as they have to be.
+void pad(PadArgs& a, const void*& src, void* dst, int64_t rows, int64_t rows_dst, int cols, int cols_dst) {
+    if (rows == rows_dst && cols == cols_dst && ((uintptr_t)src & 15) == 0) return;
     a.item[a.n++] = {src, dst, rows, rows_dst, cols, cols_dst};
+    src = dst;
 }
 
 }  // namespace
@@ -98,21 +101,20 @@ int gated_ffn_fwd(const ffn_problem* p, const void* x, const void* w_gate, const
     hipError_t e = hipSuccess;
     if (l.pad) {
         PadArgs c{};
-        add(c, x, b + l.x, l.T, l.T, p->D, l.D);
-        add(c, w_gate, b + l.wg, p->F, l.F, p->D, l.D);
-        add(c, w_up, b + l.wu, p->F, l.F, p->D, l.D);
-        add(c, w_down, b + l.wd, p->D, l.D, p->F, l.F);
+        pad(c, x, b + l.x, l.T, l.T, p->D, l.D);
+        pad(c, w_gate, b + l.wg, p->F, p->F, p->D, l.D);
+        pad(c, w_up, b + l.wu, p->F, p->F, p->D, l.D);
+        pad(c, w_down, b + l.wd, p->D, p->D, p->F, l.F);
         if ((e = launch_pad(l.e, c, stream)) != hipSuccess) return status(e);
-        x = b + l.x, w_gate = b + l.wg, w_up = b + l.wu, w_down = b + l.wd;
     }
     GemmArgs a{};
     a.act = p->act, a.part = (float*)(b + l.part);
     a.q = x, a.ldq = l.D, a.p0 = w_gate, a.p1 = w_up, a.ldp = l.D;
-    a.M = l.T, a.N = l.F, a.K = l.D;
+    a.M = l.T, a.N = l.F, a.K = l.D, a.rowsP = p->F;
     a.gu = saved, a.h = saved ? saved_h(l, saved) : b + l.h;
     if ((e = launch_gemm(p->dtype, GATE_UP, a, stream)) != hipSuccess) return status(e);
     a.q = a.h, a.ldq = l.F, a.p0 = w_down, a.p1 = nullptr, a.ldp = l.F;
-    a.N = l.D, a.K = l.F;
+    a.N = l.D, a.K = l.F, a.rowsP = p->D;
     a.out0 = y, a.ldo = p->D, a.osplit = INT_MAX, a.rows_out = l.T, a.cols_out = p->D;
     return status(launch_gemm(p->dtype, DOWN, a, stream));
 }
@@ -137,13 +139,12 @@ int gated_ffn_bwd(const ffn_problem* p, const void* x, const void* w_gate, const
     hipError_t e = hipSuccess;
     if (l.pad && l.T > 0) {
         PadArgs c{};
-        add(c, x, b + l.x, l.T, l.T, p->D, l.D);
-        add(c, dy, b + l.dy, l.T, l.T, p->D, l.D);
-        add(c, w_gate, b + l.wg, p->F, l.F, p->D, l.D);
-        add(c, w_up, b + l.wu, p->F, l.F, p->D, l.D);
-        add(c, w_down, b + l.wd, p->D, l.D, p->F, l.F);
+        pad(c, x, b + l.x, l.T, l.T, p->D, l.D);
+        pad(c, dy, b + l.dy, l.T, l.T, p->D, l.D);
+        pad(c, w_gate, b + l.wg, p->F, l.F, p->D, l.D);
+        pad(c, w_up, b + l.wu, p->F, l.F, p->D, l.D);
+        pad(c, w_down, b + l.wd, p->D, l.D, p->F, l.F);
         if ((e = launch_pad(l.e, c, stream)) != hipSuccess) return status(e);
-        x = b + l.x, dy = b + l.dy, w_gate = b + l.wg, w_up = b + l.wu, w_down = b + l.wd;
     }
     GemmArgs a{};
     a.act = p->act, a.part = (float*)(b + l.part), a.dgu = b + l.dgu, a.gu = (float*)saved;

@@ -240,6 +240,9 @@ __device__ __forceinline__ void wave_sync() {
 template <class E, int KIND, int ACT>
 __device__ __forceinline__ void finish(const GemmArgs& a, int m, int n, f32x4 v, f32x4 w, const Kept& kept) {
     if constexpr (KIND == GATE_UP) {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (n + e >= a.rowsP) v[e] = w[e] = 0.f;
         if (a.gu) {   // kept in fp32: rounded to the type they would add as much error to the gradients as the operands do
             float* row = a.gu + (int64_t)m * 2 * a.N + n;
             *(f32x4*)row = v, *(f32x4*)(row + a.N) = w;
@@ -307,7 +310,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int block, char* sm
     Q q;
     P p;
     q.init(m0, a.M, a.ldq, wave, lane);
-    p.init(n0, a.N, a.ldp, wave, lane);
+    p.init(n0, PT ? a.N : a.rowsP, a.ldp, wave, lane);
     const char* qb = (const char*)a.q + (QT ? 0 : (int64_t)m0 * a.ldq * (int64_t)sizeof(E));
     const char* pb0 = (const char*)a.p0 + (PT ? 0 : (int64_t)n0 * a.ldp * (int64_t)sizeof(E));
     const char* pb1 = a.p1 ? (const char*)a.p1 + (PT ? 0 : (int64_t)n0 * a.ldp * (int64_t)sizeof(E)) : nullptr;

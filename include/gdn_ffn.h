@@ -17,7 +17,7 @@
  * aligned, one call at a time; no output on an input or another output; equal
  * inputs give equal bits).  Where D and F are multiples of 8 (of 4 for fp32), x, dy
  * and the weights must be 16-byte aligned; otherwise to their element, and the call
- * copies them into rows of such a length first.
+ * first copies those that are not, or whose rows are not, into rows of such a length.
  */
 #ifndef GDN_FFN_H_
 #define GDN_FFN_H_

@@ -168,6 +168,22 @@ def test_ffn_misaligned_odd_rows(B):
         assert all(torch.equal(got[k], want[k]) for k in want)
 
 
+@pytest.mark.parametrize("D,F", [(64, 45), (21, 64), (64, 1), (1, 64)])
+@pytest.mark.parametrize("dtype", DT)
+def test_ffn_one_width_odd(B, D, F, dtype):
+    """Only rows that need it are copied: the others are read where they lie, with NaN behind the last, or from any element."""
+    T = 37
+    d = inputs(T, D, F, dtype)
+    ref, tol, norm = reference(**d, act="gelu", dtype=dtype)
+    for shift in (0, 1):
+        big = {n: torch.full((t.numel() + 4096,), float("nan"), dtype=t.dtype, device="cuda") for n, t in d.items()}
+        at = {n: big[n][shift:shift + t.numel()].view(t.shape).copy_(t) for n, t in d.items()}
+        got = run(B, at, "gelu")
+        for k, v in got.items():
+            close(k, v, ref[k], tol[k], norm)
+        assert torch.equal(B.gated_ffn_fwd(at["x"], at["wg"], at["wu"], at["wd"], act="gelu")["y"], got["y"])
+
+
 @pytest.mark.parametrize("T,D,F,dtype", [(70, 72, 136, "bf16"), (37, 21, 45, "f16"), (300, 64, 200, "f32")])
 def test_ffn_spoilt_tokens(B, T, D, F, dtype):
     """A token with an infinity and one with a NaN: the other tokens' rows keep their bits (no sum
