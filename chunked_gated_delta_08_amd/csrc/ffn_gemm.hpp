@@ -492,25 +492,30 @@ template <class E, int BM, int BN, int WM, int WN, int NST> __global__ FFN_BOUND
     else gemm_tile<E, DW, BM, BN, WM, WN, NST>(a, block, smem);
 }
 
-// The splits' sums in their order, and what becomes of them: four columns a lane.
+// The splits' sums in their order, and what becomes of them: four columns a lane, eight splits on their way at a time,
+// workgroups of one wave, since a token's sums are few (8 splits of 1 x 2048 with all of its forward, us: 23.4 with four
+// at a time in workgroups of 256, 22.4 so; 20 x 1024 x 8192 18.1 and 16.3).
+constexpr int JOIN_THREADS = 64;
 template <class E, int KIND> __device__ __forceinline__ void join_splits(const GemmArgs& a) {
     constexpr int STEP = KIND == GATE_UP ? 2 : 1;
     const int quads = a.N / 4;
     const int64_t total = (int64_t)a.M * quads, plane = (int64_t)a.M * STEP * a.N;
-    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
-        const int m = (int)(id / quads), n = 4 * (int)(id % quads);
+    for (int64_t id = (int64_t)blockIdx.x * JOIN_THREADS + threadIdx.x; id < total; id += (int64_t)gridDim.x * JOIN_THREADS) {
+        const int m = total >> 32 ? (int)(id / quads) : (int)((uint32_t)id / (uint32_t)quads), n = 4 * (int)(id - (int64_t)m * quads);
         const float* p = a.part + (int64_t)m * STEP * a.N + n;
         f32x4 v = *(const f32x4*)p, w = *(const f32x4*)(p + (STEP - 1) * a.N);
-        for (int s = 1; s < a.splits; s += 4) {   // four on their way at a time
-            f32x4 x[4], y[4];
+        constexpr int AT = 8;
+        for (int s = 1; s < a.splits; s += AT) {
+            f32x4 x[AT], y[AT];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float* at = p + (s + i < a.splits ? s + i : 0) * plane;
+            for (int i = 0; i < AT; i++) {
+                if (s + i >= a.splits) break;
+                const float* at = p + (s + i) * plane;
                 x[i] = *(const f32x4*)at;
                 if constexpr (STEP == 2) y[i] = *(const f32x4*)(at + a.N);
             }
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < AT; i++) {
                 if (s + i >= a.splits) break;
                 v += x[i];
                 if constexpr (STEP == 2) w += y[i];
@@ -524,8 +529,8 @@ template <class E, int KIND> __device__ __forceinline__ void join_splits(const G
     }
 }
 
-template <class E, int KIND> __global__ __launch_bounds__(256) void ffn_join_kernel(GemmArgs a) { join_splits<E, KIND>(a); }
-template <class E> __global__ __launch_bounds__(256) void ffn_join_grads_kernel(GradArgs p) {   // dx and dw end alike
+template <class E, int KIND> __global__ __launch_bounds__(JOIN_THREADS) void ffn_join_kernel(GemmArgs a) { join_splits<E, KIND>(a); }
+template <class E> __global__ __launch_bounds__(JOIN_THREADS) void ffn_join_grads_kernel(GradArgs p) {   // dx and dw end alike
     GemmArgs a = p.g[0];
     if (blockIdx.y == 1) a = p.g[1];
     if (blockIdx.y == 2) a = p.g[2];
@@ -533,22 +538,22 @@ template <class E> __global__ __launch_bounds__(256) void ffn_join_grads_kernel(
 }
 
 inline unsigned join_blocks(const GemmArgs& a) {
-    const int64_t n = ((int64_t)a.M * (a.N / 4) + 255) / 256;
-    return (unsigned)(n < 4096 ? n : 4096);
+    const int64_t n = ((int64_t)a.M * (a.N / 4) + JOIN_THREADS - 1) / JOIN_THREADS;
+    return (unsigned)(n < 16384 ? n : 16384);
 }
 template <class E, int BM, int BN, int WM, int WN, int NST> hipError_t run_grads_shape(const GradArgs& p, hipStream_t s) {
     hipLaunchKernelGGL((ffn_grads_kernel<E, BM, BN, WM, WN, NST>), dim3((unsigned)p.start[3]), dim3(64 * WM * WN), 0, s, p);
     unsigned most = 0;
     for (const GemmArgs& a : p.g)
         if (a.splits > 1 && join_blocks(a) > most) most = join_blocks(a);
-    if (most) hipLaunchKernelGGL(ffn_join_grads_kernel<E>, dim3(most, 3), dim3(256), 0, s, p);
+    if (most) hipLaunchKernelGGL(ffn_join_grads_kernel<E>, dim3(most, 3), dim3(JOIN_THREADS), 0, s, p);
     return hipGetLastError();
 }
 template <class E, int KIND, int BM, int BN, int WM, int WN, int NST>
 hipError_t run_shape(const GemmArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((ffn_gemm_kernel<E, KIND, BM, BN, WM, WN, NST>), dim3((unsigned)(a.tilesM * a.tilesN * a.splits)),
                        dim3(64 * WM * WN), 0, s, a);
-    if (a.splits > 1) hipLaunchKernelGGL((ffn_join_kernel<E, KIND>), dim3(join_blocks(a)), dim3(256), 0, s, a);
+    if (a.splits > 1) hipLaunchKernelGGL((ffn_join_kernel<E, KIND>), dim3(join_blocks(a)), dim3(JOIN_THREADS), 0, s, a);
     return hipGetLastError();
 }
 
