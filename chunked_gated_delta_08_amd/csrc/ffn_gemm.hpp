@@ -193,8 +193,9 @@ template <int ACT> __device__ __forceinline__ float act_f(float x) {
     return ACT == GDN_FFN_SILU ? x * s : s;
 }
 // act(x) and its slope.  With e = exp(-x), s = sigmoid(x) = 1 / (1 + e) and 1 - s = e s,
-// which keeps its digits where s is close to 1; e stays finite (a comparison: the minimum of a NaN and a
-// number is the number, and a NaN gate has to stay one).
+// which keeps its digits where s is close to 1.  Where e is beyond 2^126, and may be infinite, s is zero as in the
+// forward (held above zero, x s would grow again for gates far below zero) and 1 - s is 1; comparisons, so that a NaN
+// stays one.
 template <int ACT> __device__ __forceinline__ void act_slope(float x, float& a, float& d) {
     if constexpr (ACT == GDN_FFN_GELU) {
         float e;
@@ -202,7 +203,7 @@ template <int ACT> __device__ __forceinline__ void act_slope(float x, float& a, 
         a = x * phi;
         d = phi + x * 0.39894228f * e;
     } else {
-        const float e0 = layer::exp_neg(x), e = e0 > 0x1p126f ? 0x1p126f : e0, s = __builtin_amdgcn_rcpf(1.f + e), t = e * s;
+        const float e = layer::exp_neg(x), s = e > 0x1p126f ? 0.f : __builtin_amdgcn_rcpf(1.f + e), t = e > 0x1p126f ? 1.f : e * s;
         a = ACT == GDN_FFN_SILU ? x * s : s;
         d = ACT == GDN_FFN_SILU ? s * (1.f + x * t) : s * t;
     }

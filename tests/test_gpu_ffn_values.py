@@ -53,3 +53,50 @@ def test_ffn_nan_gate(B, T, D, F, dtype, act):
         assert torch.isnan(got[k][f]).all(), k
         assert torch.equal(got[k][rest], want[k][rest]), k
     assert torch.isnan(got["dw_down"][:, f]).all() and torch.equal(got["dw_down"][:, rest], want["dw_down"][:, rest])
+
+
+GATES = (0.0, 0.5, 1.3, 5.0, 20.0, 60.0, 87.0, 90.0, 104.0, 130.0, 1000.0, 60000.0, 1e20, 1e30, 1e38, 3.3e38)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("act", ACTS)
+def test_ffn_far_gates(B, dtype, act):
+    """Gates to the ends of the type, on both sides.  One token of x = (1, 0, ..) and dy = (1, 0, ..), up and down weights of
+    one: g is the gate's weight, u = dh = 1, and the gradients of the weights are act'(g) and act(g) themselves.
+
+    Tolerances, u = 2^-24.  sigmoid and with it silu: (|g| + 40) 2 u of the terms s and |g| s (the exponent's rounding and one
+    unit each for exp2, rcp and the sum, twice).  gelu: exp(-g^2 / 2) is off by (1.5 g^2 + 16) u of itself, the polynomial's
+    error included, Phi above zero by 5 u more.  Values below 104 2^-126 may be zero: |g| s where s < 2^-126.  One rounding to the
+    type for each of the two that a value meets."""
+    t = DT[dtype]
+    g = torch.tensor([s * v for v in GATES for s in (1, -1) if v < torch.finfo(t).max]).to(t)
+    F, D, U = g.numel(), 8, 2.0 ** -24
+    one = torch.zeros(1, D, dtype=t)
+    one[0, 0] = 1
+    wg, wu, wd = torch.zeros(F, D, dtype=t), torch.zeros(F, D, dtype=t), torch.zeros(D, F, dtype=t)
+    wg[:, 0], wu[:, 0], wd[0] = g, 1, 1
+    got = run(B, {k: v.cuda() for k, v in dict(x=one, wg=wg, wu=wu, wd=wd, dy=one).items()}, act)
+    x = g.double()
+    if act == "gelu":
+        tail, pdf = 0.5 * torch.erfc(x.abs() / 2 ** 0.5), torch.exp(-x * x / 2) / math.sqrt(2 * math.pi)
+        phi = torch.where(x > 0, 1 - tail, tail)
+        e = (1.5 * x * x + 16) * U
+        a, slope = x * phi, phi + x * pdf
+        ea = x.abs() * (torch.nan_to_num(e * tail) + 5 * U * (x > 0))
+        es = torch.nan_to_num(e * (tail + x.abs() * pdf)) + 5 * U * (x > 0) + 2 * U
+    else:
+        s = torch.sigmoid(x)
+        m, e = s * torch.sigmoid(-x), (x.abs() + 40) * 2 * U   # s (1 - s)
+        a, slope = (x * s, s + x * m) if act == "silu" else (s, m)
+        # of s itself the share that its exponent has, times 1 - s, and the rest
+        es0 = e * m + 8 * U * s
+        ea = es0 * (x.abs() if act == "silu" else 1)
+        es = e * (s + x.abs() * m) if act == "silu" else e * m
+    half, tiny = torch.finfo(t).eps / 2, 104 * 2.0 ** -126 + torch.finfo(t).smallest_normal * torch.finfo(t).eps
+    for k, ref, err in (("dw_up", a, ea), ("dw_gate", slope, es)):
+        v = got[k][:, 0].double().cpu()
+        tol = err + 2 * half * (ref.abs() + err) + tiny
+        bad = ~((v - ref).abs() <= tol)
+        assert not bad.any(), (k, [(float(p), float(q), float(r), float(w)) for p, q, r, w in zip(x[bad], v[bad], ref[bad], tol[bad])])
+    h = got["dw_down"][0].double().cpu()   # the forward's own act(g) u
+    assert ((h - a).abs() <= ea + 2 * half * (a.abs() + ea) + tiny).all()
