@@ -149,7 +149,7 @@ int gated_ffn_bwd(const ffn_problem* p, const void* x, const void* w_gate, const
     GemmArgs a{};
     a.act = p->act, a.part = (float*)(b + l.part), a.dgu = b + l.dgu, a.gu = (float*)saved;
     a.q = dy, a.ldq = l.D, a.p0 = w_down, a.ldp = l.F;
-    a.M = l.T, a.N = l.F, a.K = l.D;
+    a.M = l.T, a.N = l.F, a.K = l.D, a.rowsP = p->F;
     if ((e = launch_gemm(p->dtype, DH, a, stream)) != hipSuccess) return status(e);
     GemmArgs g[3];   // dx, dw of gate and up, dw of down
     for (GemmArgs& x : g) x = a, x.osplit = INT_MAX, x.p1 = nullptr;

@@ -257,6 +257,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int m, int n, f32x4 v,
         f32x4 dg, du;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
+            if (n + e >= a.rowsP) v[e] = 0.f;   // a padded column's sum has an infinite dy times zero
             float act, slope;
             act_slope<ACT>(kept.g[e], act, slope);
             dg[e] = v[e] * kept.u[e] * slope;

@@ -14,7 +14,7 @@ struct GemmArgs {
     const void* p0; const void* p1; int64_t ldp;    // P stored [n][k], or [k][n]; the second matrix of a pair
     int psplit;                                     // P stored [k][n]: rows from psplit on are p1's
     int M, N, K;                                    // N of one matrix of a pair
-    int rowsP;                                      // P stored [n][k]: rows of a matrix that exist, up to 7 fewer than N
+    int rowsP;                                      // gate and up, down, dh: columns n that exist, up to 7 fewer than N
     int tilesM, tilesN, splits, steps;              // steps: k-steps of a split
     float* part;                                    // splits > 1: sums of each split, [split][M][width of a row]
     // epilogue

@@ -100,3 +100,24 @@ def test_ffn_far_gates(B, dtype, act):
         assert not bad.any(), (k, [(float(p), float(q), float(r), float(w)) for p, q, r, w in zip(x[bad], v[bad], ref[bad], tol[bad])])
     h = got["dw_down"][0].double().cpu()   # the forward's own act(g) u
     assert ((h - a).abs() <= ea + 2 * half * (a.abs() + ea) + tiny).all()
+
+
+@pytest.mark.parametrize("T,D,F", [(2, 8, 8), (2, 8, 5), (3, 7, 13), (40, 64, 45), (3, 4096, 61)])
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("act", ACTS)
+def test_ffn_infinite_dy(B, T, D, F, dtype, act):
+    """All operands above zero and one infinite dy: every sum it enters is infinite, none is NaN, also where F is padded to
+    whole pieces."""
+    d = inputs(T, D, F, dtype, positive=True)
+    want = run(B, d, act)
+    d["dy"][1, D // 2] = float("inf")
+    got = run(B, d, act)
+    assert torch.equal(got["y"], want["y"])
+    assert (got["dx"][1] == float("inf")).all()
+    rest = [i for i in range(T) if i != 1]
+    assert torch.equal(got["dx"][rest], want["dx"][rest])
+    for k in ("dw_gate", "dw_up"):
+        assert (got[k] == float("inf")).all(), k
+    assert (got["dw_down"][D // 2] == float("inf")).all()
+    rest = [i for i in range(D) if i != D // 2]
+    assert torch.equal(got["dw_down"][rest], want["dw_down"][rest])
