@@ -66,12 +66,14 @@ template <class E, int NC> __device__ __forceinline__ int swz(int k) {
     return x & (NC - 1);
 }
 
-// 16 bytes of each lane from base + off to LDS at lds + 16 lane.  (m0 holds nothing else here: the
-// compiler sets it anew wherever it uses it, and keeps no value in it.)
+// 16 bytes of each lane from base + off to LDS at lds + 16 lane, the place in m0.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // m0 is named as overwritten so that no value of the compiler's is kept in it
 __device__ __forceinline__ void load_to_lds(uint32_t lds, const char* base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory");
+                 :: "s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
 
 // One operand of a tile.  ROWS: BM or BN.  PAIR: rows of two matrices in turn, 16 of each.
