@@ -27,7 +27,7 @@ HIP_SOURCES = ["gdr_prep.hip", "gdr_scan.hip", "gdr_grad.hip", "kda_bwd.hip", "g
 SOURCE_FLAGS = {"gdr_prep.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
                 "gdr_scan.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
                 "kda_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
-HOST_SOURCES = ["gdr_api.cpp", "bigdn_api.cpp", "layer_api.cpp", "ffn_api.cpp"]
+HOST_SOURCES = ["gdr_api.cpp", "bigdn_api.cpp", "layer_api.cpp", "ffn_api.cpp", "ffn_plan.cpp"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
 DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

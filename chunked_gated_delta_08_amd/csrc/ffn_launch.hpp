@@ -1,9 +1,11 @@
-// ffn_launch.hpp -- host-side plan and launchers of the gated feed-forward block
+// ffn_launch.hpp -- host-side launchers of the gated feed-forward block
 // (include/gdn_ffn.h; internal).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
+
+#include "ffn_plan.hpp"
 
 namespace ffn {
 
@@ -32,8 +34,6 @@ struct GradArgs {
     int start[4];
 };
 
-enum Kind { GATE_UP, DOWN, DH, DX, DW };            // which product: orientations and epilogue
-
 // A tensor to copy into rows of another length: dst[r][c] = src[r][c] where that exists, else zero.
 struct PadItem {
     const void* src; void* dst;
@@ -45,24 +45,8 @@ struct PadArgs {
     int n;
 };
 
-// Tile shape and number of splits along k of a product.
-enum Config { BIG, WIDE, MIDDLE, DEEP, LOW, SMALL, THIN, TILES };
-struct Shape {
-    int cfg, splits, steps, tilesM, tilesN;
-};
-Shape shape_of(Kind kind, int M, int N, int K, int esize);
-size_t part_floats(Kind kind, int M, int N, int K, int esize);
-
 hipError_t launch_gemm(int dtype, Kind kind, GemmArgs a, hipStream_t s);
 
-// The gradients' products: 0 dx, 1 dw of gate and up, 2 dw of down, in one launch and in this order.
-struct GradPlan {
-    int cfg;
-    Shape s[3];
-    int order[3];
-};
-GradPlan grad_plan(int T, int D, int F, int esize);
-size_t grad_floats(const GradPlan& p, int T, int D, int F);
 hipError_t launch_grads(int dtype, const GradPlan& p, const GemmArgs (&g)[3], const bool (&want)[3], float* part,
                         hipStream_t s);
 hipError_t launch_pad(int esize, const PadArgs& a, hipStream_t s);

@@ -71,7 +71,7 @@ for _k in ("add_norm_fwd_kernel", "add_norm_bwd_kernel"):
     KERNEL_SOURCES[_k].insert(1, _CS + "layer_dropout.hpp")
 KERNEL_SOURCES["dropout_kernel"] = [_CS + "layer_dropout.hip", _CS + "layer_dropout.hpp"] + _ROWS
 for _k in ("ffn_gemm_kernel", "ffn_grads_kernel", "ffn_join_kernel", "ffn_join_grads_kernel", "ffn_pad_kernel"):
-    KERNEL_SOURCES[_k] = [_CS + "ffn_gemm.hpp", _CS + "ffn.hip", _CS + "ffn_launch.hpp"] + _ROWS
+    KERNEL_SOURCES[_k] = [_CS + f for f in ("ffn_gemm.hpp", "ffn.hip", "ffn_launch.hpp", "ffn_plan.cpp", "ffn_plan.hpp")] + _ROWS
 
 
 def _code_of(text):
