@@ -123,34 +123,48 @@ constexpr Tile GRAD_TILE[] = {
     {64, 64, 2, {0.f, 0.534f}, {0.f, 1.0f}, {0.f, 1.2f}},
 };
 constexpr int GRAD_CONFIG[] = {BIG, WIDE, MIDDLE, SMALL};
+// The weights' gradients sum over the tokens, up to 2^24 of them.  Steps that a split adds up at most, for 16-bit types and
+// fp32, 4096 matrix instructions of 32 and of 4 products: an fp32 sum of equal signs loses a unit in the last place
+// with each (2^24 equal tokens in fp32, in four splits of a million instructions: 5 % off; 131072 and 16384 tokens a split now).
+constexpr int LONGEST[] = {2048, 512};
+// The join's time for each split where they are more than the four that JOIN counts.  Backward by splits of these sums, us, bf16: 16384 x 64 x
+// 64 4 47.0, 8 27.6, 16 20.4, 32 17.9, 64 18.8, 128 25.6; 16384 x 128 x 256 57.9, 38.4, 31.1, 32.3, 35.0, 46.0;
+// 65536 x 256 x 512 331, 229, 201, 206, 243, 279; 65536 x 1024 x 2816 2328, 2351, 2423, 2555, 2904, 3658.
+constexpr float JOIN_SPLIT = 0.25f;
 }  // namespace
 
 GradPlan grad_plan(int T, int D, int F, int esize) {
     const int ke = 128 / esize, wide = esize == 4;
     const int M[3] = {T, 2 * F, D}, N[3] = {D, D, F}, K[3] = {2 * F, T, T};
-    static const int by_dx[3] = {0, 1, 2}, by_dw[3] = {1, 2, 0}, dx_splits[] = {1, 2, 3, 4, 6, 8}, dw_splits[] = {1, 2, 4};
+    static const int by_dx[3] = {0, 1, 2}, by_dw[3] = {1, 2, 0}, dx_splits[] = {1, 2, 3, 4, 6, 8};
+    int first = 1;   // splits of the sums over the tokens: powers of two from here on
+    while ((T + ke - 1) / ke > first * LONGEST[wide]) first *= 2;
     const int* order = 2 * F >= T ? by_dx : by_dw;   // the longest sums first
     GradPlan best{};
     float least = -1.f;
     for (int c = 0; c < 4; c++) {
         const Tile& t = GRAD_TILE[c];
         if (t.one[wide] == 0.f) continue;
-        for (int sx : dx_splits)
-            for (int sw : dw_splits) {
+        auto fits = [&](int j, int want) {   // splits while there is work for them and room
+            const Shape x = shape(DX, c, t.bm, t.bn, M[j], N[j], (K[j] + ke - 1) / ke, want);
+            return (K[j] + ke - 1) / ke >= 4 * want && (int64_t)x.tilesM * x.tilesN * (want - 1) < 2 * CUS;
+        };
+        for (int sx : dx_splits) {
+            if (sx > 1 && !fits(0, sx)) break;
+            for (int sw = first; sw == first || (fits(1, sw) && fits(2, sw)); sw *= 2) {
                 GradPlan p{GRAD_CONFIG[c], {}, {order[0], order[1], order[2]}};
-                float us = 0.f;
-                bool ok = true, joined = false;
-                for (int i = 0; i < 3 && ok; i++) {
-                    const int j = order[i], all = (K[j] + ke - 1) / ke, want = j == 0 ? sx : sw;
-                    const Shape x = shape(DX, c, t.bm, t.bn, M[j], N[j], all, want);
-                    ok = want == 1 || (all >= 4 * want && (int64_t)x.tilesM * x.tilesN * (want - 1) < 2 * CUS);
+                float us = sw > 4 ? JOIN_SPLIT * sw : 0.f;
+                bool joined = false;
+                for (int i = 0; i < 3; i++) {
+                    const int j = order[i];
+                    const Shape x = shape(DX, c, t.bm, t.bn, M[j], N[j], (K[j] + ke - 1) / ke, j == 0 ? sx : sw);
                     if (x.splits > 1) joined = true, us += JOIN_SUM * x.splits * M[j] * N[j];
                     p.s[i] = x;
                 }
-                if (!ok) continue;
                 us += makespan(p.s, t, wide) + (joined ? JOIN : 0.f);
                 if (least < 0.f || us < least) least = us, best = p;
             }
+        }
     }
     return best;
 }

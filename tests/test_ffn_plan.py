@@ -63,3 +63,13 @@ def test_instances_are_tested(plans, esize):
     tested = set().union(*(taken(s) for s in SIZES[esize]))
     for s in sizes(10 + esize, 30000):
         assert taken(s) <= tested, (s, taken(s) - tested)
+
+
+@pytest.mark.parametrize("esize", [2, 4])
+def test_sums_over_tokens_are_short(plans, esize):
+    """A split of a weight's gradient adds up 4096 matrix instructions at most, of 32 products or (fp32) of 4."""
+    long = [(1 << 24, D, F) for D, F in ((4, 4), (64, 64), (1024, 1024), (8, 2000), (4000, 8))]
+    for s in [*sizes(20 + esize, 5000), *long]:
+        for name, _, splits, steps, _ in plans(*s, esize):
+            if name.startswith("dw"):
+                assert steps * (128 // esize) <= (4096 * 32 if esize == 2 else 4096 * 4), (s, name, splits, steps)
