@@ -175,7 +175,9 @@ template <class E, int ROWS, int NW, bool TRANS, bool PAIR> struct Operand {
 // gelu: x Phi(x), Phi(x) = erfc(-x / sqrt 2) / 2.  For z = |x| / sqrt 2, erfc(z) = exp(-z^2) t Q(t) with
 // t = 1 / (1 + z / 2) and a polynomial Q, fitted by least squares on Chebyshev points, weighted towards the
 // largest error: 8e-8 of the value at most for z < 9.5, past which exp(-z^2) is zero.  The exponential is the one
-// that the slope takes; Phi is off by 3 2^-24 at most.
+// that the slope takes.  In units of 2^-24, with one in the last place (2) each for rcp and exp2: t is off by 3 of itself near
+// zero, where t Q(t) takes that 2.3 fold, the polynomial's nine roundings by 2.9, so that Phi is off by 8 at most; below zero
+// by 16 + 1.2 x^2 of itself, the second term from the exponent's roundings.
 __device__ __forceinline__ float gauss(float x, float& e) {   // Phi(x), exp(-x^2 / 2)
     constexpr float Q[9] = {-0.0588914342f, 0.283705056f, -0.485389888f, 0.275984913f, -0.0251820963f, 0.202071592f, 0.243260592f, 0.28235355f, 0.282087684f};
     const float t = __builtin_amdgcn_rcpf(1.f + fabsf(x) * 0.35355338f);

@@ -121,3 +121,22 @@ def test_ffn_infinite_dy(B, T, D, F, dtype, act):
     assert (got["dw_down"][D // 2] == float("inf")).all()
     rest = [i for i in range(D) if i != D // 2]
     assert torch.equal(got["dw_down"][rest], want["dw_down"][rest])
+
+
+def test_ffn_gelu_error(B):
+    """gelu over its range: Phi is off by 8 u at most, and below zero by (16 + 1.2 g^2) u of itself, as derived at the function;
+    the product with g and the rounding to fp32 add u of the value."""
+    U, D = 2.0 ** -24, 4
+    for lo, hi in ((-13.0, 13.0), (-1.0, 1.0), (-1e-3, 1e-3)):
+        g = torch.linspace(lo, hi, 65536)
+        F = g.numel()
+        one = torch.zeros(1, D)
+        one[0, 0] = 1
+        wg, wu, wd = torch.zeros(F, D), torch.zeros(F, D), torch.zeros(D, F)
+        wg[:, 0], wu[:, 0], wd[0] = g, 1, 1
+        a = run(B, {k: v.cuda() for k, v in dict(x=one, wg=wg, wu=wu, wd=wd, dy=one).items()}, "gelu")["dw_up"][:, 0].double().cpu()
+        x = g.double()
+        phi = 0.5 * torch.erfc(-x / 2 ** 0.5)
+        tol = torch.where(x > 0, 8 * U, torch.minimum((16 + 1.2 * x * x) * phi, torch.tensor(8.0, dtype=torch.float64)) * U)
+        worst = ((a - x * phi).abs() / (x.abs() * tol + U * (x * phi).abs() + 2.0 ** -126)).max()
+        assert worst <= 1, (lo, float(worst))
