@@ -260,6 +260,7 @@ def gated_ffn(x, w_gate, w_up, w_down, act="silu"):
     x's dtype.  act is "silu", "gelu" (exact) or "sigmoid".
 
     Differentiable in x and the weights; the gradients are in x's dtype.  Between the passes it keeps
-    2F floats and F of the type a token, its gate and up rows and their product."""
+    2F floats and F of the type a token, its gate and up rows and their product.  That product and
+    the gradients of gate and up are held in the type: in fp16 they overflow beyond 65504."""
     t = [_on_16_bytes(v) for v in (x, w_gate, w_up, w_down)]
     return GatedFFN.apply(*t, act, torch.is_grad_enabled() and any(v.requires_grad for v in t))

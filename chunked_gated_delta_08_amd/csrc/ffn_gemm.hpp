@@ -18,13 +18,14 @@
 // lane permutes.
 //
 // Measured (bf16, 16384 tokens, D = 2048, F = 8192; kernel times): gate and up
-// 0.87 ms without and 1.00 with what the backward needs, down 0.42 (1300 TFLOP/s), dh
-// 0.72, the gradients' three products 2.2 (1250).  With zeros for operands the same code runs
+// 0.86 ms without and 1.00 with what the backward needs, down 0.42 (1300 TFLOP/s), dh
+// 0.69, the gradients' three products 2.15 (1280).  With zeros for operands the same code runs
 // 12 % faster: it is the chip's power, not the schedule, that bounds the large
 // products (the library's, k contiguous, 1240 to 1570 on the same operands, hot and
 // cool; 970 to 1030 with k strided).  gate and up and dh add what they
 // write and read, 1.3 and 1.6 GB, to their products' time.  Few tokens: the weights'
-// bytes, 5.2 TB/s (1 x 2048 x 8192: gate and up 12.8 us).
+// reads (1 x 2048 x 8192: gate and up 12.8 us with weights that the call before left in cache, 16.6 to
+// 18.2 with weights from memory, 3.7 TB/s).
 #pragma once
 #include "ffn_launch.hpp"
 #include "gdr_device.hpp"
@@ -300,9 +301,13 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int block, char* sm
 
     // Workgroups go to the chip's 8 parts in turn; each part takes a run of tiles, and within
     // it `rows` rows of tiles at a time, so that its L2 serves an operand's tile to several.  Rows of 256: three where
-    // their Q stays in the part's 4 MB (and an odd number, which spreads rows whose pitch is a power of two over
-    // the memory's channels), else four (16384 x 2048 x 8192 bf16, us: gate and up with 8, 4 and 3 rows 1128, 1094
-    // and 973, dh 717, 696 and 676; 8192 x 4096 x 12288: 1293, 1284, 1350 and 793, 796, 816).
+    // k is short and four beyond, a rule by measurement (an odd number spreads rows whose pitch is a power of two over
+    // the memory's channels; three rows of Q are 3 MB of the part's 4 at 4 KB of k).  bf16, a forward that
+    // keeps its gate and up rows, us, with 2, 3, 4, 6 and 8 rows: 16384 x 512 x 8192 634, 570, 664, 606, 745; 1024 879,
+    // 835, 917, 875, 981; 2048 1448, 1427, 1505, 1455, 1532; 2560 1870, 1813, 1873, 1881, 1906; 8192 x 4096 x 12288 1964, 1981,
+    // 1910, 1968, 1922; 8192 x 8192 x 4096 1322, 1271, 1244, 1260, 1239.  Backward with three and with four
+    // everywhere (dh goes by D; the gradients have 2 F and the tokens for k, which is four in large sizes): 16384 x 512 x 8192
+    // 1016, 1058; 1024 1602, 1618; 2048 2842, 2793; 2560 3861, 3864; 8192 x 4096 x 12288 4064, 3935.
     const int tiles = a.tilesM * a.tilesN, total = tiles * a.splits;
     const int xcd = block & 7, per = total >> 3, rem = total & 7;
     int id = xcd * per + (xcd < rem ? xcd : rem) + (block >> 3);

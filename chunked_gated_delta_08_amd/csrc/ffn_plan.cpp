@@ -10,8 +10,9 @@ namespace {
 // the CU, where as many as it holds share it (all of them), and of the rest of a tile, for 16-bit types and fp32
 // (0: not used, the smaller tiles are as fast; an fp32 step is bound by the matrix unit whatever the tile).
 // Fitted to 9036 (16-bit) and 8696 (fp32) timings of the products, 62 and 47 sizes from 100 to 16384 tokens,
-// every tile and number of splits: what the estimate picks takes 1.1 % (fp32 0.3 %) longer than the fastest, on average,
-// and at worst 30 % (9 %).
+// every tile and number of splits.  What the estimate picks, measured on 350 and 134 other sizes of 65 to 16384 tokens: a
+// forward takes 1.0 % longer than with the fastest tile and splits of gate and up, or of down, on average and 22 % at
+// worst, a backward 1.0 % and 23 % for dh.
 struct Tile {
     int bm, bn, held;
     float one[2], all[2], rest[2];
@@ -26,8 +27,9 @@ constexpr Tile TILE[] = {
 };
 constexpr float JOIN = 3.f, JOIN_SUM = 1.1e-6f;   // the launch that joins splits, and for each sum of a split
 // The same for up to 64 rows of a product with weights stored [n][k] (GATE_UP, DOWN), with the time that the join takes
-// for each split. From 2600 and 2700 timings of the products, 192 sizes each with 1 to 64 tokens: what is picked takes 0.3 %
-// longer than the fastest on average, at worst 11 % (splits wherever CUs were free took 6 %: whole forwards in a graph, us,
+// for each split. From 2600 and 2700 timings of the products, 192 sizes each with 1 to 64 tokens; measured on 1927 and 962 other
+// sizes: a forward takes 1.0 to 1.7 % longer than with the fastest choice for either product, at worst 16 % (splits wherever
+// CUs were free took 6 %: whole forwards in a graph, us,
 // 25 x 512 x 1408 bf16 11.6 and now 9.7, 64 x 1024 x 2816 17.3 and 14.1, 64 x 4096 x 5632 fp32 112 and 94).
 constexpr Tile FEW[] = {
     {32, 64, 2, {0.135f, 0.327f}, {0.241f, 0.62f}, {1.7f, 1.1f}},
@@ -86,7 +88,8 @@ size_t part_floats(Kind kind, int M, int N, int K, int esize) {
 
 namespace {
 // When the workgroups of the gradients' products are through, in us: they start in their order wherever a place is free,
-// those of a product take the same time.  The constants, as TILE's, from 17 sizes with each tile and number of splits.
+// those of a product take the same time.  The constants, as TILE's, from 17 sizes with each tile and number of splits; on the 350
+// and 134 sizes named there a backward takes 2.5 % (fp32 3.4 %) longer than with the fastest tile and splits, at worst 19 %.
 float makespan(const Shape (&s)[3], const Tile& t, int wide) {
     struct { float at; int64_t places; } level[8];
     int64_t total = 0;
@@ -127,9 +130,9 @@ constexpr int GRAD_CONFIG[] = {BIG, WIDE, MIDDLE, SMALL};
 // fp32, 4096 matrix instructions of 32 and of 4 products: an fp32 sum of equal signs loses a unit in the last place
 // with each (2^24 equal tokens in fp32, in four splits of a million instructions: 5 % off; 131072 and 16384 tokens a split now).
 constexpr int LONGEST[] = {2048, 512};
-// The join's time for each split where they are more than the four that JOIN counts.  Backward by splits of these sums, us, bf16: 16384 x 64 x
-// 64 4 47.0, 8 27.6, 16 20.4, 32 17.9, 64 18.8, 128 25.6; 16384 x 128 x 256 57.9, 38.4, 31.1, 32.3, 35.0, 46.0;
-// 65536 x 256 x 512 331, 229, 201, 206, 243, 279; 65536 x 1024 x 2816 2328, 2351, 2423, 2555, 2904, 3658.
+// The join's time for each split, where they are more than the four that JOIN counts.  Backward, us, with 4, 8, 16, 32, 64 and 128
+// splits of these sums, bf16: 16384 x 64 x 64 47.0, 27.6, 20.4, 17.9, 18.8, 25.6; 16384 x 128 x 256 57.9, 38.4, 31.1, 32.3,
+// 35.0, 46.0; 65536 x 256 x 512 331, 229, 201, 206, 243, 279; 65536 x 1024 x 2816 2328, 2351, 2423, 2555, 2904, 3658.
 constexpr float JOIN_SPLIT = 0.25f;
 }  // namespace
 

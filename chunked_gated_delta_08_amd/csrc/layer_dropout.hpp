@@ -5,7 +5,8 @@
 // numbers: as easy as 1, 2, 3", 2011), one call for 8 elements of a row, 16 bits
 // an element: half the integer work of 32 bits, which beside a pass bound by HBM
 // leaves the rate as it is, and steps of 2^-16 in the probability, which the
-// factor 1/(1-p) follows exactly.
+// factor 1/(1-p) follows exactly.  Where a lane holds four elements (the add norm with an fp32
+// residual) two lanes make the same call and take half of its bits each.
 #pragma once
 #include "layer_launch.hpp"
 #include "layer_rows.hpp"

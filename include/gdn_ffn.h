@@ -8,8 +8,9 @@
  *
  * Sums are fp32 whatever the type (products of 16-bit operands on the matrix
  * units, of fp32 ones in fp32).  g and u stay in fp32; h, dg and du are operands
- * of the next product and are rounded to the type first; each output is rounded
- * once.
+ * of the next product and are rounded to the type first (in fp16 they are infinite
+ * beyond 65504); each output is rounded once.  Sums over the tokens are formed in
+ * pieces of at most 131072 tokens (fp32: 16384) and joined in their order.
  *
  * Conventions: as in gdn_layer.h (caller-owned, contiguous, row-major device
  * pointers; asynchronous on `stream`, which must belong to the current device;
