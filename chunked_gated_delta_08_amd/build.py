@@ -10,26 +10,23 @@ import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
 
+if __package__:
+    from .build_flags import ARCH, DEVICE, OPTIMIZE, SOURCE_FLAGS
+else:   # run as a script
+    from build_flags import ARCH, DEVICE, OPTIMIZE, SOURCE_FLAGS
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libgdr.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-ARCH = "gfx950"
 
 HIP_SOURCES = ["gdr_prep.hip", "gdr_scan.hip", "gdr_grad.hip", "kda_bwd.hip", "gdr_fwd.hip", "kda_full.hip",
                "bigdn.hip", "gdr_noalloc.hip", "layer_gated_norm.hip", "layer_add_norm.hip", "layer_step.hip", "glr.hip", "layer_dropout.hip",
                "ffn.hip", "ffn_bf16.hip", "ffn_f16.hip", "ffn_f32.hip"]
-# per-source device flags: the WY-factor, scan and KDA kernels keep MFMA
-# accumulators in VGPRs; the gradient and forward-output kernels are left to
-# the compiler's register-class heuristics
-SOURCE_FLAGS = {"gdr_prep.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-                "gdr_scan.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-                "kda_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 HOST_SOURCES = ["gdr_api.cpp", "bigdn_api.cpp", "layer_api.cpp", "ffn_api.cpp", "ffn_plan.cpp"]
-COMMON = ["-O3", "-std=c++17", "-fPIC", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
-DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+COMMON = OPTIMIZE + ["-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
 
 
 def _run(cmd, verbose):

@@ -36,7 +36,7 @@ import sys
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 _CS = "chunked_gated_delta_08_amd/csrc/"
-_COMMON = [_CS + "gdr_device.hpp", _CS + "gdr_launch.hpp", "chunked_gated_delta_08_amd/build.py"]
+_COMMON = [_CS + "gdr_device.hpp", _CS + "gdr_launch.hpp", "chunked_gated_delta_08_amd/build_flags.py"]
 KERNEL_SOURCES = {
     "chunk_table_kernel": [_CS + "gdr_prep.hip"] + _COMMON,
     "prep_kernel": [_CS + "gdr_prep.hip", _CS + "gdr_tri.hpp"] + _COMMON,
