@@ -11,7 +11,9 @@
 // Bound by HBM, built like the gated norm (layer_gated_norm.hip).  Measured:
 // forward 32768 x 2048 bf16 92 us (5.8 TB/s of 537 MB), backward 16384 x 4096 fp16
 // 142 us and 7 for the join (5.4 TB/s of 805 MB), 5 x 2048 3 to 4 us, which is the
-// launch; with dropout forward 32768 x 2048 bf16 91 us, backward 16384 x 4096 fp16 155.
+// launch; with dropout forward 32768 x 2048 bf16 91 us, backward 16384 x 4096 fp16 155.  Larger
+// forwards fall off (131072 x 2048 bf16 439 us, with dropout 471, 4.9 and 4.6 TB/s; 262144 4.5 and 4.4), the
+// backward's fewer workgroups do not (380 us, 5.65; 5.35).
 // No value is spilled but in the backward with an fp32 residual and a scale beyond D = 4096
 // (three in fp32, seven with dropout, one with dropout and bf16 rows).
 #include "layer_dropout.hpp"
